@@ -370,6 +370,163 @@ int mk_debug_gemm_bf16(const void *A, const void *B, float *C, int M, int N, int
  * *n_records receives the count copied.  Waits for the device. */
 int mk_trace_copy(mk_plan *plan, void *host_buf, size_t bytes, size_t *n_records);
 
+/* ------------------------------------------------------------------ paged KV cache
+ * The plan's cache gives every sequence slot max_ctx contiguous positions.  The
+ * mk_paged_* operators work on a cache that is handed out in pages of
+ * page_size tokens, so that memory goes to the tokens that exist: one step of a
+ * serving loop is mk_paged_tables (which pages, which slots, which positions),
+ * then per layer mk_paged_append (norm and rotary positions of the new q and k,
+ * k and v into their pages) and mk_paged_attention (the new tokens over their
+ * sequence's pages; a decode step, a few drafted tokens and a chunk of a prompt
+ * are requests of one call).  They hold no state: everything is in the caller's
+ * buffers, all of it on the current device, and every call can be captured into
+ * a CUDA graph.  Calls are ordered by `stream` alone.
+ *
+ * A plan's own cache is such a cache as it lies: with max_ctx % page_size == 0,
+ * the pages of layer l are k = kv_cache + l's keys, page_stride = page_size *
+ * head_dim, head_stride = max_ctx * head_dim, token_stride = head_dim, and block
+ * j of slot s is page s * n_kv_heads * (max_ctx / page_size) + j. */
+
+enum { MK_BF16 = 0, MK_FP16 = 1 };
+
+/* Requests one call of the paged operators takes. */
+#define MK_PAGED_MAX_REQUESTS 4096
+/* Scratch of mk_paged_attention, whatever the call's sizes.  Nothing in it
+ * lives from one call to the next and it needs no initialisation; calls that
+ * may overlap (two streams, two graphs replayed at once) need one each. */
+#define MK_PAGED_WORKSPACE_BYTES (64u << 20)
+
+/* One layer's paged cache.  Token o of page p, kv head h: k (and v) + p *
+ * page_stride + h * head_stride + o * token_stride elements, head_dim
+ * contiguous elements.  Strides are multiples of 8 elements; k, v and workspace
+ * 16-byte aligned; head_dim 64 or 128; page_size 16, 32, 64, 128 or 256;
+ * n_pages * page_size < 2^31. */
+typedef struct {
+  void *k, *v;
+  void *workspace;  /* MK_PAGED_WORKSPACE_BYTES; mk_paged_attention only, else may be NULL */
+  int32_t *status;  /* device word or NULL: receives MK_ERR_BOUNDS when it held MK_OK and a
+                       page, slot, length or row was out of range; see each operator */
+  int64_t page_stride, head_stride, token_stride;
+  int n_q_heads, n_kv_heads, head_dim, page_size, n_pages;
+  int dtype; /* of q, k, v, the cache and the outputs: MK_BF16 or MK_FP16 */
+} mk_paged_cache;
+
+/* The tables of one step, device int32 arrays.  Request r's new tokens are the
+ * rows cu_new[r] .. cu_new[r + 1) of the step's q, k, v and outputs; with them it
+ * has kv_lens[r] tokens, and its token i lies in page block_table[r *
+ * max_blocks + i / page_size] at offset i % page_size. */
+typedef struct {
+  int32_t *block_table; /* [n][max_blocks]                                    */
+  int32_t *cu_new;      /* [n + 1], cu_new[0] = 0, non-decreasing             */
+  int32_t *kv_lens;     /* [n]                                                */
+  int32_t *positions;   /* [max_tokens], mk_paged_tables only                 */
+  int32_t *slots;       /* [max_tokens] page * page_size + offset, or -1      */
+  int n;                /* 1 .. MK_PAGED_MAX_REQUESTS                         */
+  int max_blocks;       /* n * max_blocks * page_size bounds: see the calls   */
+  int max_tokens;       /* rows of the step's buffers (rows past cu_new[n] are
+                           padding: they are read by nothing and left alone)  */
+  int max_new;          /* no request has more new tokens (attention only)    */
+  int page_size;
+} mk_paged_batch;
+
+/* Build a step's tables on the GPU from the requests' lengths.  Request r has
+ * ctx_lens[r] cached tokens, in the pages that block_table's first
+ * ceil(ctx_lens[r] / page_size) entries name, and receives new_lens[r] >= 0 new
+ * ones (0: it rests, or pads the batch).  Pages that these need are taken from
+ * the end of the free list free_pages[0 .. *n_free), in the order of the
+ * requests, and entered in block_table behind the held ones (its other entries
+ * are left alone); *n_left receives what remains.  free_pages is not written:
+ * pages are given back by writing them at free_pages[*n_left ..].
+ *   cu_new, kv_lens, positions, slots: written, as described above; rows past
+ *   cu_new[n]: positions 0, slots -1.
+ * A request that is refused keeps its rows but gets kv_lens = 0, no pages and
+ * slots -1, positions 0 (so that append leaves its rows out and attention
+ * answers zeros), and MK_ERR_BOUNDS is latched in *status:
+ *   - lengths negative or ctx + new > max_blocks * page_size (such a request
+ *     gets no rows either);
+ *   - its rows would pass max_tokens (rows up to max_tokens are kept);
+ *   - the free pages do not suffice for it and the requests before it (a later
+ *     one that needs no page is still served).
+ * Pages are taken as they are named; the operators that use a page check it (one
+ * that no cache can have gives the slot 2^31 - 1).  *n_free outside 0 .. free_capacity is latched and clamped.
+ * All pointers device; n_left must not be n_free.  n * max_blocks < 2^31 and
+ * max_blocks * page_size < 2^31. */
+int mk_paged_tables(const mk_paged_batch *batch, const int32_t *ctx_lens, const int32_t *new_lens,
+                    const int32_t *free_pages, int free_capacity, const int32_t *n_free,
+                    int32_t *n_left, int32_t *status, void *stream);
+
+/* Rotary positions, a host struct passed by pointer and read during the call.
+ * Pair i (0 <= i < rotary_dim / 2) is the elements i and i + rotary_dim / 2 of a
+ * head (the pairing of the plan's kernels) and is turned by positions[axis[i]]
+ * * turn[i] / 2^64 of a full circle: whole turns drop out of the 64-bit product,
+ * so that far positions lose nothing.  Elements past rotary_dim stay. */
+typedef struct {
+  int rotary_dim, n_axes;
+  uint64_t turn[64];
+  uint8_t axis[64];
+} mk_rope;
+
+/* Fill a mk_rope: rotary_dim a multiple of 16, 16 .. 128; inv_freq (host double
+ * [rotary_dim / 2], radians per position) or NULL for theta^(-2 i / rotary_dim);
+ * axis_of_pair (host [rotary_dim / 2], each < n_axes) or NULL for n_axes = 1;
+ * n_axes 1 .. 4 (text has one axis; images and video turn pairs by time, height
+ * and width, in sections or interleaved as axis_of_pair says).  Host only. */
+int mk_rope_init(mk_rope *rope, int rotary_dim, double theta, const double *inv_freq, int n_axes,
+                 const uint8_t *axis_of_pair);
+
+/* The new tokens' q, k and v: RMSNorm of each q and k head where a gain is given
+ * (x / sqrt(mean x^2 + eps) * gain, as the plan's qk_norm), rotary positions, q to
+ * q_out, k and v to their slots of the cache; sums and angles in fp32 or more,
+ * each output rounded once.
+ *   q [n_tokens][n_q_heads][head_dim], k, v [n_tokens][n_kv_heads][head_dim],
+ *     q_out as q: *_stride elements from token to token (multiples of 8; heads
+ *     lie end to end), so that q, k, v can be parts of one projection's rows.
+ *     q_out may be q itself and may otherwise overlap nothing.
+ *   q_norm, k_norm  device [head_dim], or NULL
+ *   rope            or NULL (no rotation; positions is then not read)
+ *   positions       device int32 [n_axes][...], pos_stride words from axis to axis
+ *   slots           device int32 [n_tokens]: page * page_size + offset.  A token of
+ *                   slot < 0 is left out (nothing of it is read or written).  One
+ *                   past the last page likewise, with MK_ERR_BOUNDS latched.  No two
+ *                   tokens of a call may share a slot.
+ * n_tokens >= 0 (0: nothing is launched). */
+int mk_paged_append(const mk_paged_cache *cache, const void *q, int64_t q_stride, const void *k,
+                    int64_t k_stride, const void *v, int64_t v_stride, void *q_out,
+                    int64_t q_out_stride, const void *q_norm, const void *k_norm, float eps,
+                    const mk_rope *rope, const int32_t *positions, int64_t pos_stride,
+                    const int32_t *slots, int n_tokens, void *stream);
+
+/* Attention of every request's new tokens over its pages.  Row i of request r is
+ * the token at position p = kv_lens[r] - (cu_new[r + 1] - cu_new[r]) + i; query
+ * head h reads kv head h / (n_q_heads / n_kv_heads); it sees the keys j <= p with
+ * j >= 0 and, for window > 0, j > p - window:
+ *   out = sum_j exp(scale q.k_j - lse) v_j,  lse = log sum_j exp(scale q.k_j)
+ * A row that sees no key (kv_lens[r] less than the new tokens) gives out = 0 and
+ * lse = -inf.  Sums and the softmax are fp32; the weights of a row enter the
+ * product with V relative to a running maximum, rounded to the cache's type.
+ * Keys that no row of the request sees (the tail of its last page, pages before
+ * the window) are not read into any sum, whatever they hold; table entries of
+ * pages that hold no such key are not looked at.  Within the keys a request
+ * reads, a non-finite v reaches all rows of its kv head that are computed with it.
+ *   q, out  [rows][n_q_heads][head_dim], q_stride / out_stride elements from row
+ *           to row (multiples of 8); they may not overlap
+ *   lse     float [rows][n_q_heads] or NULL
+ *   scale   0: 1 / sqrt(head_dim)
+ *   window  0: none
+ * n_q_heads a multiple of n_kv_heads, at most 64 query heads per kv head.
+ * batch->max_tokens = rows of q, out and lse; batch->max_new bounds the new
+ * tokens of a request; positions and slots are not read.  MK_ERR_BOUNDS is latched
+ * in cache->status, and nothing out of range is touched, where kv_lens[r] is
+ * negative (taken as 0) or passes max_blocks * page_size (the keys past it are
+ * taken as absent), a page is not
+ * one of the cache's (its keys and values count as zeros), or a request's rows
+ * are more than max_new, not ordered or past max_tokens (they are left as they
+ * were).  The result of a row depends on the batch only through the order in
+ * which partial sums of its keys are joined; equal calls give equal bits. */
+int mk_paged_attention(const mk_paged_cache *cache, const mk_paged_batch *batch, const void *q,
+                       int64_t q_stride, void *out, int64_t out_stride, float *lse, float scale,
+                       int window, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,3 +16,4 @@ from .model import (  # noqa: F401
     prefill,
     causal_gqa_attention,
 )
+from .paged import paged_tables, rope_rows, paged_attention  # noqa: F401

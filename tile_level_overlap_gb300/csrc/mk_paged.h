@@ -1,0 +1,44 @@
+// Launch parameters of the paged-cache operators (mk_paged_*.cu).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mk.h"
+
+namespace mk {
+
+struct PagedTablesParams {
+  const int32_t *ctx, *add, *free_pages, *n_free;
+  int32_t *table, *cu, *kv, *pos, *slot, *n_left, *status;
+  int n, max_blocks, max_tokens, free_cap, page_shift;
+};
+
+struct PagedAppendParams {
+  const uint16_t *q, *k, *v, *q_gain, *k_gain;
+  uint16_t *q_out, *kc, *vc;
+  const int32_t *pos, *slot;
+  int32_t* status;
+  int64_t q_stride, k_stride, v_stride, qo_stride, pos_stride;
+  int64_t page_stride, head_stride, token_stride;
+  int hq, hkv, n_tokens, n_slots, page_shift;
+  float eps;
+  mk_rope rope;  // rotary_dim 0: no rotation
+};
+
+struct PagedAttnParams {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const uint16_t *kc, *vc;
+  const int32_t *table, *cu, *kv;
+  int32_t* status;
+  int64_t q_stride, o_stride;
+  int64_t page_stride, head_stride, token_stride;
+  int n, max_blocks, rows, max_new, n_pages, page_shift;
+  int hkv, rep, window;  // window 0x7fffffff: none
+  float scale;
+};
+
+cudaError_t paged_attention_launch(const PagedAttnParams& p, int d, int dtype, cudaStream_t st);
+
+}  // namespace mk
