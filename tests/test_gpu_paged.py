@@ -319,6 +319,10 @@ ATT = [
     ([3000, 0, 130], [100, 513, 1], 4, 1, 128, 64, 333, "hp", "bf16"),
     ([0], [1500], 4, 1, 128, 16, 0, "hp", "bf16"),
     ([5000], [260], 4, 1, 64, 16, 0, "hp", "bf16"),
+    # many blocks per SM: the load rings go round
+    ([30000, 17, 21111, 25000], [1, 1, 1, 1], 16, 16, 128, 64, 0, "hp", "bf16"),
+    ([30000, 17, 21111, 25000], [4, 1, 3, 2], 32, 8, 64, 16, 0, "hp", "fp16"),
+    ([30000, 17, 21111], [4, 8, 3], 32, 8, 128, 16, 0, "ph", "bf16"),
 ]
 
 

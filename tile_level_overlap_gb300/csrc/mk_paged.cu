@@ -1,14 +1,10 @@
 // Paged KV cache: a step's tables from the requests' lengths, the new tokens'
 // norm, rotary positions and write to their pages, and the C entry points of
 // the paged operators (include/mk.h).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <cmath>
 #include <cstring>
 
-#include "mk_device.cuh"
-#include "mk_paged.h"
+#include "mk_paged_dev.cuh"
 
 namespace mk {
 namespace {
@@ -29,21 +25,6 @@ struct PtSmem {
   int wpage[PT_THREADS / 32];
   int taken;
 };
-
-// Largest r in [0, n) with a[r] <= x (a non-decreasing, a[0] <= x).
-__device__ __forceinline__ int find_le(const int* a, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
-__device__ __forceinline__ void latch_bounds(int32_t* status) {
-  if (status) atomicCAS(status, MK_OK, MK_ERR_BOUNDS);
-}
 
 __global__ void __launch_bounds__(PT_THREADS) paged_tables_kernel(const PagedTablesParams P) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -130,7 +111,7 @@ __global__ void __launch_bounds__(PT_THREADS) paged_tables_kernel(const PagedTab
     }
   }
   if (served_upto > 0) atomicMax(&S.taken, served_upto);
-  if (bad && blockIdx.x == 0) latch_bounds(P.status);
+  if (bad && blockIdx.x == 0) latch(P.status, MK_ERR_BOUNDS);
   __syncthreads();
   const int taken = S.taken;
   if (blockIdx.x == 0 && tid == 0) {
@@ -173,38 +154,6 @@ __global__ void __launch_bounds__(PT_THREADS) paged_tables_kernel(const PagedTab
 // other's pairs, so the rotation needs no exchange.
 constexpr int PA_THREADS = 256;
 
-template <bool BF>
-__device__ __forceinline__ float2 up2(uint32_t w) {
-  if constexpr (BF) return make_float2(bf_lo(w), bf_hi(w));
-  const __half2 h = *reinterpret_cast<const __half2*>(&w);
-  return __half22float2(h);
-}
-template <bool BF>
-__device__ __forceinline__ uint32_t down2(float a, float b) {
-  if constexpr (BF) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-template <bool BF>
-__device__ __forceinline__ void up8(const uint4 w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = up2<BF>(u[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-template <bool BF>
-__device__ __forceinline__ uint4 down8(const float (&x)[8]) {
-  return make_uint4(down2<BF>(x[0], x[1]), down2<BF>(x[2], x[3]), down2<BF>(x[4], x[5]),
-                    down2<BF>(x[6], x[7]));
-}
-
 template <int HD, bool BF>
 __global__ void __launch_bounds__(PA_THREADS) paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
   __shared__ float2 cs[HD / 2];  // cos, sin of the token's pairs
@@ -212,7 +161,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_append_kernel(const __grid_c
   const int slot = P.slot[t];
   if (slot < 0) return;
   if (slot >= P.n_slots) {
-    if (tid == 0) latch_bounds(P.status);
+    if (tid == 0) latch(P.status, MK_ERR_BOUNDS);
     return;
   }
   const int half = P.rope.rotary_dim / 2;
@@ -306,8 +255,12 @@ int check_cache(const mk_paged_cache* c) {
   if (!c || !c->k || !c->v || !al16(c->k) || !al16(c->v) || !al4(c->status)) return MK_ERR_INVALID_ARG;
   if (c->n_q_heads < 1 || c->n_kv_heads < 1 || c->n_pages < 1) return MK_ERR_INVALID_ARG;
   if (c->dtype != MK_BF16 && c->dtype != MK_FP16) return MK_ERR_INVALID_ARG;
-  if ((c->page_stride | c->head_stride | c->token_stride) & 7) return MK_ERR_INVALID_ARG;
-  if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < c->head_dim) return MK_ERR_INVALID_ARG;
+  // a stride from token to token, head to head, page to page; one that joins
+  // nothing (one head, one page) is not used
+  const int64_t strides[] = {c->token_stride, c->n_kv_heads > 1 ? c->head_stride : c->token_stride,
+                             c->n_pages > 1 ? c->page_stride : c->token_stride};
+  for (int64_t s : strides)
+    if ((s & 7) || s < c->head_dim || s >= (1ll << 38)) return MK_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return MK_ERR_UNSUPPORTED;
   if (log2_page(c->page_size) < 0) return MK_ERR_UNSUPPORTED;
   if ((int64_t)c->n_pages * c->page_size > 0x7fffffffll) return MK_ERR_UNSUPPORTED;
@@ -448,7 +401,14 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch*
   p.hkv = c->n_kv_heads; p.rep = c->n_q_heads / c->n_kv_heads;
   p.window = window ? window : 0x7fffffff;
   p.scale = scale != 0.f ? scale : 1.0f / sqrtf((float)c->head_dim);
-  return paged_attention_launch(p, c->head_dim, c->dtype, (cudaStream_t)stream) == cudaSuccess
-             ? MK_OK
-             : MK_ERR_CUDA;
+  // units of work are counted in 32 bits (64 keys x (128 rows or a request))
+  const int64_t tiles = (int64_t)b->max_tokens * p.rep / 64 + b->n;
+  if (tiles * c->n_kv_heads * ((int64_t)b->max_blocks * b->page_size / 64 + 1) > 0x7fffffffll)
+    return MK_ERR_UNSUPPORTED;
+  const PagedKv kv = {c->k, c->v, c->page_stride, c->head_stride, c->token_stride,
+                      c->n_pages, c->n_kv_heads, c->page_size};
+  const cudaError_t e = paged_attention_launch(p, kv, c->head_dim, c->dtype, c->workspace, (cudaStream_t)stream);
+  if (e == cudaSuccess) return MK_OK;
+  cudaGetLastError();
+  return MK_ERR_CUDA;
 }

@@ -36,9 +36,37 @@ struct PagedAttnParams {
   int64_t page_stride, head_stride, token_stride;
   int n, max_blocks, rows, max_new, n_pages, page_shift;
   int hkv, rep, window;  // window 0x7fffffff: none
+  int few_rows;  // requests of at most this many rows (new tokens x rep) go to the few-row kernel
   float scale;
 };
 
-cudaError_t paged_attention_launch(const PagedAttnParams& p, int d, int dtype, cudaStream_t st);
+// The cache as the tensor maps see it.
+struct PagedKv {
+  const void *k, *v;
+  int64_t page_stride, head_stride, token_stride;
+  int n_pages, hkv, page;
+};
+
+// A pair's (or tile's) rows whose keys were divided among CTAs: `parts` of them
+// from CTA desc index on; 0: none.
+struct PartDesc {
+  int row0, rows, head, parts;
+};
+// Workspace of one kernel's divided rows: part 2 c (+ 1) is CTA c's first (second)
+// unfinished run of keys, o [part][rt][head_dim] unnormalised, ml [part][rt]
+// maximum (base 2) and sum.
+struct PagedParts {
+  PartDesc* desc;
+  float2* ml;
+  float* o;
+  int rt, ctas;
+};
+
+cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
+                             bool bf, cudaStream_t st);
+cudaError_t paged_join_launch(const PagedAttnParams& p, const PagedParts& a, const PagedParts& b, int d,
+                              bool bf, cudaStream_t st);
+cudaError_t paged_attention_launch(const PagedAttnParams& p, const PagedKv& kv, int d, int dtype,
+                                   void* workspace, cudaStream_t st);
 
 }  // namespace mk

@@ -1,9 +1,5 @@
 // Attention over a paged KV cache.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "mk_device.cuh"
-#include "mk_paged.h"
+#include "mk_paged_dev.cuh"
 
 namespace mk {
 namespace {
@@ -35,6 +31,7 @@ __global__ void __launch_bounds__(256) paged_attn_kernel(const PagedAttnParams P
       break;
     }
   if (r < 0) return;
+  if ((int64_t)(P.cu[r + 1] - P.cu[r]) * P.rep <= P.few_rows) return;
   const int first = P.cu[r], add = P.cu[r + 1] - first, room = P.max_blocks << P.page_shift;
   const int kv_raw = P.kv[r], kv = min(max(kv_raw, 0), room);
   if (kv != kv_raw && P.status && lane == 0) atomicCAS(P.status, MK_OK, MK_ERR_BOUNDS);
@@ -78,7 +75,31 @@ __global__ void __launch_bounds__(256) paged_attn_kernel(const PagedAttnParams P
 
 }  // namespace
 
-cudaError_t paged_attention_launch(const PagedAttnParams& p, int d, int dtype, cudaStream_t st) {
+cudaError_t paged_attention_launch(const PagedAttnParams& p0, const PagedKv& kv, int d, int dtype,
+                                   void* workspace, cudaStream_t st) {
+  PagedAttnParams p = p0;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const bool bf = dtype == MK_BF16;
+  // rows of the few-row kernel: those of the longest request where it takes
+  // them all, else those of single tokens
+  const int64_t most = (int64_t)p.max_new * p.rep;
+  const bool all_few = most <= 32;
+  const int want = all_few ? (int)most : p.rep;
+  p.few_rows = want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 ? 32 : 0;
+  uint8_t* w = (uint8_t*)workspace;
+  PagedParts few{};
+  few.rt = p.few_rows;
+  few.ctas = sms;
+  few.desc = (PartDesc*)w;
+  few.ml = (float2*)(w + 16384);
+  few.o = (float*)(w + 16384 + 2 * 8 * 32 * (size_t)sms);
+  e = paged_few_launch(p, kv, few, d, bf, st);
+  if (e != cudaSuccess) return e;
+  e = paged_join_launch(p, few, PagedParts{}, d, bf, st);
+  if (e != cudaSuccess || all_few) return e;
   const int64_t warps = (int64_t)p.rows * p.hkv * p.rep;
   const unsigned grid = (unsigned)((warps + 7) / 8);
   if (d == 128 && dtype == MK_BF16) paged_attn_kernel<128, true><<<grid, 256, 0, st>>>(p);

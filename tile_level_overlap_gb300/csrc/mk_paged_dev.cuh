@@ -1,0 +1,155 @@
+// Device helpers of the paged-cache kernels: conversions, the requests' scan,
+// bounded mbarrier waits, page loads.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mk_device.cuh"
+#include "mk_paged.h"
+
+namespace mk {
+
+__device__ __forceinline__ void latch(int32_t* status, int code) {
+  if (status) atomicCAS(status, MK_OK, code);
+}
+
+// Largest r in [0, n) with a[r] <= x (a non-decreasing, a[0] <= x).
+__device__ __forceinline__ int find_le(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------- 16-bit pairs
+template <bool BF>
+__device__ __forceinline__ float2 up2(uint32_t w) {
+  if constexpr (BF) return make_float2(bf_lo(w), bf_hi(w));
+  const __half2 h = *reinterpret_cast<const __half2*>(&w);
+  return __half22float2(h);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t down2(float a, float b) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <bool BF>
+__device__ __forceinline__ void up8(const uint4 w, float (&x)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = up2<BF>(u[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <bool BF>
+__device__ __forceinline__ uint4 down8(const float (&x)[8]) {
+  return make_uint4(down2<BF>(x[0], x[1]), down2<BF>(x[2], x[3]), down2<BF>(x[4], x[5]),
+                    down2<BF>(x[6], x[7]));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---------------------------------------------------------------- dependent launches
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait_prior() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- bounded waits
+// Wait for the phase; after two seconds give up: `*dead` is raised, the status
+// latched, and every later wait of the CTA returns at once.
+static __device__ __noinline__ void wait_gave_up(volatile int* dead, int32_t* status) {
+  *dead = 1;
+  latch(status, MK_ERR_TIMEOUT);
+}
+__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, volatile int* dead,
+                                           int32_t* status) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*dead) return;
+    if (globaltimer() - t0 > 2000000000ull) {
+      wait_gave_up(dead, status);
+      return;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- page loads
+// Box of 64 elements x tokens of one head and page (tensor map dimensions:
+// element, token, head, page).  A page outside the map reads as zeros.
+__device__ __forceinline__ void tma_page(void* dst, const void* tmap, int x, int token, int head,
+                                         int page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// ---------------------------------------------------------------- the requests
+// What a request asks of attention, from the device arrays; `bad` where the
+// status is to be latched.  Keys [lo, hi) are what any of its rows may see;
+// its first row stands at pos0.
+struct Request {
+  int row0, add, pos0, lo, hi;
+  bool bad;
+};
+__device__ __forceinline__ Request read_request(const PagedAttnParams& P, int r) {
+  Request q;
+  const int c0 = P.cu[r], c1 = P.cu[r + 1], kv = P.kv[r];
+  const int room = P.max_blocks << P.page_shift;
+  const int kvp = max(kv, 0);
+  q.bad = kv < 0 || kvp > room;
+  q.row0 = c0;
+  q.add = 0;
+  if (c0 < 0 || c1 < c0 || c1 > P.rows || c1 - c0 > P.max_new) q.bad = true;
+  else q.add = c1 - c0;
+  q.pos0 = kvp - q.add;
+  q.hi = min(kvp, room);
+  // the first row's window begins at pos0 - window + 1
+  q.lo = q.pos0 >= P.window ? min(q.pos0 - P.window + 1, q.hi) : 0;
+  return q;
+}
+
+// Exclusive prefix sums of one value per thread of a block of W warps.
+template <int W>
+__device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += u;
+  }
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const int t = tmp[w];
+    before += w < warp ? t : 0;
+    all += t;
+  }
+  *total = all;
+  return before + x - v;
+}
+
+}  // namespace mk

@@ -1,0 +1,593 @@
+// Attention over a paged cache for requests with few rows (new tokens x query
+// heads per kv head <= 32): decode steps and drafted tokens.
+//
+// Bound by HBM: every key and value of a (request, kv head) is read once, 4
+// head_dim bytes, for 4 head_dim flops per row.  The work is the list of key
+// blocks of all (request, kv head) pairs, end to end; each of the persistent
+// CTAs (one per SM) takes an equal run of it, whatever the lengths, so a run
+// may begin and end inside a pair's keys.  Such a part leaves its running
+// maximum, sum and unnormalised output in the workspace, and a second launch
+// joins the parts of each pair in the order of their keys.
+//
+// A producer warp walks the run: it posts each pair's description and query
+// rows (bulk copies) to a small ring and loads the key blocks (32 KB of keys
+// and values: 64 keys at head_dim 128, 128 at 64) page by page through a
+// ring with TMA, 128-byte swizzle.  Eight consumer warps in two groups take
+// the blocks in turn, 16 (32) keys each warp, with a softmax state of their
+// own: S^T = K Q^T and O^T += V^T P^T by warp-level products, keys and
+// dimensions on the 16-row side and the query rows on the 8-column side, so
+// that 8 rows fill a product that would be half empty the other way round,
+// and the softmax of a row stays in the lanes that rescale its output.  The
+// legacy tensor path is ample here (a block costs its four warps 16 products
+// each).  At the end of a pair the eight states are joined in shared memory.
+#include "mk_paged_dev.cuh"
+#include "mk_tmap.h"
+
+namespace mk {
+namespace {
+
+constexpr int PF_WARPS = 8;             // consumers
+constexpr int PF_THREADS = 32 * (PF_WARPS + 1);
+constexpr int PF_STAGE = 32768;         // one block's keys, then its values
+
+template <int HD, int NT>
+struct FewCfg {
+  static constexpr int KS = HD == 128 ? 64 : 128;  // keys of a block
+  static constexpr int RT = 8 * NT;                // rows of an item
+  static constexpr int QROW = HD * 2 + 16;         // padded: conflict-free row reads
+  static constexpr int QSLOTS = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int OROW = HD + 4;              // floats; conflict-free column pairs
+  static constexpr int STAGES = NT == 4 ? 4 : 5;
+  static constexpr int o_q = STAGES * PF_STAGE;
+  static constexpr int o_merge = o_q + QSLOTS * RT * QROW;
+  static constexpr int o_ml = o_merge + PF_WARPS * 8 * OROW * 4;
+  static constexpr int o_meta = o_ml + PF_WARPS * RT * 8;
+  static constexpr int o_bar = o_meta + QSLOTS * 48;
+  static constexpr int o_pre = o_bar + 8 * (2 * STAGES + 2 * QSLOTS) + 64;
+  static constexpr int total(int n) { return o_pre + 4 * (n + 1); }
+};
+static_assert(FewCfg<128, 1>::total(MK_PAGED_MAX_REQUESTS) <= 232448 &&
+                  FewCfg<128, 2>::total(MK_PAGED_MAX_REQUESTS) <= 232448 &&
+                  FewCfg<128, 4>::total(MK_PAGED_MAX_REQUESTS) <= 232448,
+              "shared memory of a CTA");
+
+// One part of a (request, kv head): blocks [blk, blk + nblk) of its `of`.
+struct Segment {
+  int key0, nblk;            // first key; 0 blocks: the end of the run
+  int row0, rows, head;
+  int pos0, lo, hi;          // Request's
+  int part;                  // workspace part, -1: all of the pair's blocks
+  int pad[3];
+};
+static_assert(sizeof(Segment) == 48, "meta slot");
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movm(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+template <bool BF>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF) {
+    mma_bf16_16816(c, a[0], a[1], a[2], a[3], b0, b1);
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+// Untiled copy of one query row into shared memory.
+__device__ __forceinline__ void bulk_row(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Whether any of the barrier's threads says so.
+__device__ __forceinline__ bool any_of(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.or.pred q, %1, %2, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+// A CTA that gives up leaves only after its loads in flight, none of which
+// takes a millisecond, have landed.
+__device__ __noinline__ void let_copies_land() {
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 1000000ull) {
+  }
+}
+
+template <int HD, bool BF, int NT>
+__global__ void __launch_bounds__(PF_THREADS, 1)
+    paged_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                     const __grid_constant__ PagedAttnParams P, const __grid_constant__ PagedParts W) {
+  using C = FewCfg<HD, NT>;
+  constexpr int KS = C::KS, RT = C::RT, MT = KS / 64;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::o_bar);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* qfull = empty + C::STAGES;
+  uint64_t* qempty = qfull + C::QSLOTS;
+  volatile int* dead = reinterpret_cast<volatile int*>(qempty + C::QSLOTS);
+  int* scan_tmp = const_cast<int*>(dead) + 1;
+  int* pre = reinterpret_cast<int*>(smem + C::o_pre);
+  Segment* meta = reinterpret_cast<Segment*>(smem + C::o_meta);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  grid_launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], PF_WARPS);
+    }
+    for (int s = 0; s < C::QSLOTS; ++s) {
+      mbar_init(&qfull[s], 1);
+      mbar_init(&qempty[s], PF_WARPS);
+    }
+    *dead = 0;
+    W.desc[blockIdx.x].parts = 0;
+    fence_mbar_init();
+  }
+  for (int i = tid; i < C::QSLOTS * RT * C::QROW / 16; i += PF_THREADS)
+    reinterpret_cast<uint4*>(smem + C::o_q)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+
+  // units: key blocks of all (request, kv head) pairs, pairs of a request end to end
+  const int per = (P.n + PF_THREADS - 1) / PF_THREADS;
+  int mine = 0;
+  bool bad = false;
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    if (r >= P.n) break;
+    const Request q = read_request(P, r);
+    bad |= q.bad;
+    int u = 0;
+    if (q.add > 0 && (int64_t)q.add * P.rep <= P.few_rows)
+      u = P.hkv * max(1, (q.hi + KS - 1) / KS - q.lo / KS);
+    pre[r] = u;
+    mine += u;
+  }
+  int T;
+  int at = block_scan<PF_THREADS / 32>(mine, scan_tmp, &T);
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    if (r >= P.n) break;
+    const int u = pre[r];
+    pre[r] = at;
+    at += u;
+  }
+  if (tid == 0) pre[P.n] = T;
+  if (bad && blockIdx.x == 0) latch(P.status, MK_ERR_BOUNDS);
+  __syncthreads();
+
+  // this CTA's run of units: [c T / G, (c + 1) T / G) of the G CTAs in use
+  const int G = min((int)gridDim.x, T), c = blockIdx.x;
+  if (c >= G) return;
+  const int u0 = (int)((int64_t)c * T / G), u1 = (int)((int64_t)(c + 1) * T / G);
+
+  if (warp == PF_WARPS) {
+    // ------------------------------------------------------------ producer
+    const int boxt = min(KS, 1 << P.page_shift), nbox = KS / boxt;
+    const int mask = (1 << P.page_shift) - 1;
+    int r = find_le(pre, P.n, u0), stage = 0, slot = 0;
+    uint32_t sphase = 1, qphase = 1;  // parities of the "empty" waits
+    for (int u = u0; u < u1;) {
+      while (pre[r + 1] <= u) ++r;
+      const Request q = read_request(P, r);
+      const int nb = (pre[r + 1] - pre[r]) / P.hkv, local = u - pre[r];
+      const int head = local / nb, blk = local - head * nb, nblk = min(nb - blk, u1 - u);
+      const int b0 = q.lo / KS + blk, rows = q.add * P.rep;
+      const bool whole = blk == 0 && nblk == nb;
+      if (blk == 0 && !whole) {  // joined by this CTA's block of the second launch
+        const int last = (int)(((int64_t)(u + nb) * G - 1) / T);  // CTA of the pair's last unit
+        if (lane == 0) {
+          PartDesc d;
+          d.row0 = q.row0; d.rows = rows; d.head = head; d.parts = last - c + 1;
+          W.desc[c] = d;
+        }
+      }
+      wait_phase(&qempty[slot], qphase, dead, P.status);
+      if (*dead) return let_copies_land();
+      if (lane == 0) {
+        Segment s;
+        s.key0 = b0 * KS; s.nblk = nblk; s.row0 = q.row0; s.rows = rows; s.head = head;
+        s.pos0 = q.pos0; s.lo = q.lo; s.hi = q.hi;
+        s.part = whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
+        meta[slot] = s;
+        mbar_arrive_expect_tx(&qfull[slot], (uint32_t)rows * HD * 2);
+      }
+      __syncwarp();
+      if (lane < rows)
+        bulk_row(smem + C::o_q + (slot * RT + lane) * C::QROW,
+                 P.q + (int64_t)(q.row0 + lane / P.rep) * P.q_stride +
+                     (int64_t)(head * P.rep + lane % P.rep) * HD,
+                 HD * 2, &qfull[slot]);
+      if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
+      const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
+      // page of this lane's box of a block; -1 where no row sees any of it
+      auto page_of = [&](int b) {
+        const int key = b * KS + lane * boxt;
+        if (lane >= nbox || key >= q.hi || key + boxt <= q.lo) return -1;
+        const int p = tab[key >> P.page_shift];
+        if (p >= 0 && p < P.n_pages) return p;
+        latch(P.status, MK_ERR_BOUNDS);
+        return -1;
+      };
+      int page = page_of(b0);
+      for (int i = 0; i < nblk; ++i) {
+        const int next = i + 1 < nblk ? page_of(b0 + i + 1) : -1;
+        wait_phase(&empty[stage], sphase, dead, P.status);
+        if (*dead) return let_copies_land();
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], PF_STAGE);
+        __syncwarp();
+        if (lane < nbox) {
+          uint8_t* dst = smem + stage * PF_STAGE + lane * boxt * 128;
+          const int tok = ((b0 + i) * KS + lane * boxt) & mask;
+#pragma unroll
+          for (int x = 0; x < HD / 64; ++x)
+            tma_page(dst + x * KS * 128, &tk, 64 * x, tok, head, page, &full[stage]);
+#pragma unroll
+          for (int x = 0; x < HD / 64; ++x)
+            tma_page(dst + PF_STAGE / 2 + x * KS * 128, &tv, 64 * x, tok, head, page, &full[stage]);
+        }
+        if (++stage == C::STAGES) { stage = 0; sphase ^= 1; }
+        page = next;
+      }
+      u += nblk;
+    }
+    // the end of the run
+    wait_phase(&qempty[slot], qphase, dead, P.status);
+    if (*dead) return let_copies_land();
+    if (lane == 0) {
+      meta[slot].nblk = 0;
+      mbar_arrive(&qfull[slot]);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int grp = warp >> 2, kw = warp & 3, g = lane >> 2, t = lane & 3;
+  const float cs = P.scale * 1.4426950408889634f;
+  float* merge = reinterpret_cast<float*>(smem + C::o_merge);
+  float2* mls = reinterpret_cast<float2*>(smem + C::o_ml);
+  // row and 16-byte chunk that this lane addresses in a 16 x 16 matrix load
+  const int lr = (lane & 7) + ((lane >> 3) & 1) * 8, lc = lane >> 4;     // keys on rows
+  const int vr = (lane & 7) + (lane >> 4) * 8, vc = (lane >> 3) & 1;     // transposed
+  int stage = 0, slot = 0, turn = 0;
+  uint32_t sphase = 0, qphase = 0;
+  for (;;) {
+    wait_phase(&qfull[slot], qphase, dead, P.status);
+    if (any_of(2, 32 * PF_WARPS, *dead)) break;  // all warps agree, also on giving up
+    const Segment s = meta[slot];
+    if (s.nblk == 0) break;
+    const uint32_t qs = smem_u32(smem + C::o_q + slot * RT * C::QROW);
+    uint32_t qf[NT <= 2 ? NT : 1][HD / 16][2];
+    if constexpr (NT <= 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k2 = 0; k2 < HD / 32; ++k2) {
+          uint32_t r4[4];
+          ldsm4(r4, qs + (nt * 8 + (lane & 7)) * C::QROW + k2 * 64 + (lane >> 3) * 16);
+          qf[nt][2 * k2][0] = r4[0]; qf[nt][2 * k2][1] = r4[1];
+          qf[nt][2 * k2 + 1][0] = r4[2]; qf[nt][2 * k2 + 1][1] = r4[3];
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qempty[slot]);
+    }
+    // keys [first, last] are what this lane's rows see
+    int first[NT][2], last[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = nt * 8 + 2 * t + e, pos = s.pos0 + (row < s.rows ? row / P.rep : 0);
+        last[nt][e] = min(pos, s.hi - 1);
+        first[nt][e] = pos >= P.window ? pos - P.window + 1 : 0;
+      }
+    float m[NT][2], l[NT][2], o[HD / 16][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
+    }
+    // every row sees the keys [all_lo, all_hi)
+    const int end = s.pos0 + (s.rows - 1) / P.rep;
+    const int all_lo = end >= P.window ? end - P.window + 1 : 0, all_hi = min(s.pos0 + 1, s.hi);
+    for (int i = 0; i < s.nblk; ++i) {
+      // both groups see every block's phase, also of those they leave to the
+      // other one (a warp that skipped one could take the next for it)
+      wait_phase(&full[stage], sphase, dead, P.status);
+      if (turn == grp) {
+        const uint32_t kb = smem_u32(smem + stage * PF_STAGE), vb = kb + PF_STAGE / 2;
+        const int key0 = s.key0 + i * KS;
+        const bool partial = key0 < all_lo || key0 + KS > all_hi;
+        float sc[MT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          uint32_t b4[NT <= 2 ? 1 : NT][2];
+          if constexpr (NT > 2) {
+#pragma unroll
+            for (int n2 = 0; n2 < NT / 2; ++n2) {
+              uint32_t r4[4];
+              ldsm4(r4, qs + (n2 * 16 + (lane & 7) + (lane >> 4) * 8) * C::QROW + ks * 32 + ((lane >> 3) & 1) * 16);
+              b4[2 * n2][0] = r4[0]; b4[2 * n2][1] = r4[1];
+              b4[2 * n2 + 1][0] = r4[2]; b4[2 * n2 + 1][1] = r4[3];
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[4];
+            const int row = (kw * MT + mt) * 16 + lr, ch = 2 * ks + lc;
+            ldsm4(a, kb + (ch >> 3) * (KS * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (NT <= 2) mma16<BF>(sc[mt][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+              else mma16<BF>(sc[mt][nt], a, b4[nt][0], b4[nt][1]);
+            }
+          }
+        }
+        // softmax of the block's columns: this lane has keys g, g + 8 of each
+        // 16, rows 2t and 2t + 1 of each 8
+        float al[NT][2];
+        bool move = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float x = sc[mt][nt][2 * h + e] * cs;
+                if (partial) {
+                  const int key = key0 + (kw * MT + mt) * 16 + g + 8 * h;
+                  if (key > last[nt][e] || key < first[nt][e]) x = -INFINITY;
+                }
+                sc[mt][nt][2 * h + e] = x;
+                mx = fmaxf(mx, x);
+              }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m[nt][e], mx), ref = mn == -INFINITY ? 0.f : mn;
+            al[nt][e] = ex2(m[nt][e] - ref);
+            move |= mn != m[nt][e];
+            m[nt][e] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float p = ex2(sc[mt][nt][2 * h + e] - ref);
+                sc[mt][nt][2 * h + e] = p;
+                sum += p;
+              }
+            l[nt][e] = l[nt][e] * al[nt][e] + sum;
+          }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int x = 0; x < HD / 16; ++x)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[x][nt][e] *= al[nt][e & 1];
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t b[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            b[nt][0] = movm(down2<BF>(sc[mt][nt][0], sc[mt][nt][1]));
+            b[nt][1] = movm(down2<BF>(sc[mt][nt][2], sc[mt][nt][3]));
+          }
+          // values of keys that no row sees may be anything: made zero
+          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+          if (partial) {
+            const int key = key0 + (kw * MT + mt) * 16 + 2 * t;
+            auto seen = [&](int k) { return k >= s.lo && k < s.hi; };
+            keep0 = (seen(key) ? 0xffffu : 0u) | (seen(key + 1) ? 0xffff0000u : 0u);
+            keep1 = (seen(key + 8) ? 0xffffu : 0u) | (seen(key + 9) ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+          for (int x = 0; x < HD / 16; ++x) {
+            uint32_t a[4];
+            const int row = (kw * MT + mt) * 16 + vr, ch = 2 * x + vc;
+            ldsm4t(a, vb + (ch >> 3) * (KS * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            a[0] &= keep0; a[1] &= keep0; a[2] &= keep1; a[3] &= keep1;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[x][nt], a, b[nt][0], b[nt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      turn ^= 1;
+      if (++stage == C::STAGES) { stage = 0; sphase ^= 1; }
+    }
+    if constexpr (NT > 2) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qempty[slot]);
+    }
+    if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
+
+    // join the eight warps' states, eight rows at a time
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt * 8 >= s.rows) break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[nt][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        l[nt][e] = x;
+      }
+      named_bar(1, 32 * PF_WARPS);  // the previous rows have been read
+      if (g == 0) {
+        mls[warp * RT + nt * 8 + 2 * t] = make_float2(m[nt][0], l[nt][0]);
+        mls[warp * RT + nt * 8 + 2 * t + 1] = make_float2(m[nt][1], l[nt][1]);
+      }
+      float* mine_o = merge + warp * 8 * C::OROW;
+#pragma unroll
+      for (int x = 0; x < HD / 16; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mine_o[(2 * t + (e & 1)) * C::OROW + 16 * x + g + 8 * (e >> 1)] = o[x][nt][e];
+      named_bar(1, 32 * PF_WARPS);
+      constexpr int LPR = HD / 4;  // threads of a row
+      const int row = tid / LPR, d4 = (tid % LPR) * 4, irow = nt * 8 + row;
+      if (row < 8 && irow < s.rows) {
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < PF_WARPS; ++w) mm = fmaxf(mm, mls[w * RT + irow].x);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float ll = 0.f;
+#pragma unroll
+        for (int w = 0; w < PF_WARPS; ++w) {
+          const float2 ml = mls[w * RT + irow];
+          const float f = ex2(ml.x - ref);
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * C::OROW + d4);
+          ll += ml.y * f;
+          acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
+        }
+        if (s.part < 0) {
+          const int tok = s.row0 + irow / P.rep, hq = s.head * P.rep + irow % P.rep;
+          const float inv = ll > 0.f ? 1.f / ll : 0.f;
+          *reinterpret_cast<uint2*>(P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD + d4) =
+              make_uint2(down2<BF>(acc.x * inv, acc.y * inv), down2<BF>(acc.z * inv, acc.w * inv));
+          if (P.lse && d4 == 0)
+            P.lse[(int64_t)tok * (P.hkv * P.rep) + hq] =
+                ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        } else {
+          *reinterpret_cast<float4*>(W.o + ((int64_t)s.part * W.rt + irow) * HD + d4) = acc;
+          if (d4 == 0) W.ml[(int64_t)s.part * W.rt + irow] = make_float2(mm, ll);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- join
+// Block c joins the parts of the pair that CTA c of the first launch left open:
+// its own second part and the first parts of the CTAs after it, in that order.
+template <int HD, bool BF>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams P,
+                                                         const __grid_constant__ PagedParts A,
+                                                         const __grid_constant__ PagedParts B) {
+  grid_wait_prior();
+  const bool first = (int)blockIdx.x < A.ctas;
+  const PagedParts& W = first ? A : B;
+  const int c = first ? blockIdx.x : blockIdx.x - A.ctas;
+  const PartDesc d = W.desc[c];
+  if (d.parts == 0) return;
+  constexpr int LPR = HD / 4;
+  const int d4 = (threadIdx.x % LPR) * 4;
+  for (int row = blockIdx.y * (256 / LPR) + threadIdx.x / LPR; row < d.rows; row += gridDim.y * (256 / LPR)) {
+    float mm = -INFINITY, ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < d.parts; ++k) {
+      const int64_t at = (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * W.rt + row;
+      const float2 ml = W.ml[at];
+      const float4 v = *reinterpret_cast<const float4*>(W.o + at * HD + d4);
+      const float mn = fmaxf(mm, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+      const float a = ex2(mm - ref), f = ex2(ml.x - ref);
+      ll = ll * a + ml.y * f;
+      acc.x = acc.x * a + v.x * f; acc.y = acc.y * a + v.y * f;
+      acc.z = acc.z * a + v.z * f; acc.w = acc.w * a + v.w * f;
+      mm = mn;
+    }
+    const int tok = d.row0 + row / P.rep, hq = d.head * P.rep + row % P.rep;
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    *reinterpret_cast<uint2*>(P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD + d4) =
+        make_uint2(down2<BF>(acc.x * inv, acc.y * inv), down2<BF>(acc.z * inv, acc.w * inv));
+    if (P.lse && d4 == 0)
+      P.lse[(int64_t)tok * (P.hkv * P.rep) + hq] =
+          ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+template <int HD, bool BF, int NT>
+cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  if (!make_page_tmap(&tk, kv.k, kv, HD, FewCfg<HD, NT>::KS, BF) ||
+      !make_page_tmap(&tv, kv.v, kv, HD, FewCfg<HD, NT>::KS, BF))
+    return cudaErrorInvalidValue;
+  const int smem = FewCfg<HD, NT>::total(p.n);
+  const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<HD, BF, NT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  paged_few_kernel<HD, BF, NT><<<w.ctas, PF_THREADS, smem, st>>>(tk, tv, p, w);
+  return cudaGetLastError();
+}
+
+template <int HD, bool BF>
+cudaError_t launch_rows(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
+  return p.few_rows <= 8    ? launch<HD, BF, 1>(p, kv, w, st)
+         : p.few_rows <= 16 ? launch<HD, BF, 2>(p, kv, w, st)
+                            : launch<HD, BF, 4>(p, kv, w, st);
+}
+
+}  // namespace
+
+cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
+                             bool bf, cudaStream_t st) {
+  if (d == 128) return bf ? launch_rows<128, true>(p, kv, w, st) : launch_rows<128, false>(p, kv, w, st);
+  return bf ? launch_rows<64, true>(p, kv, w, st) : launch_rows<64, false>(p, kv, w, st);
+}
+
+cudaError_t paged_join_launch(const PagedAttnParams& p, const PagedParts& a, const PagedParts& b, int d,
+                              bool bf, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(a.ctas + b.ctas, 1);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (d == 128)
+    return bf ? cudaLaunchKernelEx(&cfg, paged_join_kernel<128, true>, p, a, b)
+              : cudaLaunchKernelEx(&cfg, paged_join_kernel<128, false>, p, a, b);
+  return bf ? cudaLaunchKernelEx(&cfg, paged_join_kernel<64, true>, p, a, b)
+            : cudaLaunchKernelEx(&cfg, paged_join_kernel<64, false>, p, a, b);
+}
+
+}  // namespace mk
