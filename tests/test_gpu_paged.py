@@ -323,6 +323,9 @@ ATT = [
     ([30000, 17, 21111, 25000], [1, 1, 1, 1], 16, 16, 128, 64, 0, "hp", "bf16"),
     ([30000, 17, 21111, 25000], [4, 1, 3, 2], 32, 8, 64, 16, 0, "hp", "fp16"),
     ([30000, 17, 21111], [4, 8, 3], 32, 8, 128, 16, 0, "ph", "bf16"),
+    ([9000], [2000], 8, 8, 64, 16, 0, "hp", "bf16"),
+    ([6000, 30, 999], [1111, 1300, 1], 8, 4, 128, 32, 0, "ph", "fp16"),
+    ([6000, 30], [1111, 1300], 14, 2, 128, 64, 1500, "hp", "bf16"),
 ]
 
 

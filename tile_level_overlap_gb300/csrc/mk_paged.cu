@@ -1,6 +1,7 @@
 // Paged KV cache: a step's tables from the requests' lengths, the new tokens'
 // norm, rotary positions and write to their pages, and the C entry points of
 // the paged operators (include/mk.h).
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -241,6 +242,43 @@ cudaError_t append_launch(const PagedAppendParams& p, int dtype, cudaStream_t st
   return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------- attention
+// Which kernel takes which request is a rule on its rows (new tokens x query
+// heads per kv head); both walk the same device arrays and leave the other's
+// requests out, so that a step may mix them.
+cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool bf, void* workspace,
+                             cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // The few-row kernel has the rows of the longest request where it takes them
+  // all, else those of a single token (its products cost by the row).
+  const int64_t most = (int64_t)p.max_new * p.rep;
+  const bool all_few = most <= 32;
+  const int want = all_few ? (int)most : p.rep;
+  p.few_rows = want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 ? 32 : 0;
+  // workspace: descriptions, maxima and sums, outputs of the two kernels' parts
+  const int ctas = std::min(sms, 224);
+  uint8_t* w = (uint8_t*)workspace;
+  PagedParts few{}, chunk{};
+  few.rt = 32;
+  chunk.rt = 256;
+  few.ctas = ctas;
+  chunk.ctas = all_few ? 0 : ctas;
+  few.desc = (PartDesc*)w;
+  chunk.desc = few.desc + ctas;
+  few.ml = (float2*)(chunk.desc + ctas);
+  chunk.ml = few.ml + (size_t)2 * ctas * few.rt;
+  few.o = (float*)(chunk.ml + (size_t)2 * ctas * chunk.rt);
+  chunk.o = few.o + (size_t)2 * ctas * few.rt * d;
+  static_assert(224 * (2 * 16 + 2 * (32 + 256) * (8 + 128 * 4)) <= MK_PAGED_WORKSPACE_BYTES, "workspace");
+  e = paged_few_launch(p, kv, few, d, bf, st);
+  if (e == cudaSuccess && !all_few) e = paged_chunk_launch(p, kv, chunk, d, bf, st);
+  if (e == cudaSuccess) e = paged_join_launch(p, few, chunk, d, bf, st);
+  return e;
+}
+
 // ---------------------------------------------------------------- argument checks
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
@@ -392,10 +430,8 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch*
   if (b->max_tokens == 0) return MK_OK;
   PagedAttnParams p{};
   p.q = (const uint16_t*)q; p.out = (uint16_t*)out; p.lse = lse;
-  p.kc = (const uint16_t*)c->k; p.vc = (const uint16_t*)c->v;
   p.table = b->block_table; p.cu = b->cu_new; p.kv = b->kv_lens; p.status = c->status;
   p.q_stride = q_stride; p.o_stride = out_stride;
-  p.page_stride = c->page_stride; p.head_stride = c->head_stride; p.token_stride = c->token_stride;
   p.n = b->n; p.max_blocks = b->max_blocks; p.rows = b->max_tokens; p.max_new = b->max_new;
   p.n_pages = c->n_pages; p.page_shift = log2_page(c->page_size);
   p.hkv = c->n_kv_heads; p.rep = c->n_q_heads / c->n_kv_heads;
@@ -407,7 +443,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch*
     return MK_ERR_UNSUPPORTED;
   const PagedKv kv = {c->k, c->v, c->page_stride, c->head_stride, c->token_stride,
                       c->n_pages, c->n_kv_heads, c->page_size};
-  const cudaError_t e = paged_attention_launch(p, kv, c->head_dim, c->dtype, c->workspace, (cudaStream_t)stream);
+  const cudaError_t e = attention_launch(p, kv, c->head_dim, c->dtype == MK_BF16, c->workspace, (cudaStream_t)stream);
   if (e == cudaSuccess) return MK_OK;
   cudaGetLastError();
   return MK_ERR_CUDA;

@@ -29,11 +29,9 @@ struct PagedAttnParams {
   const uint16_t* q;
   uint16_t* out;
   float* lse;
-  const uint16_t *kc, *vc;
   const int32_t *table, *cu, *kv;
   int32_t* status;
   int64_t q_stride, o_stride;
-  int64_t page_stride, head_stride, token_stride;
   int n, max_blocks, rows, max_new, n_pages, page_shift;
   int hkv, rep, window;  // window 0x7fffffff: none
   int few_rows;  // requests of at most this many rows (new tokens x rep) go to the few-row kernel
@@ -64,9 +62,9 @@ struct PagedParts {
 
 cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
                              bool bf, cudaStream_t st);
+cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
+                               bool bf, cudaStream_t st);
 cudaError_t paged_join_launch(const PagedAttnParams& p, const PagedParts& a, const PagedParts& b, int d,
                               bool bf, cudaStream_t st);
-cudaError_t paged_attention_launch(const PagedAttnParams& p, const PagedKv& kv, int d, int dtype,
-                                   void* workspace, cudaStream_t st);
 
 }  // namespace mk

@@ -1,0 +1,548 @@
+// Attention over a paged cache for requests with many rows: chunks of prompts.
+//
+// Bound by the tensor cores: 4 head_dim flops per (row, key).  A tile is up to
+// 256 rows of one (request, kv head), as two halves of 128: whole tokens, each
+// with all query heads of the kv head, so that one load of a key block serves
+// them all.  The work is the list of key blocks (128 keys) of all tiles, end
+// to end, after the causal bound and the window; each persistent CTA (one per
+// SM) takes an equal run of it, and rows whose keys lie in several runs are
+// joined as in the few-row kernel.
+//
+// Warps of a CTA: one loads (TMA: queries, then K and V blocks page by page,
+// 128-byte swizzle), one issues tcgen05.mma, two groups of four own a half each
+// (thread = row).  Per half and block: S = Q K^T into 128 TMEM columns; its
+// group reads the row, masks it where the block crosses a bound, exponentiates
+// relative to a running maximum and writes P over S in the cache's type; O += P V
+// with P read from TMEM.  The two halves alternate on the tensor cores: while
+// one's softmax runs the other's products do.  The maximum that P is relative
+// to is only moved when it has grown by more than 2^8 (P stays far inside the
+// 16-bit range and sums are fp32), so O, which lives in TMEM, is seldom rescaled.
+// No wait on O is needed for that: S of block j is issued behind P V of block
+// j - 1, so when S is complete O is at rest.
+#include "mk_paged_dev.cuh"
+#include "mk_paged_tc.cuh"
+#include "mk_tmap.h"
+
+namespace mk {
+namespace {
+
+constexpr int PC_THREADS = 384;
+constexpr int PC_LOAD = 8, PC_MMA = 9;       // warps; 0-3 and 4-7 own the halves
+constexpr int PC_REGS = 168, PC_REGS_SOFT = 216, PC_REGS_REST = 72;
+static_assert(2 * PC_REGS_SOFT + PC_REGS_REST == 3 * PC_REGS, "registers of the three warpgroups");
+
+template <int HD>
+struct ChunkCfg {
+  static constexpr int TILE = 128 * HD * 2;                // 128 rows or keys
+  static constexpr int STAGES = HD == 128 ? 4 : 8;         // K and V blocks in turn
+  static constexpr int SLOTS = 2;
+  static constexpr int o_kv = 2 * TILE;                    // after the queries' halves
+  static constexpr int o_meta = o_kv + STAGES * TILE;
+  static constexpr int o_bar = o_meta + SLOTS * 64;
+  static constexpr int o_pre = o_bar + 256;
+  static constexpr int total(int n) { return o_pre + 4 * (n + 1); }
+};
+static_assert(ChunkCfg<128>::total(MK_PAGED_MAX_REQUESTS) <= 232448, "shared memory of a CTA");
+
+struct Tile {
+  int key0, nblk;          // first key of the run; 0 blocks: the end
+  int row0, ntok, head;    // first token (row of q), tokens of the tile
+  int pos0;                // position of the first token
+  int lo, hi;              // keys the request's rows may see
+  int part;                // workspace part, -1: all of the tile's blocks
+  int pad[7];
+};
+static_assert(sizeof(Tile) == 64, "meta slot");
+
+// First block and number of blocks of tile t of a request (TT tokens a tile).
+__device__ __forceinline__ int tile_blocks(const PagedAttnParams& P, const Request& q, int t, int TT, int* first) {
+  const int p0 = q.pos0 + t * TT, p1 = q.pos0 + min(q.add, (t + 1) * TT);
+  const int hi = min(max(p1, 0), q.hi);
+  const int lo = p0 >= P.window ? min(p0 - P.window + 1, hi) : 0;
+  *first = lo / 128;
+  return max(1, (hi + 127) / 128 - lo / 128);
+}
+
+__device__ __forceinline__ void let_land() {
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 1000000ull) {
+  }
+}
+
+template <int HD, bool BF>
+__global__ void __launch_bounds__(PC_THREADS, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedAttnParams P,
+                       const __grid_constant__ PagedParts W) {
+  using C = ChunkCfg<HD>;
+  constexpr int ST = C::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::o_bar);
+  uint64_t* empty = full + ST;
+  uint64_t* qfull = empty + ST;
+  uint64_t* qempty = qfull + 1;
+  uint64_t* mfull = qempty + 1;
+  uint64_t* mempty = mfull + C::SLOTS;
+  uint64_t* sfull = mempty + C::SLOTS;   // S of half h complete
+  uint64_t* pfull = sfull + 2;           // P of half h written
+  uint64_t* ofull = pfull + 2;           // O of half h complete
+  volatile int* dead = reinterpret_cast<volatile int*>(ofull + 2);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(const_cast<int*>(dead) + 1);
+  Tile* meta = reinterpret_cast<Tile*>(smem + C::o_meta);
+  int* pre = reinterpret_cast<int*>(smem + C::o_pre);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int TS = 128 / P.rep, TT = 2 * TS;  // tokens of a half, of a tile
+
+  grid_launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    for (int s = 0; s < C::SLOTS; ++s) {
+      mbar_init(&mfull[s], 1);
+      mbar_init(&mempty[s], 9);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&sfull[h], 1);
+      mbar_init(&pfull[h], 4);
+      mbar_init(&ofull[h], 1);
+    }
+    *dead = 0;
+    W.desc[blockIdx.x].parts = 0;
+    fence_mbar_init();
+  }
+  // query rows that no token fills (128 % rep) stay zero
+  for (int i = tid; i < 2 * C::TILE / 16; i += PC_THREADS)
+    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  if (warp == PC_MMA) tmem_alloc(tslot, 512);
+
+  const int per = (P.n + PC_THREADS - 1) / PC_THREADS;
+  int mine = 0;
+  bool bad = false;
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    if (r >= P.n) break;
+    const Request q = read_request(P, r);
+    bad |= q.bad;
+    int u = 0;
+    if ((int64_t)q.add * P.rep > P.few_rows)
+      for (int t = 0; t * TT < q.add; ++t) {
+        int b0;
+        u += tile_blocks(P, q, t, TT, &b0);
+      }
+    u *= P.hkv;
+    pre[r] = u;
+    mine += u;
+  }
+  int T;
+  int* scan_tmp = reinterpret_cast<int*>(smem + C::o_kv);  // not loaded to yet
+  int at = block_scan<PC_THREADS / 32>(mine, scan_tmp, &T);
+  for (int i = 0; i < per; ++i) {
+    const int r = tid * per + i;
+    if (r >= P.n) break;
+    const int u = pre[r];
+    pre[r] = at;
+    at += u;
+  }
+  if (tid == 0) pre[P.n] = T;
+  if (bad && blockIdx.x == 0) latch(P.status, MK_ERR_BOUNDS);
+  fence_proxy_async_smem();  // the scan's words, before a load takes their place
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+
+  const int G = min((int)gridDim.x, T), c = blockIdx.x;
+  const int u0 = c < G ? (int)((int64_t)c * T / G) : 0, u1 = c < G ? (int)((int64_t)(c + 1) * T / G) : 0;
+
+  if (warp >= PC_LOAD) {
+    setmaxnreg_dec<PC_REGS_REST>();
+    if (warp == PC_LOAD) {
+      // ---------------------------------------------------------- loads
+      const int boxt = min(128, 1 << P.page_shift), nbox = 128 / boxt;
+      const int mask = (1 << P.page_shift) - 1;
+      int stage = 0, slot = 0;
+      uint32_t sphase = 1, mphase = 1, qphase = 1;
+      int r = u0 < u1 ? find_le(pre, P.n, u0) : 0, t = -1, head = 0;
+      bool up = true;
+      for (int u = u0; u < u1 && up;) {
+        while (pre[r + 1] <= u) {
+          ++r;
+          t = -1;
+        }
+        const Request q = read_request(P, r);
+        const int per_head = (pre[r + 1] - pre[r]) / P.hkv, ntile = (q.add + TT - 1) / TT;
+        int blk = 0, b0, nb;
+        if (t < 0) {  // find the tile of unit u
+          const int local = u - pre[r];
+          head = local / per_head;
+          int rem = local - head * per_head;
+          for (int base = 0;; base += 32) {
+            int f, k = 0;
+            if (base + lane < ntile) k = tile_blocks(P, q, base + lane, TT, &f);
+            int x = k;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(0xffffffffu, x, o);
+              if (lane >= o) x += y;
+            }
+            const uint32_t over = __ballot_sync(0xffffffffu, x > rem);
+            if (over || base + 32 >= ntile) {
+              const int l = over ? __ffs(over) - 1 : 31;
+              t = base + l;
+              blk = rem - __shfl_sync(0xffffffffu, x - k, l);
+              break;
+            }
+            rem -= __shfl_sync(0xffffffffu, x, 31);
+          }
+        }
+        nb = tile_blocks(P, q, t, TT, &b0);
+        const int nblk = min(nb - blk, u1 - u), ntok = min(TT, q.add - t * TT);
+        const bool whole = blk == 0 && nblk == nb;
+        if (blk == 0 && !whole && lane == 0) {
+          const int last = (int)(((int64_t)(u + nb) * G - 1) / T);  // CTA of the tile's last unit
+          PartDesc d;
+          d.row0 = q.row0 + t * TT; d.rows = ntok * P.rep; d.head = head; d.parts = last - c + 1;
+          W.desc[c] = d;
+        }
+        wait_phase(&mempty[slot], mphase, dead, P.status);
+        if (*dead) break;
+        if (lane == 0) {
+          Tile m;
+          m.key0 = (b0 + blk) * 128; m.nblk = nblk; m.row0 = q.row0 + t * TT; m.ntok = ntok; m.head = head;
+          m.pos0 = q.pos0 + t * TT; m.lo = q.lo; m.hi = q.hi;
+          m.part = whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
+          meta[slot] = m;
+          mbar_arrive(&mfull[slot]);
+        }
+        if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
+        const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
+        auto page_of = [&](int b) {  // of this lane's box; -1 where no row of the request sees any of it
+          const int key = b * 128 + lane * boxt;
+          if (lane >= nbox || key >= q.hi || key + boxt <= q.lo) return -1;
+          const int p = tab[key >> P.page_shift];
+          if (p >= 0 && p < P.n_pages) return p;
+          latch(P.status, MK_ERR_BOUNDS);
+          return -1;
+        };
+        auto load = [&](const CUtensorMap* tm, int b, int page) {
+          wait_phase(&empty[stage], sphase, dead, P.status);
+          if (*dead) return false;
+          if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::TILE);
+          __syncwarp();
+          if (lane < nbox) {
+            uint8_t* dst = smem + C::o_kv + stage * C::TILE + lane * boxt * 128;
+            const int tok = (b * 128 + lane * boxt) & mask;
+#pragma unroll
+            for (int x = 0; x < HD / 64; ++x)
+              tma_page(dst + x * 16384, tm, 64 * x, tok, head, page, &full[stage]);
+          }
+          if (++stage == ST) { stage = 0; sphase ^= 1; }
+          return true;
+        };
+        int page = page_of(b0 + blk);
+        for (int i = 0; i < nblk && up; ++i) {
+          const int b = b0 + blk + i;
+          const int next = i + 1 < nblk ? page_of(b + 1) : -1;
+          up = load(&tk, b, page);
+          if (up && i == 0) {
+            wait_phase(qempty, qphase, dead, P.status);
+            qphase ^= 1;
+            if (*dead) { up = false; break; }
+            const int halves = ntok > TS ? 2 : 1;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(qfull, halves * (HD / 64) * TS * P.rep * 128);
+              for (int h = 0; h < halves; ++h)
+                for (int x = 0; x < HD / 64; ++x)
+                  tma_rows(smem + h * C::TILE + x * 16384, &tq, 64 * x, head * P.rep,
+                           q.row0 + t * TT + h * TS, qfull);
+            }
+            __syncwarp();
+          }
+          if (up) up = load(&tv, b, page);
+          page = next;
+        }
+        u += nblk;
+        if (++t == ntile) {
+          t = 0;
+          ++head;
+        }
+      }
+      if (!*dead) wait_phase(&mempty[slot], mphase, dead, P.status);
+      if (*dead) {
+        let_land();
+      } else if (lane == 0) {
+        meta[slot].nblk = 0;
+        mbar_arrive(&mfull[slot]);
+      }
+    } else if (warp == PC_MMA) {
+      // ---------------------------------------------------------- products
+      if (lane == 0) {
+        constexpr uint32_t id_s = idesc_f16(128, 128, BF), id_o = idesc_f16(128, HD, BF, true);
+        uint32_t blkn = 0, pn[2] = {0, 0}, qn = 0;  // blocks loaded, P's and tiles seen
+        int slot = 0;
+        uint32_t mphase = 0;
+        const uint32_t q_s = smem_u32(smem), kv_s = smem_u32(smem + C::o_kv);
+        auto s_product = [&](int h, uint32_t kst) {
+          const uint32_t k0 = kv_s + kst * C::TILE, a0 = q_s + h * C::TILE;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
+            tc_mma(tbase + 128u * h, sdesc_sw128(a0 + off), sdesc_sw128(k0 + off), id_s, kk != 0);
+          }
+          tc_commit(&sfull[h]);
+        };
+        for (;;) {
+          wait_phase(&mfull[slot], mphase, dead, P.status);
+          if (*dead) break;
+          const int nblk = meta[slot].nblk, halves = meta[slot].ntok > TS ? 2 : 1;
+          mbar_arrive(&mempty[slot]);
+          if (nblk == 0) break;
+          if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
+          wait_phase(qfull, qn & 1, dead, P.status);
+          ++qn;
+          auto kst = [&](uint32_t b) { return (2 * b) % ST; };
+          auto kph = [&](uint32_t b) { return ((2 * b) / ST) & 1; };
+          wait_phase(&full[kst(blkn)], kph(blkn), dead, P.status);
+          tc_fence_after();
+          for (int h = 0; h < halves; ++h) s_product(h, kst(blkn));
+          tc_commit(&empty[kst(blkn)]);
+          if (nblk == 1) tc_commit(qempty);
+          for (int j = 0; j < nblk; ++j, ++blkn) {
+            const uint32_t vst = kst(blkn) + 1;
+            for (int h = 0; h < halves; ++h) {
+              wait_phase(&pfull[h], pn[h] & 1, dead, P.status);
+              ++pn[h];
+              if (h == 0) wait_phase(&full[vst], kph(blkn), dead, P.status);
+              if (*dead) break;
+              tc_fence_after();
+              const uint32_t v0 = kv_s + vst * C::TILE;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_ta(tbase + 256u + 128u * h, tbase + 128u * h + 8u * kk,
+                          sdesc_sw128_mn(v0 + 2048u * kk, 16384u), id_o, (j | kk) != 0);
+              if (h + 1 == halves) tc_commit(&empty[vst]);
+              if (j + 1 == nblk) tc_commit(&ofull[h]);
+              else {
+                const uint32_t b = blkn + 1;
+                if (h == 0) {
+                  wait_phase(&full[kst(b)], kph(b), dead, P.status);
+                  if (*dead) break;
+                  tc_fence_after();
+                }
+                s_product(h, kst(b));
+                if (h + 1 == halves) {
+                  tc_commit(&empty[kst(b)]);
+                  if (j + 2 == nblk) tc_commit(qempty);
+                }
+              }
+            }
+            if (*dead) break;
+          }
+          if (*dead) break;
+        }
+        if (*dead) let_land();
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    setmaxnreg_inc<PC_REGS_SOFT>();
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_t = tbase + 128u * half + lanes, o_t = tbase + 256u + 128u * half + lanes;
+    const int tok_in = row / P.rep, hq_in = row - tok_in * P.rep;
+    const float cs = fabsf(P.scale) * 1.4426950408889634f;
+    const bool neg = P.scale < 0.f;
+    uint32_t blkn = 0, sn = 0, on = 0;
+    int slot = 0;
+    uint32_t mphase = 0;
+    for (;;) {
+      wait_phase(&mfull[slot], mphase, dead, P.status);
+      if (*dead) break;
+      const Tile m = meta[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mempty[slot]);
+      if (m.nblk == 0) break;
+      if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
+      const int tok0 = half * TS;             // this half's first token of the tile
+      if (tok0 >= m.ntok) {
+        blkn += m.nblk;
+        continue;
+      }
+      const int ntok = min(TS, m.ntok - tok0);
+      const int pos0 = m.pos0 + tok0, pos = pos0 + min(tok_in, ntok - 1), end = pos0 + ntok - 1;
+      const int last = min(pos, m.hi - 1), first = pos >= P.window ? pos - P.window + 1 : 0;
+      // every row of the half sees the keys [all_lo, all_hi)
+      const int all_lo = end >= P.window ? end - P.window + 1 : 0, all_hi = min(pos0 + 1, m.hi);
+      float mx = -INFINITY, l = 0.f;
+      for (int j = 0; j < m.nblk; ++j, ++blkn) {
+        const int key0 = m.key0 + 128 * j;
+        wait_phase(&sfull[half], sn & 1, dead, P.status);
+        ++sn;
+        tc_fence_after();
+        float s[128];
+        tmem_ld128(s_t, s);
+        if (neg) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = -s[i];
+        }
+        if (key0 < all_lo || key0 + 128 > all_hi) {
+          const int c0 = first - key0, width = last + 1 - first;  // visible columns [c0, c0 + width)
+          const uint32_t w = width > 0 ? (uint32_t)width : 0u;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if ((uint32_t)(i - c0) >= w) s[i] = -INFINITY;
+        }
+        float t0 = max3(s[0], s[1], s[2]), t1 = max3(s[3], s[4], s[5]);
+#pragma unroll
+        for (int i = 6; i < 126; i += 4) {
+          t0 = max3(t0, s[i], s[i + 1]);
+          t1 = max3(t1, s[i + 2], s[i + 3]);
+        }
+        const float bm = max3(fmaxf(t0, t1), s[126], s[127]);
+        const float mn = fmaxf(mx, bm);
+        if (__any_sync(0xffffffffu, (mn - mx) * cs > 8.f)) {
+          const float a = mx == -INFINITY ? 0.f : ex2((mx - mn) * cs);
+          l *= a;
+          mx = mn;
+          if (j > 0) {
+#pragma unroll 1
+            for (int x = 0; x < HD; x += 32) {
+              float o[32];
+              tmem_ld32(o_t + x, o);
+              uint32_t w[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * a);
+              tmem_st32(o_t + x, w);
+            }
+          }
+        }
+        const float ref = mx == -INFINITY ? 0.f : mx * cs;
+        const u64 cs2 = pack_f32x2(cs, cs), ref2 = pack_f32x2(-ref, -ref);
+        u64 sum0 = 0, sum1 = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[32 / 2];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const u64 x = fma_f32x2(pack_f32x2(s[32 * q + 2 * i], s[32 * q + 2 * i + 1]), cs2, ref2);
+            const float p0 = ex2(__uint_as_float((uint32_t)x)), p1 = ex2(__uint_as_float((uint32_t)(x >> 32)));
+            if (i & 1) sum1 = add_f32x2(sum1, pack_f32x2(p0, p1));
+            else sum0 = add_f32x2(sum0, pack_f32x2(p0, p1));
+            pk[i] = down2<BF>(p0, p1);
+          }
+          tmem_st16(s_t + 16 * q, pk);
+        }
+        l += pair_sum(add_f32x2(sum0, sum1));
+        // values of keys that no row sees may be anything: the first half's
+        // group makes them zero before the block's first product with V
+        if (half == 0 && (key0 < m.lo || key0 + 128 > m.hi)) {
+          const uint32_t vst = (2 * blkn) % ST + 1;
+          wait_phase(&full[vst], ((2 * blkn) / ST) & 1, dead, P.status);
+          const int key = key0 + row;  // rows of 128 threads
+          if (key < m.lo || key >= m.hi) {
+            uint8_t* v = smem + C::o_kv + vst * C::TILE + row * 128;
+#pragma unroll
+            for (int x = 0; x < HD / 64; ++x)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(v + x * 16384 + 16 * i) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[half]);
+      }
+      wait_phase(&ofull[half], on & 1, dead, P.status);
+      ++on;
+      tc_fence_after();
+      const bool live = tok_in < ntok;
+      const float out_scale = m.part >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      const int tok = m.row0 + tok0 + tok_in, hq = m.head * P.rep + hq_in;
+      const int prow = tok0 * P.rep + row;
+      uint16_t* dst = P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD;
+      float* pdst = W.o + ((int64_t)max(m.part, 0) * W.rt + prow) * HD;
+#pragma unroll 1
+      for (int x = 0; x < HD; x += 32) {
+        float o[32];
+        tmem_ld32(o_t + x, o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= out_scale;
+        if (live) {
+          if (m.part < 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(dst + x + i) =
+                  make_uint4(down2<BF>(o[i], o[i + 1]), down2<BF>(o[i + 2], o[i + 3]),
+                             down2<BF>(o[i + 4], o[i + 5]), down2<BF>(o[i + 6], o[i + 7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(pdst + x + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+      }
+      tc_fence_before();  // the next tile's first P V is issued behind this group's next P
+      if (live) {
+        if (m.part >= 0)
+          W.ml[(int64_t)m.part * W.rt + prow] = make_float2(mx * cs, l);
+        else if (P.lse)
+          P.lse[(int64_t)tok * (P.hkv * P.rep) + hq] =
+              l > 0.f ? (mx * cs + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == PC_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+  // the join that follows waits for this launch alone, so this launch ends
+  // after the few-row kernel before it
+  grid_wait_prior();
+}
+
+template <int HD, bool BF>
+cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
+  CUtensorMap tq, tk, tv;
+  if (!make_page_tmap(&tk, kv.k, kv, HD, 128, BF) || !make_page_tmap(&tv, kv.v, kv, HD, 128, BF) ||
+      !make_rows_tmap(&tq, p.q, p.rows, p.hkv * p.rep, HD, p.q_stride, p.rep, 128 / p.rep, BF))
+    return cudaErrorInvalidValue;
+  // the register split needs the block to be launched with what it counts on
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, paged_chunk_kernel<HD, BF>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != PC_REGS) return cudaErrorInvalidKernelImage;
+  const int smem = ChunkCfg<HD>::total(p.n);
+  e = cudaFuncSetAttribute(paged_chunk_kernel<HD, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(w.ctas);
+  cfg.blockDim = dim3(PC_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<HD, BF>, tq, tk, tv, p, w);
+}
+
+}  // namespace
+
+cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
+                               bool bf, cudaStream_t st) {
+  if (d == 128) return bf ? launch<128, true>(p, kv, w, st) : launch<128, false>(p, kv, w, st);
+  return bf ? launch<64, true>(p, kv, w, st) : launch<64, false>(p, kv, w, st);
+}
+
+}  // namespace mk

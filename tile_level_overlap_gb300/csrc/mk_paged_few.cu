@@ -578,7 +578,7 @@ cudaError_t paged_join_launch(const PagedAttnParams& p, const PagedParts& a, con
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(a.ctas + b.ctas, 1);
+  cfg.gridDim = dim3(a.ctas + b.ctas, b.ctas ? 8 : 1);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cfg.attrs = &at;

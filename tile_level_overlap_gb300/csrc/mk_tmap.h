@@ -61,4 +61,21 @@ inline bool make_page_tmap(CUtensorMap* out, const void* base, const Kv& c, int 
   return r == CUDA_SUCCESS;
 }
 
+// Tensor map over query rows [rows][heads][d] (row_stride elements from row to
+// row), boxes of 64 elements x box_heads x box_rows with 128-byte swizzle.
+inline bool make_rows_tmap(CUtensorMap* out, const void* base, int rows, int heads, int d,
+                           int64_t row_stride, int box_heads, int box_rows, bool bf16) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)row_stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace mk
