@@ -51,7 +51,7 @@ struct PartDesc {
   int row0, rows, head, parts;
 };
 // Workspace of one kernel's divided rows: part 2 c (+ 1) is CTA c's first (second)
-// unfinished run of keys, o [part][rt][head_dim] unnormalised, ml [part][rt]
+// unfinished run of keys: o, rt rows x head_dim unnormalised, ml [part][rt]
 // maximum (base 2) and sum.
 struct PagedParts {
   PartDesc* desc;

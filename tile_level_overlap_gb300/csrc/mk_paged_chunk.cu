@@ -30,6 +30,10 @@ constexpr int PC_THREADS = 384;
 constexpr int PC_LOAD = 8, PC_MMA = 9;       // warps; 0-3 and 4-7 own the halves
 constexpr int PC_REGS = 168, PC_REGS_SOFT = 216, PC_REGS_REST = 72;
 static_assert(2 * PC_REGS_SOFT + PC_REGS_REST == 3 * PC_REGS, "registers of the three warpgroups");
+// What a tile costs beside its blocks (filling the pipeline, writing the rows),
+// in blocks: without it the SMs with the short tiles of a prompt's start ended
+// a quarter later than the others.
+constexpr int PC_OVER = 2;
 
 template <int HD>
 struct ChunkCfg {
@@ -66,6 +70,18 @@ __device__ __forceinline__ int tile_blocks(const PagedAttnParams& P, const Reque
 __device__ __forceinline__ void let_land() {
   const uint64_t t0 = globaltimer();
   while (globaltimer() - t0 < 1000000ull) {
+  }
+}
+
+// Lanes l and l ^ D exchange: the lower one's b for the upper one's a.
+template <int D>
+__device__ __forceinline__ void quad_swap(uint32_t (&a)[4], uint32_t (&b)[4], int lane) {
+  const bool up = lane & D;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a[i] : b[i], D);
+    if (up) a[i] = got;
+    else b[i] = got;
   }
 }
 
@@ -120,22 +136,37 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   fence_proxy_async_smem();
   if (warp == PC_MMA) tmem_alloc(tslot, 512);
 
+  // units: the tiles' blocks and overheads.  A thread counts its requests'
+  // tiles; a warp together those of a request with many.
   const int per = (P.n + PC_THREADS - 1) / PC_THREADS;
   int mine = 0;
   bool bad = false;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
-    if (r >= P.n) break;
-    const Request q = read_request(P, r);
-    bad |= q.bad;
-    int u = 0;
-    if ((int64_t)q.add * P.rep > P.few_rows)
-      for (int t = 0; t * TT < q.add; ++t) {
-        int b0;
-        u += tile_blocks(P, q, t, TT, &b0);
-      }
-    u *= P.hkv;
-    pre[r] = u;
+    int u = 0, ntile = 0, b0;
+    Request q{};
+    if (r < P.n) {
+      q = read_request(P, r);
+      bad |= q.bad;
+      if ((int64_t)q.add * P.rep > P.few_rows) ntile = (q.add + TT - 1) / TT;
+    }
+    if (ntile <= 8)
+      for (int t = 0; t < ntile; ++t) u += tile_blocks(P, q, t, TT, &b0);
+    for (uint32_t many = __ballot_sync(0xffffffffu, ntile > 8); many; many &= many - 1) {
+      const int from = __ffs(many) - 1;
+      Request x{};
+      x.add = __shfl_sync(0xffffffffu, q.add, from);
+      x.pos0 = __shfl_sync(0xffffffffu, q.pos0, from);
+      x.hi = __shfl_sync(0xffffffffu, q.hi, from);
+      const int nt = __shfl_sync(0xffffffffu, ntile, from);
+      int v = 0;
+      for (int t = lane; t < nt; t += 32) v += tile_blocks(P, x, t, TT, &b0);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == from) u = v;
+    }
+    u = (u + PC_OVER * ntile) * P.hkv;
+    if (r < P.n) pre[r] = u;
     mine += u;
   }
   int T;
@@ -154,7 +185,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *tslot;
+  // every column is this CTA's: the allocation starts at column 0
+  constexpr uint32_t T_S = 0, T_O = 256;
 
   const int G = min((int)gridDim.x, T), c = blockIdx.x;
   const int u0 = c < G ? (int)((int64_t)c * T / G) : 0, u1 = c < G ? (int)((int64_t)(c + 1) * T / G) : 0;
@@ -176,14 +208,14 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         }
         const Request q = read_request(P, r);
         const int per_head = (pre[r + 1] - pre[r]) / P.hkv, ntile = (q.add + TT - 1) / TT;
-        int blk = 0, b0, nb;
+        int x0 = 0, b0;  // first unit of the tile in this run
         if (t < 0) {  // find the tile of unit u
           const int local = u - pre[r];
           head = local / per_head;
           int rem = local - head * per_head;
           for (int base = 0;; base += 32) {
             int f, k = 0;
-            if (base + lane < ntile) k = tile_blocks(P, q, base + lane, TT, &f);
+            if (base + lane < ntile) k = tile_blocks(P, q, base + lane, TT, &f) + PC_OVER;
             int x = k;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -194,17 +226,20 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             if (over || base + 32 >= ntile) {
               const int l = over ? __ffs(over) - 1 : 31;
               t = base + l;
-              blk = rem - __shfl_sync(0xffffffffu, x - k, l);
+              x0 = rem - __shfl_sync(0xffffffffu, x - k, l);
               break;
             }
             rem -= __shfl_sync(0xffffffffu, x, 31);
           }
         }
-        nb = tile_blocks(P, q, t, TT, &b0);
-        const int nblk = min(nb - blk, u1 - u), ntok = min(TT, q.add - t * TT);
+        // units [x0, x1) of the tile: blocks [blk, blk + nblk)
+        const int nb = tile_blocks(P, q, t, TT, &b0), x1 = min(nb + PC_OVER, x0 + u1 - u);
+        const int blk = max(0, x0 - PC_OVER), nblk = max(0, x1 - PC_OVER) - blk;
+        const int ntok = min(TT, q.add - t * TT), end = u - x0 + nb + PC_OVER;
+        if (nblk == 0) break;  // the run ends with the tile's overhead: the next CTA has it all
         const bool whole = blk == 0 && nblk == nb;
         if (blk == 0 && !whole && lane == 0) {
-          const int last = (int)(((int64_t)(u + nb) * G - 1) / T);  // CTA of the tile's last unit
+          const int last = (int)(((int64_t)end * G - 1) / T);  // CTA of the tile's last unit
           PartDesc d;
           d.row0 = q.row0 + t * TT; d.rows = ntok * P.rep; d.head = head; d.parts = last - c + 1;
           W.desc[c] = d;
@@ -266,7 +301,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           if (up) up = load(&tv, b, page);
           page = next;
         }
-        u += nblk;
+        u += x1 - x0;
         if (++t == ntile) {
           t = 0;
           ++head;
@@ -281,72 +316,79 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       }
     } else if (warp == PC_MMA) {
       // ---------------------------------------------------------- products
-      if (lane == 0) {
-        constexpr uint32_t id_s = idesc_f16(128, 128, BF), id_o = idesc_f16(128, HD, BF, true);
-        uint32_t blkn = 0, pn[2] = {0, 0}, qn = 0;  // blocks loaded, P's and tiles seen
-        int slot = 0;
-        uint32_t mphase = 0;
-        const uint32_t q_s = smem_u32(smem), kv_s = smem_u32(smem + C::o_kv);
-        auto s_product = [&](int h, uint32_t kst) {
-          const uint32_t k0 = kv_s + kst * C::TILE, a0 = q_s + h * C::TILE;
+      // The whole warp walks the run (addresses and descriptors stay in uniform
+      // registers); one elected thread issues.
+      constexpr uint32_t id_s = idesc_f16(128, 128, BF), id_o = idesc_f16(128, HD, BF, true);
+      const uint64_t dq = sdesc_sw128(smem_u32(smem)), dk = sdesc_sw128(smem_u32(smem + C::o_kv));
+      const uint64_t dv = sdesc_sw128_mn(smem_u32(smem + C::o_kv), 16384u);
+      uint32_t blkn = 0, pn[2] = {0, 0}, qn = 0;  // blocks loaded, P's and tiles seen
+      int slot = 0;
+      uint32_t mphase = 0;
+      auto kst = [](uint32_t b) { return (2 * b) % ST; };
+      auto kph = [](uint32_t b) { return ((2 * b) / ST) & 1; };
+      // S of half h from the K block in stage st
+      auto s_product = [&](int h, uint32_t st) {
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
-            tc_mma(tbase + 128u * h, sdesc_sw128(a0 + off), sdesc_sw128(k0 + off), id_s, kk != 0);
-          }
-          tc_commit(&sfull[h]);
-        };
-        for (;;) {
-          wait_phase(&mfull[slot], mphase, dead, P.status);
-          if (*dead) break;
-          const int nblk = meta[slot].nblk, halves = meta[slot].ntok > TS ? 2 : 1;
-          mbar_arrive(&mempty[slot]);
-          if (nblk == 0) break;
-          if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
-          wait_phase(qfull, qn & 1, dead, P.status);
-          ++qn;
-          auto kst = [&](uint32_t b) { return (2 * b) % ST; };
-          auto kph = [&](uint32_t b) { return ((2 * b) / ST) & 1; };
-          wait_phase(&full[kst(blkn)], kph(blkn), dead, P.status);
-          tc_fence_after();
-          for (int h = 0; h < halves; ++h) s_product(h, kst(blkn));
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint32_t off = ((uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u) >> 4;
+          tc_mma(T_S + 128u * h, dq + (h * C::TILE / 16 + off), dk + (st * (C::TILE / 16) + off), id_s, kk != 0);
+        }
+        tc_commit(&sfull[h]);
+      };
+      for (;;) {
+        wait_phase(&mfull[slot], mphase, dead, P.status);
+        if (*dead) break;
+        const int nblk = meta[slot].nblk, halves = meta[slot].ntok > TS ? 2 : 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mempty[slot]);
+        if (nblk == 0) break;
+        if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
+        wait_phase(qfull, qn & 1, dead, P.status);
+        ++qn;
+        wait_phase(&full[kst(blkn)], kph(blkn), dead, P.status);
+        tc_fence_after();
+        if (elect_one()) {
+          s_product(0, kst(blkn));
+          if (halves == 2) s_product(1, kst(blkn));
           tc_commit(&empty[kst(blkn)]);
           if (nblk == 1) tc_commit(qempty);
-          for (int j = 0; j < nblk; ++j, ++blkn) {
-            const uint32_t vst = kst(blkn) + 1;
-            for (int h = 0; h < halves; ++h) {
-              wait_phase(&pfull[h], pn[h] & 1, dead, P.status);
-              ++pn[h];
-              if (h == 0) wait_phase(&full[vst], kph(blkn), dead, P.status);
-              if (*dead) break;
-              tc_fence_after();
-              const uint32_t v0 = kv_s + vst * C::TILE;
+        }
+        for (int j = 0; j < nblk; ++j, ++blkn) {
+          const uint32_t vst = kst(blkn) + 1, nst = kst(blkn + 1);
+          const bool more = j + 1 < nblk;
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_ta(tbase + 256u + 128u * h, tbase + 128u * h + 8u * kk,
-                          sdesc_sw128_mn(v0 + 2048u * kk, 16384u), id_o, (j | kk) != 0);
-              if (h + 1 == halves) tc_commit(&empty[vst]);
-              if (j + 1 == nblk) tc_commit(&ofull[h]);
-              else {
-                const uint32_t b = blkn + 1;
-                if (h == 0) {
-                  wait_phase(&full[kst(b)], kph(b), dead, P.status);
-                  if (*dead) break;
-                  tc_fence_after();
-                }
-                s_product(h, kst(b));
-                if (h + 1 == halves) {
-                  tc_commit(&empty[kst(b)]);
-                  if (j + 2 == nblk) tc_commit(qempty);
-                }
-              }
+          for (int h = 0; h < 2; ++h) {
+            if (h == halves) break;
+            wait_phase(&pfull[h], pn[h] & 1, dead, P.status);
+            ++pn[h];
+            if (h == 0) {
+              wait_phase(&full[vst], kph(blkn), dead, P.status);
+              if (more) wait_phase(&full[nst], kph(blkn + 1), dead, P.status);
             }
             if (*dead) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_ta(T_O + 128u * h, T_S + 128u * h + 8u * kk, dv + (vst * (C::TILE / 16) + 128u * kk), id_o,
+                          (j | kk) != 0);
+              if (h + 1 == halves) tc_commit(&empty[vst]);
+              if (more) {
+                s_product(h, nst);
+                if (h + 1 == halves) {
+                  tc_commit(&empty[nst]);
+                  if (j + 2 == nblk) tc_commit(qempty);
+                }
+              } else {
+                tc_commit(&ofull[h]);
+              }
+            }
           }
           if (*dead) break;
         }
-        if (*dead) let_land();
+        if (*dead) break;
       }
+      if (*dead) let_land();
       __syncwarp();
     }
   } else {
@@ -354,7 +396,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     setmaxnreg_inc<PC_REGS_SOFT>();
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_t = tbase + 128u * half + lanes, o_t = tbase + 256u + 128u * half + lanes;
+    const uint32_t s_t = T_S + 128u * half + lanes, o_t = T_O + 128u * half + lanes;
     const int tok_in = row / P.rep, hq_in = row - tok_in * P.rep;
     const float cs = fabsf(P.scale) * 1.4426950408889634f;
     const bool neg = P.scale < 0.f;
@@ -464,46 +506,62 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       ++on;
       tc_fence_after();
       const bool live = tok_in < ntok;
-      const float out_scale = m.part >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
-      const int tok = m.row0 + tok0 + tok_in, hq = m.head * P.rep + hq_in;
       const int prow = tok0 * P.rep + row;
-      uint16_t* dst = P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD;
-      float* pdst = W.o + ((int64_t)max(m.part, 0) * W.rt + prow) * HD;
+      if (m.part < 0) {
+        // Four lanes exchange 16-byte pieces so that a store writes 64
+        // contiguous bytes of a row: lane 4 a + b then has piece b of the rows
+        // 4 a + i (16 scattered bytes a lane took three times as long).
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint16_t* dst[4];
+        bool put[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rw = (row & ~3) + i, tk = rw / P.rep;
+          put[i] = tk < ntok;
+          dst[i] = P.out + (int64_t)(m.row0 + tok0 + tk) * P.o_stride +
+                   (int64_t)(m.head * P.rep + rw - tk * P.rep) * HD + (lane & 3) * 8;
+        }
 #pragma unroll 1
-      for (int x = 0; x < HD; x += 32) {
-        float o[32];
-        tmem_ld32(o_t + x, o);
+        for (int x = 0; x < HD; x += 32) {
+          float o[32];
+          tmem_ld32(o_t + x, o);
+          uint32_t c[4][4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= out_scale;
-        if (live) {
-          if (m.part < 0) {
+          for (int i = 0; i < 16; ++i) c[i >> 2][i & 3] = down2<BF>(o[2 * i] * inv, o[2 * i + 1] * inv);
+          quad_swap<1>(c[0], c[1], lane);
+          quad_swap<1>(c[2], c[3], lane);
+          quad_swap<2>(c[0], c[2], lane);
+          quad_swap<2>(c[1], c[3], lane);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(dst + x + i) =
-                  make_uint4(down2<BF>(o[i], o[i + 1]), down2<BF>(o[i + 2], o[i + 3]),
-                             down2<BF>(o[i + 4], o[i + 5]), down2<BF>(o[i + 6], o[i + 7]));
-          } else {
+          for (int i = 0; i < 4; ++i)
+            if (put[i]) *reinterpret_cast<uint4*>(dst[i] + x) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+        }
+        if (live && P.lse)
+          P.lse[(int64_t)(m.row0 + tok0 + tok_in) * (P.hkv * P.rep) + m.head * P.rep + hq_in] =
+              l > 0.f ? (mx * cs + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        // a part: [4 columns][row], a warp's lanes end to end
+        float* dst = W.o + (int64_t)m.part * W.rt * HD + prow * 4;
+#pragma unroll 1
+        for (int x = 0; x < HD; x += 32) {
+          float o[32];
+          tmem_ld32(o_t + x, o);
+          if (live) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(pdst + x + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              *reinterpret_cast<float4*>(dst + (x + i) * W.rt) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
+        if (live) W.ml[(int64_t)m.part * W.rt + prow] = make_float2(mx * cs, l);
       }
       tc_fence_before();  // the next tile's first P V is issued behind this group's next P
-      if (live) {
-        if (m.part >= 0)
-          W.ml[(int64_t)m.part * W.rt + prow] = make_float2(mx * cs, l);
-        else if (P.lse)
-          P.lse[(int64_t)tok * (P.hkv * P.rep) + hq] =
-              l > 0.f ? (mx * cs + log2f(l)) * 0.6931471805599453f : -INFINITY;
-      }
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == PC_MMA) {
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc(*tslot, 512);
   }
   // the join that follows waits for this launch alone, so this launch ends
   // after the few-row kernel before it

@@ -73,21 +73,23 @@ __device__ __forceinline__ void grid_wait_prior() {
 }
 
 // ---------------------------------------------------------------- bounded waits
-// Wait for the phase; after two seconds give up: `*dead` is raised, the status
-// latched, and every later wait of the CTA returns at once.
-static __device__ __noinline__ void wait_gave_up(volatile int* dead, int32_t* status) {
-  *dead = 1;
-  latch(status, MK_ERR_TIMEOUT);
-}
+// Wait for the phase.  After WAIT_TRIES tries (each suspends the thread for a
+// while; tens of milliseconds at the very least, and no wait here depends on
+// another CTA) give up: `*dead` is raised, the status latched, and every later
+// wait of the CTA returns soon.  Tries are counted, not time: reading a timer
+// between two tries costs as much as the waits themselves.
+constexpr uint32_t WAIT_TRIES = 1u << 23;
 __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, volatile int* dead,
                                            int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = globaltimer();
+  uint32_t tries = 0;
   while (!mbar_try_wait(bar, parity)) {
-    if (*dead) return;
-    if (globaltimer() - t0 > 2000000000ull) {
-      wait_gave_up(dead, status);
-      return;
+    if ((++tries & 1023u) == 0) {
+      if (*dead) return;
+      if (tries >= WAIT_TRIES) {
+        *dead = 1;
+        latch(status, MK_ERR_TIMEOUT);
+        return;
+      }
     }
   }
 }

@@ -29,6 +29,7 @@ namespace {
 constexpr int PF_WARPS = 8;             // consumers
 constexpr int PF_THREADS = 32 * (PF_WARPS + 1);
 constexpr int PF_STAGE = 32768;         // one block's keys, then its values
+constexpr int PF_OVER = 1;              // what a pair costs beside its blocks, in blocks
 
 template <int HD, int NT>
 struct FewCfg {
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     bad |= q.bad;
     int u = 0;
     if (q.add > 0 && (int64_t)q.add * P.rep <= P.few_rows)
-      u = P.hkv * max(1, (q.hi + KS - 1) / KS - q.lo / KS);
+      u = P.hkv * (max(1, (q.hi + KS - 1) / KS - q.lo / KS) + PF_OVER);
     pre[r] = u;
     mine += u;
   }
@@ -197,12 +198,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     for (int u = u0; u < u1;) {
       while (pre[r + 1] <= u) ++r;
       const Request q = read_request(P, r);
-      const int nb = (pre[r + 1] - pre[r]) / P.hkv, local = u - pre[r];
-      const int head = local / nb, blk = local - head * nb, nblk = min(nb - blk, u1 - u);
+      // units [x0, x1) of the pair: blocks [blk, blk + nblk)
+      const int units = (pre[r + 1] - pre[r]) / P.hkv, local = u - pre[r], nb = units - PF_OVER;
+      const int head = local / units, x0 = local - head * units, x1 = min(units, x0 + u1 - u);
+      const int blk = max(0, x0 - PF_OVER), nblk = max(0, x1 - PF_OVER) - blk;
+      if (nblk == 0) break;  // the run ends with the pair's overhead: the next CTA has it all
       const int b0 = q.lo / KS + blk, rows = q.add * P.rep;
       const bool whole = blk == 0 && nblk == nb;
       if (blk == 0 && !whole) {  // joined by this CTA's block of the second launch
-        const int last = (int)(((int64_t)(u + nb) * G - 1) / T);  // CTA of the pair's last unit
+        const int last = (int)(((int64_t)(u - x0 + units) * G - 1) / T);  // CTA of the pair's last unit
         if (lane == 0) {
           PartDesc d;
           d.row0 = q.row0; d.rows = rows; d.head = head; d.parts = last - c + 1;
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (++stage == C::STAGES) { stage = 0; sphase ^= 1; }
         page = next;
       }
-      u += nblk;
+      u += x1 - x0;
     }
     // the end of the run
     wait_phase(&qempty[slot], qphase, dead, P.status);
@@ -504,42 +508,81 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 }
 
 // ---------------------------------------------------------------- join
-// Block c joins the parts of the pair that CTA c of the first launch left open:
-// its own second part and the first parts of the CTAs after it, in that order.
+// The parts of the pair (tile) that CTA c of a kernel left open, in the order
+// of their keys: its own second part and the first parts of the CTAs after it.
+// The few-row kernel's parts are [row][dimension], a block joins 8 (16) rows at
+// a time; the tile kernel's are [4 dimensions][row], a block joins 32 rows.
+struct Joined {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float2 ml, float4 v) {
+    const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+    const float a = ex2(m - ref), f = ex2(ml.x - ref);
+    l = l * a + ml.y * f;
+    o.x = o.x * a + v.x * f; o.y = o.y * a + v.y * f;
+    o.z = o.z * a + v.z * f; o.w = o.w * a + v.w * f;
+    m = mn;
+  }
+  template <bool BF>
+  __device__ __forceinline__ uint2 out() const {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    return make_uint2(down2<BF>(o.x * inv, o.y * inv), down2<BF>(o.z * inv, o.w * inv));
+  }
+  __device__ __forceinline__ float lse() const {
+    return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  }
+};
+
+constexpr int JOIN_ROWS = 32;  // of a tile, a block
+
 template <int HD, bool BF>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams P,
                                                          const __grid_constant__ PagedParts A,
                                                          const __grid_constant__ PagedParts B) {
+  constexpr int LPR = HD / 4;  // threads of a row
+  __shared__ uint2 rows_out[JOIN_ROWS][LPR + 1];
   grid_wait_prior();
-  const bool first = (int)blockIdx.x < A.ctas;
-  const PagedParts& W = first ? A : B;
-  const int c = first ? blockIdx.x : blockIdx.x - A.ctas;
-  const PartDesc d = W.desc[c];
-  if (d.parts == 0) return;
-  constexpr int LPR = HD / 4;
-  const int d4 = (threadIdx.x % LPR) * 4;
-  for (int row = blockIdx.y * (256 / LPR) + threadIdx.x / LPR; row < d.rows; row += gridDim.y * (256 / LPR)) {
-    float mm = -INFINITY, ll = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int tid = threadIdx.x, hqs = P.hkv * P.rep;
+  if ((int)blockIdx.x < A.ctas) {
+    const int c = blockIdx.x;
+    const PartDesc d = A.desc[c];
+    if (d.parts == 0) return;
+    const int d4 = (tid % LPR) * 4;
+    for (int row = tid / LPR; row < d.rows; row += 256 / LPR) {
+      Joined j;
+#pragma unroll 4
+      for (int k = 0; k < d.parts; ++k) {
+        const int64_t at = (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * A.rt + row;
+        j.add(A.ml[at], *reinterpret_cast<const float4*>(A.o + at * HD + d4));
+      }
+      const int tok = d.row0 + row / P.rep, hq = d.head * P.rep + row % P.rep;
+      *reinterpret_cast<uint2*>(P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD + d4) = j.out<BF>();
+      if (P.lse && d4 == 0) P.lse[(int64_t)tok * hqs + hq] = j.lse();
+    }
+    return;
+  }
+  const int per = B.rt / JOIN_ROWS, c = (blockIdx.x - A.ctas) / per;
+  const int row0 = ((blockIdx.x - A.ctas) % per) * JOIN_ROWS, lane = tid & 31, row = row0 + lane;
+  const PartDesc d = B.desc[c];
+  if (d.parts == 0 || row0 >= d.rows) return;
+#pragma unroll 1
+  for (int q = tid >> 5; q < LPR; q += 8) {  // four dimensions a warp, lanes on rows
+    Joined j;
 #pragma unroll 4
     for (int k = 0; k < d.parts; ++k) {
-      const int64_t at = (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * W.rt + row;
-      const float2 ml = W.ml[at];
-      const float4 v = *reinterpret_cast<const float4*>(W.o + at * HD + d4);
-      const float mn = fmaxf(mm, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-      const float a = ex2(mm - ref), f = ex2(ml.x - ref);
-      ll = ll * a + ml.y * f;
-      acc.x = acc.x * a + v.x * f; acc.y = acc.y * a + v.y * f;
-      acc.z = acc.z * a + v.z * f; acc.w = acc.w * a + v.w * f;
-      mm = mn;
+      const int64_t part = k == 0 ? 2 * c + 1 : 2 * (c + k);
+      j.add(B.ml[part * B.rt + row], *reinterpret_cast<const float4*>(B.o + part * B.rt * HD + (q * B.rt + row) * 4));
     }
-    const int tok = d.row0 + row / P.rep, hq = d.head * P.rep + row % P.rep;
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
-    *reinterpret_cast<uint2*>(P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD + d4) =
-        make_uint2(down2<BF>(acc.x * inv, acc.y * inv), down2<BF>(acc.z * inv, acc.w * inv));
-    if (P.lse && d4 == 0)
-      P.lse[(int64_t)tok * (P.hkv * P.rep) + hq] =
-          ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    rows_out[lane][q] = j.out<BF>();
+    if (q == 0 && P.lse && row < d.rows)
+      P.lse[(int64_t)(d.row0 + row / P.rep) * hqs + d.head * P.rep + row % P.rep] = j.lse();
+  }
+  __syncthreads();
+  for (int i = tid; i < JOIN_ROWS * LPR; i += 256) {
+    const int rw = row0 + i / LPR, q = i % LPR;
+    if (rw >= d.rows) break;
+    *reinterpret_cast<uint2*>(P.out + (int64_t)(d.row0 + rw / P.rep) * P.o_stride +
+                              (int64_t)(d.head * P.rep + rw % P.rep) * HD + q * 4) = rows_out[i / LPR][q];
   }
 }
 
@@ -578,7 +621,7 @@ cudaError_t paged_join_launch(const PagedAttnParams& p, const PagedParts& a, con
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(a.ctas + b.ctas, b.ctas ? 8 : 1);
+  cfg.gridDim = dim3(a.ctas + b.ctas * (b.rt / JOIN_ROWS));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cfg.attrs = &at;

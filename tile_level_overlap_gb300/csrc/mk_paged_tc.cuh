@@ -75,6 +75,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      :
+      : "memory");
+  return r != 0;
+}
+
 // Instruction descriptor of tcgen05.mma.kind::f16 for bf16 or fp16 operands.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b_mn = false) {
   return bf16 ? idesc_bf16_f32(M, N, b_mn) : idesc_bf16_f32(M, N, b_mn) & ~((1u << 7) | (1u << 10));
