@@ -19,17 +19,20 @@ constexpr int PT_THREADS = 512;
 constexpr int PT_PER_THREAD = MK_PAGED_MAX_REQUESTS / PT_THREADS;
 
 struct PtSmem {
-  int cu[MK_PAGED_MAX_REQUESTS + 1];    // first row of each request (clamped to max_tokens)
-  int upto[MK_PAGED_MAX_REQUESTS + 1];  // pages needed by the requests before
-  int ctx[MK_PAGED_MAX_REQUESTS];       // cached tokens; -1 - ctx: refused
   long long wrow[PT_THREADS / 32];
   int wpage[PT_THREADS / 32];
-  int taken;
+  int taken, pad;
+  // then cu [n + 1]: first row of each request (clamped to max_tokens); upto
+  // [n + 1]: pages needed by the requests before; ctx [n]: cached tokens, -1: refused
+  static size_t bytes(int n) { return sizeof(PtSmem) + 4 * (3 * (size_t)n + 2); }
 };
 
 __global__ void __launch_bounds__(PT_THREADS) paged_tables_kernel(const PagedTablesParams P) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   PtSmem& S = *reinterpret_cast<PtSmem*>(smem_raw);
+  int* s_cu = reinterpret_cast<int*>(&S + 1);
+  int* s_upto = s_cu + P.n + 1;
+  int* s_ctx = s_upto + P.n + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int page_mask = (1 << P.page_shift) - 1;
   const int free_raw = *P.n_free;
@@ -95,13 +98,13 @@ __global__ void __launch_bounds__(PT_THREADS) paged_tables_kernel(const PagedTab
         served = false;
         bad = true;
       }
-      S.cu[r] = (int)min(row0, (long long)P.max_tokens);
-      S.upto[r] = page0;
-      S.ctx[r] = served ? ctx[i] : -1;
+      s_cu[r] = (int)min(row0, (long long)P.max_tokens);
+      s_upto[r] = page0;
+      s_ctx[r] = served ? ctx[i] : -1;
       if (served && need[i] > 0) served_upto = max(served_upto, page1);
       if (r == P.n - 1) {
-        S.cu[P.n] = (int)min(row1, (long long)P.max_tokens);
-        S.upto[P.n] = page1;
+        s_cu[P.n] = (int)min(row1, (long long)P.max_tokens);
+        s_upto[P.n] = page1;
       }
       if (blockIdx.x == 0) {
         P.cu[r + 1] = (int)min(row1, (long long)P.max_tokens);
@@ -121,23 +124,23 @@ __global__ void __launch_bounds__(PT_THREADS) paged_tables_kernel(const PagedTab
   }
   const int gtid = blockIdx.x * PT_THREADS + tid, gsize = gridDim.x * PT_THREADS;
   for (int p = gtid; p < taken; p += gsize) {
-    const int r = find_le(S.upto, P.n, p);
-    if (S.ctx[r] < 0) continue;  // before the last served one every request that needs pages is served
-    const int held = (int)(((long long)S.ctx[r] + page_mask) >> P.page_shift);
-    P.table[(int64_t)r * P.max_blocks + held + (p - S.upto[r])] = P.free_pages[n_free - 1 - p];
+    const int r = find_le(s_upto, P.n, p);
+    if (s_ctx[r] < 0) continue;  // before the last served one every request that needs pages is served
+    const int held = (int)(((long long)s_ctx[r] + page_mask) >> P.page_shift);
+    P.table[(int64_t)r * P.max_blocks + held + (p - s_upto[r])] = P.free_pages[n_free - 1 - p];
   }
-  const int total = S.cu[P.n];
+  const int total = s_cu[P.n];
   for (int t = gtid; t < P.max_tokens; t += gsize) {
     int pos = 0, slot = -1;
     if (t < total) {
-      const int r = find_le(S.cu, P.n, t);
-      const int c = S.ctx[r];
+      const int r = find_le(s_cu, P.n, t);
+      const int c = s_ctx[r];
       if (c >= 0) {
-        pos = c + (t - S.cu[r]);
+        pos = c + (t - s_cu[r]);
         const int blk = pos >> P.page_shift;
         const int held = (int)(((long long)c + page_mask) >> P.page_shift);
         const int page = blk < held ? P.table[(int64_t)r * P.max_blocks + blk]
-                                    : P.free_pages[n_free - 1 - (S.upto[r] + blk - held)];
+                                    : P.free_pages[n_free - 1 - (s_upto[r] + blk - held)];
         // a page that no cache has gives the slot that append refuses
         const long long at = ((long long)page << P.page_shift) | (pos & page_mask);
         slot = at >= 0 && at < 0x7fffffffll ? (int)at : 0x7fffffff;
@@ -252,6 +255,7 @@ cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool 
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  p.device = dev;
   // The few-row kernel has the rows of the longest request where it takes them
   // all, else those of a single token (its products cost by the row).
   const int64_t most = (int64_t)p.max_new * p.rep;
@@ -317,6 +321,18 @@ int check_batch(const mk_paged_batch* b) {
 }
 
 }  // namespace
+
+cudaError_t paged_prepare(const void* kernel, int smem, int regs, int device, std::atomic<uint64_t>* done) {
+  const uint64_t bit = 1ull << (device & 63);
+  if (device < 64 && (done->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess && regs && fa.numRegs != regs) e = cudaErrorInvalidKernelImage;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 }  // namespace mk
 
 using namespace mk;
@@ -339,13 +355,14 @@ extern "C" int mk_paged_tables(const mk_paged_batch* b, const int32_t* ctx_lens,
   p.slot = b->slots; p.n_left = n_left; p.status = status;
   p.n = b->n; p.max_blocks = b->max_blocks; p.max_tokens = b->max_tokens;
   p.free_cap = free_capacity; p.page_shift = log2_page(b->page_size);
-  if (cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sizeof(PtSmem)) != cudaSuccess) {
+  const size_t smem = PtSmem::bytes(b->n);
+  if (smem > 49152 && cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return MK_ERR_CUDA;
   }
   const int grid = min(152, max(1, (b->max_tokens + 2 * PT_THREADS - 1) / (2 * PT_THREADS)));
-  paged_tables_kernel<<<grid, PT_THREADS, sizeof(PtSmem), (cudaStream_t)stream>>>(p);
+  paged_tables_kernel<<<grid, PT_THREADS, smem, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 

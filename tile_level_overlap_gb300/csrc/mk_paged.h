@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/mk.h"
 
 namespace mk {
@@ -34,6 +36,7 @@ struct PagedAttnParams {
   int64_t q_stride, o_stride;
   int n, max_blocks, rows, max_new, n_pages, page_shift;
   int hkv, rep, window;  // window 0x7fffffff: none
+  int device;
   int few_rows;  // requests of at most this many rows (new tokens x rep) go to the few-row kernel
   float scale;
 };
@@ -59,6 +62,11 @@ struct PagedParts {
   float* o;
   int rt, ctas;
 };
+
+// Opt a kernel into `smem` bytes of shared memory, once per device (the limit
+// is set to the largest a call can ask for).  `regs`: what the kernel has to be
+// compiled to, 0: any.  `done` is the kernel's own word, a bit per device.
+cudaError_t paged_prepare(const void* kernel, int smem, int regs, int device, std::atomic<uint64_t>* done);
 
 cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
                              bool bf, cudaStream_t st);

@@ -575,12 +575,9 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
       !make_rows_tmap(&tq, p.q, p.rows, p.hkv * p.rep, HD, p.q_stride, p.rep, 128 / p.rep, BF))
     return cudaErrorInvalidValue;
   // the register split needs the block to be launched with what it counts on
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, paged_chunk_kernel<HD, BF>);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != PC_REGS) return cudaErrorInvalidKernelImage;
-  const int smem = ChunkCfg<HD>::total(p.n);
-  e = cudaFuncSetAttribute(paged_chunk_kernel<HD, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF>,
+                                      ChunkCfg<HD>::total(MK_PAGED_MAX_REQUESTS), PC_REGS, p.device, &ready);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at{};
@@ -588,7 +585,7 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(w.ctas);
   cfg.blockDim = dim3(PC_THREADS);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = ChunkCfg<HD>::total(p.n);
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;

@@ -592,11 +592,11 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
   if (!make_page_tmap(&tk, kv.k, kv, HD, FewCfg<HD, NT>::KS, BF) ||
       !make_page_tmap(&tv, kv.v, kv, HD, FewCfg<HD, NT>::KS, BF))
     return cudaErrorInvalidValue;
-  const int smem = FewCfg<HD, NT>::total(p.n);
-  const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<HD, BF, NT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = paged_prepare((const void*)paged_few_kernel<HD, BF, NT>,
+                                      FewCfg<HD, NT>::total(MK_PAGED_MAX_REQUESTS), 0, p.device, &ready);
   if (e != cudaSuccess) return e;
-  paged_few_kernel<HD, BF, NT><<<w.ctas, PF_THREADS, smem, st>>>(tk, tv, p, w);
+  paged_few_kernel<HD, BF, NT><<<w.ctas, PF_THREADS, FewCfg<HD, NT>::total(p.n), st>>>(tk, tv, p, w);
   return cudaGetLastError();
 }
 

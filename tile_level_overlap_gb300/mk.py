@@ -349,51 +349,59 @@ class Plan:
 
 
 # ---------------------------------------------------------------- paged KV cache
+# A step makes these calls per layer, and the smallest take the GPU a few
+# microseconds: the checks of a call are one expression each, and what is wrong
+# is worked out after one has failed.
 
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
 
 
-def _on_gpu(t, dtype, what: str) -> None:
-    _need(t.is_cuda and t.dtype == dtype, f"{what}: a CUDA tensor of {dtype} is wanted")
+def _tensors(device, **wanted):
+    """Raise for the first of name=(tensor, dtype, shape or None) that is not a
+    contiguous tensor of that kind on `device`."""
+    for name, (t, dtype, shape) in wanted.items():
+        if t is None:
+            continue
+        _need(t.is_cuda and t.device == device, f"{name}: a CUDA tensor on {device} is wanted")
+        _need(t.dtype == dtype, f"{name}: {dtype} is wanted, not {t.dtype}")
+        _need(shape is None or tuple(t.shape) == shape, f"{name}: {shape} is wanted, not {tuple(t.shape)}")
+        _need(t.is_contiguous(), f"{name}: contiguous")
 
 
-def _int32(t, what: str) -> None:
-    import torch
-    _on_gpu(t, torch.int32, what)
-    _need(t.is_contiguous(), f"{what}: contiguous")
+def _heads(device, dtype, **wanted):
+    """Raise for the first of name=(tensor, shape) that is not [tokens, heads,
+    head_dim] with heads that lie end to end."""
+    for name, (t, shape) in wanted.items():
+        _need(t.is_cuda and t.device == device and t.dtype == dtype and tuple(t.shape) == shape,
+              f"{name}: {dtype} {shape} on {device} is wanted, not {t.dtype} {tuple(t.shape)} on {t.device}")
+        s = t.stride()
+        _need(s[2] == 1 and (shape[1] == 1 or s[1] == shape[2]), f"{name}: heads that lie end to end")
 
 
-def _heads(t, n_heads: int, dim: int, dtype, device, what: str) -> int:
-    """Stride from token to token of a [tokens, heads, head_dim] tensor whose
-    heads lie end to end."""
-    _on_gpu(t, dtype, what)
-    s = t.stride()
-    _need(t.device == device and t.dim() == 3 and t.shape[1] == n_heads and t.shape[2] == dim
-          and s[2] == 1 and (n_heads == 1 or s[1] == dim),
-          f"{what}: [tokens, {n_heads}, {dim}] with contiguous heads on the cache's device")
-    return s[0] if t.shape[0] > 1 else max(s[0], n_heads * dim)
+class _OnDevice:
+    """Calls on one device's tensors: its current stream, or a given one, with
+    that device current."""
 
+    def _place(self, device):
+        import torch
+        self.device, self._dev = device, device.index
+        self._i32, self._f32 = torch.int32, torch.float32
+        self._current, self._guard = torch.cuda.current_device, torch.cuda.device
+        # the current stream as an address, without a Stream object for it
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
 
-def _run_on(device, stream):
-    """(device guard or None, raw stream) of a call on `device`'s tensors: the
-    given stream or the device's current one."""
-    import torch
-    raw = (int(stream.cuda_stream) if stream is not None
-           else torch.cuda.current_stream(device).cuda_stream)
-    return (None if torch.cuda.current_device() == device.index else torch.cuda.device(device)), raw
-
-
-def _call(device, stream, what: str, fn, *args) -> None:
-    guard, raw = _run_on(device, stream)
-    if guard is None:
-        rc = fn(*args, raw)
-    else:
-        with guard:
+    def _call(self, what: str, fn, stream, *args) -> None:
+        raw = self._raw_stream(self._dev) if stream is None else int(stream.cuda_stream)
+        if self._current() == self._dev:
             rc = fn(*args, raw)
-    if rc != MK_OK:
-        raise MkError(rc, what)
+        else:
+            with self._guard(self._dev):
+                rc = fn(*args, raw)
+        if rc:
+            raise MkError(rc, what)
 
 
 class Rope:
@@ -428,26 +436,25 @@ class Rope:
         self._p = ctypes.addressof(self.c)
 
 
-class PagedBatch:
+class PagedBatch(_OnDevice):
     """The tables of a step (mk_paged_batch) over torch int32 CUDA tensors:
     block_table [n, max_blocks], cu_new [n + 1], kv_lens [n], and for build()
     and append positions and slots [max_tokens].  Holds references to them."""
 
     def __init__(self, block_table, cu_new, kv_lens, positions=None, slots=None, *, page_size: int,
                  max_new: int):
-        for name, t in (("block_table", block_table), ("cu_new", cu_new), ("kv_lens", kv_lens),
-                        ("positions", positions), ("slots", slots)):
-            if t is not None:
-                _int32(t, name)
-                _need(t.device == kv_lens.device, f"{name}: on one device with kv_lens")
+        lib()
+        self._place(kv_lens.device)
         n = kv_lens.numel()
-        _need(block_table.dim() == 2 and block_table.shape[0] == n and cu_new.numel() == n + 1,
-              "block_table [n, max_blocks], cu_new [n + 1], kv_lens [n]")
-        _need((positions is None) == (slots is None) and
-              (slots is None or positions.numel() == slots.numel()), "positions and slots of one length")
+        _need(block_table.dim() == 2, "block_table: [n, max_blocks]")
+        rows = None if slots is None else (slots.numel(),)
+        _need((positions is None) == (slots is None), "positions and slots: both or neither")
+        _tensors(self.device, kv_lens=(kv_lens, self._i32, (n,)), cu_new=(cu_new, self._i32, (n + 1,)),
+                 block_table=(block_table, self._i32, (n, block_table.shape[1])),
+                 slots=(slots, self._i32, rows), positions=(positions, self._i32, rows))
         self.block_table, self.cu_new, self.kv_lens = block_table, cu_new, kv_lens
         self.positions, self.slots = positions, slots
-        self.n, self.device, self.page_size, self.max_new = n, kv_lens.device, page_size, int(max_new)
+        self.n, self.page_size, self.max_new = n, page_size, int(max_new)
         self.max_tokens = 0 if slots is None else slots.numel()
         self.c = mk_paged_batch(_ptr(block_table), _ptr(cu_new), _ptr(kv_lens),
                                 None if slots is None else _ptr(positions),
@@ -458,22 +465,28 @@ class PagedBatch:
     def build(self, ctx_lens, new_lens, free_pages, n_free, n_left, status=None, stream=None) -> None:
         """mk_paged_tables: fill the tables from device int32 lengths [n], taking
         pages from the end of free_pages[0 : n_free[0]]; n_left[0] receives what
-        remains."""
-        _need(self.slots is not None, "build needs positions and slots")
-        for name, t, k in (("ctx_lens", ctx_lens, self.n), ("new_lens", new_lens, self.n),
-                           ("free_pages", free_pages, None), ("n_free", n_free, 1),
-                           ("n_left", n_left, 1), ("status", status, 1)):
-            if t is not None:
-                _int32(t, name)
-                _need(t.device == self.device and (k is None or t.numel() == k),
-                      f"{name}: {k} values on the batch's device")
+        remains.  `status` (int32 [1]) receives MK_ERR_BOUNDS where a request is
+        refused."""
+        i32, dev, n = self._i32, self._dev, self.n
+        if not (ctx_lens.dtype is i32 and ctx_lens.get_device() == dev and ctx_lens.numel() == n
+                and ctx_lens.is_contiguous() and new_lens.dtype is i32 and new_lens.get_device() == dev
+                and new_lens.numel() == n and new_lens.is_contiguous() and free_pages.dtype is i32
+                and free_pages.get_device() == dev and free_pages.is_contiguous() and n_free.dtype is i32
+                and n_free.get_device() == dev and n_free.numel() == 1 and n_left.dtype is i32
+                and n_left.get_device() == dev and n_left.numel() == 1 and self.slots is not None
+                and (status is None or (status.dtype is i32 and status.get_device() == dev
+                                        and status.numel() == 1))):
+            _need(self.slots is not None, "build needs positions and slots")
+            _tensors(self.device, ctx_lens=(ctx_lens, i32, (n,)), new_lens=(new_lens, i32, (n,)),
+                     free_pages=(free_pages, i32, None), n_free=(n_free, i32, (1,)),
+                     n_left=(n_left, i32, (1,)), status=(status, i32, (1,)))
         self.c.max_tokens = self.max_tokens
-        _call(self.device, stream, "mk_paged_tables", lib().mk_paged_tables, self._p, _ptr(ctx_lens),
-              _ptr(new_lens), _ptr(free_pages), free_pages.numel(), _ptr(n_free), _ptr(n_left),
-              None if status is None else _ptr(status))
+        self._call("mk_paged_tables", _lib.mk_paged_tables, stream, self._p, ctx_lens.data_ptr(),
+                   new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
+                   n_left.data_ptr(), None if status is None else status.data_ptr())
 
 
-class PagedCache:
+class PagedCache(_OnDevice):
     """One layer's paged cache (mk_paged_cache) over torch tensors k and v
     [n_pages, n_kv_heads, page_size, head_dim] of bf16 or fp16 (any view of that
     shape with contiguous head_dim, equal strides for both).  `workspace`
@@ -487,8 +500,10 @@ class PagedCache:
               and k.dtype in (torch.bfloat16, torch.float16), "k, v: CUDA tensors of bf16 or fp16")
         _need(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1,
               "k, v: [n_pages, n_kv_heads, page_size, head_dim], same strides")
+        lib()
+        self._place(k.device)
         n_pages, hkv, page, d = k.shape
-        self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        self.k, self.v, self.dtype = k, v, k.dtype
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size = n_q_heads, hkv, d, page
         self._status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self.workspace = None
@@ -512,53 +527,70 @@ class PagedCache:
         """mk_paged_append: q [T, n_q_heads, head_dim], k, v [T, n_kv_heads,
         head_dim], slots int32 [T], positions int32 [T] or [n_axes, T]; q_out
         defaults to q itself."""
-        q_out = q if q_out is None else q_out
-        hq, hkv, d, dev, typ = self.n_q_heads, self.n_kv_heads, self.head_dim, self.device, self.dtype
+        if q_out is None:
+            q_out = q
+        hq, hkv, d, dev, typ, i32 = self.n_q_heads, self.n_kv_heads, self.head_dim, self._dev, self.dtype, self._i32
         n = q.shape[0]
-        _int32(slots, "slots")
-        _need(slots.numel() == n and k.shape[0] == n and v.shape[0] == n and q_out.shape[0] == n
-              and slots.device == dev, "q, k, v, q_out and slots of one length and device")
-        for name, g in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if g is not None:
-                _on_gpu(g, typ, name)
-                _need(g.numel() == d and g.is_contiguous() and g.device == dev, f"{name}: [{d}]")
-        pos = pos_stride = 0
+        qs, ks, vs, os = q.stride(), k.stride(), v.stride(), q_out.stride()
+        wide, narrow = (n, hq, d), (n, hkv, d)
+        if not (q.shape == wide and k.shape == narrow and v.shape == narrow and q_out.shape == wide
+                and q.dtype is typ and k.dtype is typ and v.dtype is typ and q_out.dtype is typ
+                and q.get_device() == dev and k.get_device() == dev and v.get_device() == dev
+                and q_out.get_device() == dev and qs[2] == 1 and ks[2] == 1 and vs[2] == 1 and os[2] == 1
+                and (hq == 1 or (qs[1] == d and os[1] == d)) and (hkv == 1 or (ks[1] == d and vs[1] == d))
+                and slots.dtype is i32 and slots.get_device() == dev and slots.numel() == n
+                and slots.is_contiguous()):
+            _heads(self.device, typ, q=(q, wide), k=(k, narrow), v=(v, narrow), q_out=(q_out, wide))
+            _tensors(self.device, slots=(slots, i32, (n,)))
+        if (q_norm is not None or k_norm is not None):
+            for g in (q_norm, k_norm):
+                if g is not None and not (g.dtype is typ and g.get_device() == dev and g.shape == (d,)
+                                          and g.is_contiguous()):
+                    _tensors(self.device, q_norm=(q_norm, typ, (d,)), k_norm=(k_norm, typ, (d,)))
+        pos, pos_stride, rp = None, 0, None
         if rope is not None:
             _need(positions is not None, "rope needs positions")
-            _on_gpu(positions, self._status.dtype, "positions")
-            one = positions.dim() == 1
-            _need(positions.shape[-1] == n and positions.device == dev and positions.dim() <= 2 and
-                  (1 if one else positions.shape[0]) == rope.n_axes and (n < 2 or positions.stride(-1) == 1),
-                  f"positions: [{rope.n_axes}, {n}]")
-            pos, pos_stride = _ptr(positions), 0 if one else positions.stride(0)
-        qs, ks, vs, os = (_heads(q, hq, d, typ, dev, "q"), _heads(k, hkv, d, typ, dev, "k"),
-                          _heads(v, hkv, d, typ, dev, "v"), _heads(q_out, hq, d, typ, dev, "q_out"))
+            shape, rp = positions.shape, rope._p
+            if not (positions.dtype is i32 and positions.get_device() == dev and shape[-1] == n
+                    and (shape == (rope.n_axes, n) or (len(shape) == 1 and rope.n_axes == 1))
+                    and (n < 2 or positions.stride(-1) == 1)):
+                raise ValueError(f"positions: int32 [{rope.n_axes}, {n}] on {self.device}, rows contiguous")
+            pos = positions.data_ptr()
+            if rope.n_axes > 1:
+                pos_stride = positions.stride(0)
         if n == 0:
             return
-        _call(dev, stream, "mk_paged_append", lib().mk_paged_append, self._p, _ptr(q), qs, _ptr(k), ks,
-              _ptr(v), vs, _ptr(q_out), os, None if q_norm is None else _ptr(q_norm),
-              None if k_norm is None else _ptr(k_norm), eps, None if rope is None else rope._p,
-              pos or None, pos_stride, _ptr(slots), n)
+        # the stride of a lone token joins nothing and may be any number
+        self._call("mk_paged_append", _lib.mk_paged_append, stream, self._p,
+                   q.data_ptr(), qs[0] if n > 1 else hq * d, k.data_ptr(), ks[0] if n > 1 else hkv * d,
+                   v.data_ptr(), vs[0] if n > 1 else hkv * d, q_out.data_ptr(), os[0] if n > 1 else hq * d,
+                   None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                   eps, rp, pos, pos_stride, slots.data_ptr(), n)
 
     def attention(self, q, batch: PagedBatch, out, lse=None, scale: float = 0.0, window: int = 0,
                   stream=None) -> None:
         """mk_paged_attention: q, out [rows, n_q_heads, head_dim], lse float32
         [rows, n_q_heads] or None."""
-        import torch
         if self.workspace is None:
+            import torch
             self._set_workspace(torch.empty(MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device))
-        hq, d, dev, typ = self.n_q_heads, self.head_dim, self.device, self.dtype
+        hq, d, dev, typ = self.n_q_heads, self.head_dim, self._dev, self.dtype
         n = q.shape[0]
-        _need(out.shape[0] == n and batch.device == dev, "q, out and batch of one length and device")
-        if lse is not None:
-            _on_gpu(lse, torch.float32, "lse")
-            _need(lse.is_contiguous() and lse.numel() == n * hq and lse.device == dev, f"lse: [{n}, {hq}]")
-        qs, os = _heads(q, hq, d, typ, dev, "q"), _heads(out, hq, d, typ, dev, "out")
+        wide, qs, os = (n, hq, d), q.stride(), out.stride()
+        if not (q.shape == wide and out.shape == wide and q.dtype is typ and out.dtype is typ
+                and q.get_device() == dev and out.get_device() == dev and batch._dev == dev
+                and qs[2] == 1 and os[2] == 1 and (hq == 1 or (qs[1] == d and os[1] == d))
+                and (lse is None or (lse.dtype is self._f32 and lse.get_device() == dev
+                                     and lse.shape == (n, hq) and lse.is_contiguous()))):
+            _heads(self.device, typ, q=(q, wide), out=(out, wide))
+            _tensors(self.device, lse=(lse, self._f32, (n, hq)))
+            _need(batch._dev == dev, "batch: on the cache's device")
         if n == 0:
             return
         batch.c.max_tokens = n
-        _call(dev, stream, "mk_paged_attention", lib().mk_paged_attention, self._p, batch._p, _ptr(q), qs,
-              _ptr(out), os, None if lse is None else _ptr(lse), scale, window)
+        self._call("mk_paged_attention", _lib.mk_paged_attention, stream, self._p, batch._p, q.data_ptr(),
+                   qs[0] if n > 1 else hq * d, out.data_ptr(), os[0] if n > 1 else hq * d,
+                   None if lse is None else lse.data_ptr(), scale, window)
 
     def status(self) -> int:
         """The status word (waits for the device work that writes it)."""
