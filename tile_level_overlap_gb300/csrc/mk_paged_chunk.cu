@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             const int tok = (b * 128 + lane * boxt) & mask;
 #pragma unroll
             for (int x = 0; x < HD / 64; ++x)
-              tma_page(dst + x * 16384, tm, 64 * x, tok, head, page, &full[stage]);
+              tma_page(dst + x * 16384, tm, tok, x, head, page, &full[stage]);
           }
           if (++stage == ST) { stage = 0; sphase ^= 1; }
           return true;
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
 template <int HD, bool BF>
 cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
   CUtensorMap tq, tk, tv;
-  if (!make_page_tmap(&tk, kv.k, kv, HD, 128, BF) || !make_page_tmap(&tv, kv.v, kv, HD, 128, BF) ||
+  if (!make_page_tmap(&tk, kv.k, kv, HD, 128, 1, BF) || !make_page_tmap(&tv, kv.v, kv, HD, 128, 1, BF) ||
       !make_rows_tmap(&tq, p.q, p.rows, p.hkv * p.rep, HD, p.q_stride, p.rep, 128 / p.rep, BF))
     return cudaErrorInvalidValue;
   // the register split needs the block to be launched with what it counts on

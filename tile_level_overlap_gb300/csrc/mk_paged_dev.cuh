@@ -95,14 +95,15 @@ __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, volat
 }
 
 // ---------------------------------------------------------------- page loads
-// Box of 64 elements x tokens of one head and page (tensor map dimensions:
-// element, token, head, page).  A page outside the map reads as zeros.
-__device__ __forceinline__ void tma_page(void* dst, const void* tmap, int x, int token, int head,
+// Box of 64 elements x tokens x parts of one head and page, from part `part` on
+// (the map's dimensions: element, token, part, head, page).  A page outside the
+// map reads as zeros.
+__device__ __forceinline__ void tma_page(void* dst, const void* tmap, int token, int part, int head,
                                          int page, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(tmap), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(0), "r"(token), "r"(part), "r"(head), "r"(page), "r"(smem_u32(bar))
       : "memory");
 }
 

@@ -248,14 +248,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], PF_STAGE);
         __syncwarp();
         if (lane < nbox) {
-          uint8_t* dst = smem + stage * PF_STAGE + lane * boxt * 128;
+          uint8_t* dst = smem + stage * PF_STAGE + lane * boxt * (2 * HD);
           const int tok = ((b0 + i) * KS + lane * boxt) & mask;
-#pragma unroll
-          for (int x = 0; x < HD / 64; ++x)
-            tma_page(dst + x * KS * 128, &tk, 64 * x, tok, head, page, &full[stage]);
-#pragma unroll
-          for (int x = 0; x < HD / 64; ++x)
-            tma_page(dst + PF_STAGE / 2 + x * KS * 128, &tv, 64 * x, tok, head, page, &full[stage]);
+          tma_page(dst, &tk, tok, 0, head, page, &full[stage]);
+          tma_page(dst + PF_STAGE / 2, &tv, tok, 0, head, page, &full[stage]);
         }
         if (++stage == C::STAGES) { stage = 0; sphase ^= 1; }
         page = next;
@@ -280,6 +276,19 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   // row and 16-byte chunk that this lane addresses in a 16 x 16 matrix load
   const int lr = (lane & 7) + ((lane >> 3) & 1) * 8, lc = lane >> 4;     // keys on rows
   const int vr = (lane & 7) + (lane >> 4) * 8, vc = (lane >> 3) & 1;     // transposed
+  // A box holds the first 64 elements of its tokens, then the next 64: byte
+  // offsets of this lane's rows in a block, and of a box's second half.
+  const int bsh = min(P.page_shift, HD == 128 ? 6 : 7);
+  const uint32_t part = HD == 128 ? 128u << bsh : 0u;
+  auto row_at = [&](int key) -> uint32_t {
+    return ((uint32_t)(key >> bsh) * (2u * HD) << bsh) + (uint32_t)(key & ((1 << bsh) - 1)) * 128u;
+  };
+  uint32_t k_at[MT], v_at[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    k_at[mt] = row_at((kw * MT + mt) * 16 + lr);
+    v_at[mt] = row_at((kw * MT + mt) * 16 + vr);
+  }
   int stage = 0, slot = 0, turn = 0;
   uint32_t sphase = 0, qphase = 0;
   for (;;) {
@@ -355,8 +364,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t a[4];
-            const int row = (kw * MT + mt) * 16 + lr, ch = 2 * ks + lc;
-            ldsm4(a, kb + (ch >> 3) * (KS * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            const int ch = 2 * ks + lc;
+            ldsm4(a, kb + k_at[mt] + (ks >= 4 ? part : 0u) + (((ch & 7) ^ (lr & 7)) << 4));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               if constexpr (NT <= 2) mma16<BF>(sc[mt][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
@@ -430,8 +439,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll
           for (int x = 0; x < HD / 16; ++x) {
             uint32_t a[4];
-            const int row = (kw * MT + mt) * 16 + vr, ch = 2 * x + vc;
-            ldsm4t(a, vb + (ch >> 3) * (KS * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            const int ch = 2 * x + vc;
+            ldsm4t(a, vb + v_at[mt] + (x >= 4 ? part : 0u) + (((ch & 7) ^ (vr & 7)) << 4));
             a[0] &= keep0; a[1] &= keep0; a[2] &= keep1; a[3] &= keep1;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[x][nt], a, b[nt][0], b[nt][1]);
@@ -589,8 +598,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 template <int HD, bool BF, int NT>
 cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
   CUtensorMap tk, tv;
-  if (!make_page_tmap(&tk, kv.k, kv, HD, FewCfg<HD, NT>::KS, BF) ||
-      !make_page_tmap(&tv, kv.v, kv, HD, FewCfg<HD, NT>::KS, BF))
+  if (!make_page_tmap(&tk, kv.k, kv, HD, FewCfg<HD, NT>::KS, HD / 64, BF) ||
+      !make_page_tmap(&tv, kv.v, kv, HD, FewCfg<HD, NT>::KS, HD / 64, BF))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = paged_prepare((const void*)paged_few_kernel<HD, BF, NT>,

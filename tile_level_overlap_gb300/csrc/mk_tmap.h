@@ -40,21 +40,23 @@ inline bool make_tmap_bf16(CUtensorMap* out, const void* base, uint64_t rows, ui
   return r == CUDA_SUCCESS;
 }
 
-// Tensor map over a paged cache: (element, token of the page, kv head, page),
-// boxes of 64 elements (128 B) x min(page, most) tokens with 128-byte swizzle.
-// Pages (and tokens) out of range read as zero.  Strides of dimensions of size
-// one are never used and replaced by a valid one.
+// Tensor map over a paged cache: (element, token of the page, 64-element part of
+// the head, kv head, page), boxes of 64 elements (128 B) x min(page, most) tokens
+// x `parts` with 128-byte swizzle, so a box's parts lie one after another in
+// shared memory.  Pages (and tokens) out of range read as zero.  Strides of
+// dimensions of size one are never used and replaced by a valid one.
 template <class Kv>
-inline bool make_page_tmap(CUtensorMap* out, const void* base, const Kv& c, int d, int most, bool bf16) {
+inline bool make_page_tmap(CUtensorMap* out, const void* base, const Kv& c, int d, int most, int parts,
+                           bool bf16) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
   if (!enc) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)c.page, (cuuint64_t)c.hkv, (cuuint64_t)c.n_pages};
-  cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2,
+  cuuint64_t dims[5] = {64, (cuuint64_t)c.page, (cuuint64_t)(d / 64), (cuuint64_t)c.hkv, (cuuint64_t)c.n_pages};
+  cuuint64_t strides[4] = {(cuuint64_t)c.token_stride * 2, 128,
                            (cuuint64_t)(c.hkv > 1 ? c.head_stride : c.token_stride) * 2,
                            (cuuint64_t)(c.n_pages > 1 ? c.page_stride : c.token_stride) * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)(c.page < most ? c.page : most), 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = enc(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+  cuuint32_t box[5] = {64, (cuuint32_t)(c.page < most ? c.page : most), (cuuint32_t)parts, 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
