@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(PT_THREADS) paged_tables_kernel(const PagedTab
   int* s_ctx = s_upto + P.n + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int page_mask = (1 << P.page_shift) - 1;
+  grid_launch_dependents();
+  grid_wait_prior();
   const int free_raw = *P.n_free;
   const int n_free = min(max(free_raw, 0), P.free_cap);
   const long long room = (long long)P.max_blocks << P.page_shift;
@@ -162,6 +164,8 @@ template <int HD, bool BF>
 __global__ void __launch_bounds__(PA_THREADS) paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
   __shared__ float2 cs[HD / 2];  // cos, sin of the token's pairs
   const int t = blockIdx.x, tid = threadIdx.x;
+  grid_launch_dependents();
+  grid_wait_prior();
   const int slot = P.slot[t];
   if (slot < 0) return;
   if (slot >= P.n_slots) {
@@ -240,9 +244,8 @@ __global__ void __launch_bounds__(PA_THREADS) paged_append_kernel(const __grid_c
 
 template <int HD>
 cudaError_t append_launch(const PagedAppendParams& p, int dtype, cudaStream_t st) {
-  if (dtype == MK_BF16) paged_append_kernel<HD, true><<<p.n_tokens, PA_THREADS, 0, st>>>(p);
-  else paged_append_kernel<HD, false><<<p.n_tokens, PA_THREADS, 0, st>>>(p);
-  return cudaGetLastError();
+  return dtype == MK_BF16 ? paged_launch(paged_append_kernel<HD, true>, p.n_tokens, PA_THREADS, 0, st, p)
+                          : paged_launch(paged_append_kernel<HD, false>, p.n_tokens, PA_THREADS, 0, st, p);
 }
 
 // ---------------------------------------------------------------- attention
@@ -309,6 +312,14 @@ int check_cache(const mk_paged_cache* c) {
   return MK_OK;
 }
 
+// The code of a call whose launches said `e` (a failed one leaves nothing behind
+// for the next CUDA call to report).
+int done(cudaError_t e) {
+  if (e == cudaSuccess) return MK_OK;
+  cudaGetLastError();
+  return MK_ERR_CUDA;
+}
+
 int check_batch(const mk_paged_batch* b) {
   if (!b || !b->block_table || !b->cu_new || !b->kv_lens) return MK_ERR_INVALID_ARG;
   if (!al4(b->block_table) || !al4(b->cu_new) || !al4(b->kv_lens)) return MK_ERR_INVALID_ARG;
@@ -362,8 +373,7 @@ extern "C" int mk_paged_tables(const mk_paged_batch* b, const int32_t* ctx_lens,
     return MK_ERR_CUDA;
   }
   const int grid = min(152, max(1, (b->max_tokens + 2 * PT_THREADS - 1) / (2 * PT_THREADS)));
-  paged_tables_kernel<<<grid, PT_THREADS, smem, (cudaStream_t)stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  return done(paged_launch(paged_tables_kernel, grid, PT_THREADS, (int)smem, (cudaStream_t)stream, p));
 }
 
 extern "C" int mk_rope_init(mk_rope* rope, int rotary_dim, double theta, const double* inv_freq,
@@ -425,7 +435,7 @@ extern "C" int mk_paged_append(const mk_paged_cache* c, const void* q, int64_t q
   if (rope) p.rope = *rope;
   const cudaError_t e = c->head_dim == 128 ? append_launch<128>(p, c->dtype, (cudaStream_t)stream)
                                            : append_launch<64>(p, c->dtype, (cudaStream_t)stream);
-  return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  return done(e);
 }
 
 extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch* b, const void* q,
@@ -461,7 +471,5 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch*
   const PagedKv kv = {c->k, c->v, c->page_stride, c->head_stride, c->token_stride,
                       c->n_pages, c->n_kv_heads, c->page_size};
   const cudaError_t e = attention_launch(p, kv, c->head_dim, c->dtype == MK_BF16, c->workspace, (cudaStream_t)stream);
-  if (e == cudaSuccess) return MK_OK;
-  cudaGetLastError();
-  return MK_ERR_CUDA;
+  return done(e);
 }

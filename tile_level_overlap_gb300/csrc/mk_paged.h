@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <utility>
 
 #include "../../include/mk.h"
 
@@ -67,6 +68,22 @@ struct PagedParts {
 // is set to the largest a call can ask for).  `regs`: what the kernel has to be
 // compiled to, 0: any.  `done` is the kernel's own word, a bit per device.
 cudaError_t paged_prepare(const void* kernel, int smem, int regs, int device, std::atomic<uint64_t>* done);
+
+// Launch as a programmatic dependent of what precedes in the stream.
+template <class... P, class... A>
+inline cudaError_t paged_launch(void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
                              bool bf, cudaStream_t st);

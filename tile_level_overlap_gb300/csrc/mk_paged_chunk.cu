@@ -44,9 +44,10 @@ struct ChunkCfg {
   static constexpr int o_meta = o_kv + STAGES * TILE;
   static constexpr int o_bar = o_meta + SLOTS * 64;
   static constexpr int o_pre = o_bar + 256;
-  static constexpr int total(int n) { return o_pre + 4 * (n + 1); }
+  static constexpr int total(int n) { return o_pre + Kept::bytes(n); }
+  static constexpr int most = o_pre + KEPT_MOST;
 };
-static_assert(ChunkCfg<128>::total(MK_PAGED_MAX_REQUESTS) <= 232448, "shared memory of a CTA");
+static_assert(ChunkCfg<128>::most <= 232448 && ChunkCfg<64>::most <= 232448, "shared memory of a CTA");
 
 struct Tile {
   int key0, nblk;          // first key of the run; 0 blocks: the end
@@ -105,7 +106,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   volatile int* dead = reinterpret_cast<volatile int*>(ofull + 2);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(const_cast<int*>(dead) + 1);
   Tile* meta = reinterpret_cast<Tile*>(smem + C::o_meta);
-  int* pre = reinterpret_cast<int*>(smem + C::o_pre);
+  const Kept kept(smem + C::o_pre, P.n);
+  int* pre = kept.pre;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int TS = 128 / P.rep, TT = 2 * TS;  // tokens of a half, of a tile
 
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     int u = 0, ntile = 0, b0;
     Request q{};
     if (r < P.n) {
-      q = read_request(P, r);
+      q = kept.read(P, r);
       bad |= q.bad;
       if ((int64_t)q.add * P.rep > P.few_rows) ntile = (q.add + TT - 1) / TT;
     }
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           ++r;
           t = -1;
         }
-        const Request q = read_request(P, r);
+        const Request q = kept.again(P, r);
         const int per_head = (pre[r + 1] - pre[r]) / P.hkv, ntile = (q.add + TT - 1) / TT;
         int x0 = 0, b0;  // first unit of the tile in this run
         if (t < 0) {  // find the tile of unit u
@@ -577,19 +579,9 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
   // the register split needs the block to be launched with what it counts on
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF>,
-                                      ChunkCfg<HD>::total(MK_PAGED_MAX_REQUESTS), PC_REGS, p.device, &ready);
+                                      ChunkCfg<HD>::most, PC_REGS, p.device, &ready);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(w.ctas);
-  cfg.blockDim = dim3(PC_THREADS);
-  cfg.dynamicSmemBytes = ChunkCfg<HD>::total(p.n);
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<HD, BF>, tq, tk, tv, p, w);
+  return paged_launch(paged_chunk_kernel<HD, BF>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st, tq, tk, tv, p, w);
 }
 
 }  // namespace

@@ -65,6 +65,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ---------------------------------------------------------------- dependent launches
+// Every kernel here is launched as a programmatic dependent of what precedes it
+// in the stream: it may be set up while that one's last blocks run, and touches
+// global memory only after grid_wait_prior() has seen it complete.  (The tile
+// kernel waits later: it is started by the few-row kernel, which lets it go
+// only after its own wait.)
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -115,9 +120,8 @@ struct Request {
   int row0, add, pos0, lo, hi;
   bool bad;
 };
-__device__ __forceinline__ Request read_request(const PagedAttnParams& P, int r) {
+__device__ __forceinline__ Request make_request(const PagedAttnParams& P, int c0, int c1, int kv) {
   Request q;
-  const int c0 = P.cu[r], c1 = P.cu[r + 1], kv = P.kv[r];
   const int room = P.max_blocks << P.page_shift;
   const int kvp = max(kv, 0);
   q.bad = kv < 0 || kvp > room;
@@ -131,6 +135,28 @@ __device__ __forceinline__ Request read_request(const PagedAttnParams& P, int r)
   q.lo = q.pos0 >= P.window ? min(q.pos0 - P.window + 1, q.hi) : 0;
   return q;
 }
+
+// The scan's results in shared memory: pre [n + 1], a request's first unit, and
+// for n up to REQ_KEPT also what read_request read, so that the walk over the
+// units does not wait for it again.
+constexpr int REQ_KEPT = 1024;
+struct Kept {
+  int *pre, *c0, *c1, *kv;
+  __host__ __device__ static constexpr int bytes(int n) { return 4 * (n + 1) + (n <= REQ_KEPT ? 12 * n : 0); }
+  __device__ __forceinline__ Kept(void* base, int n) : pre((int*)base), c0(pre + n + 1), c1(c0 + n), kv(c1 + n) {}
+  __device__ __forceinline__ Request read(const PagedAttnParams& P, int r) const {
+    const int a = P.cu[r], b = P.cu[r + 1], k = P.kv[r];
+    if (P.n <= REQ_KEPT) { c0[r] = a; c1[r] = b; kv[r] = k; }
+    return make_request(P, a, b, k);
+  }
+  __device__ __forceinline__ Request again(const PagedAttnParams& P, int r) const {
+    if (P.n <= REQ_KEPT) return make_request(P, c0[r], c1[r], kv[r]);
+    return make_request(P, P.cu[r], P.cu[r + 1], P.kv[r]);
+  }
+};
+constexpr int KEPT_MOST = Kept::bytes(REQ_KEPT) > Kept::bytes(MK_PAGED_MAX_REQUESTS)
+                              ? Kept::bytes(REQ_KEPT)
+                              : Kept::bytes(MK_PAGED_MAX_REQUESTS);
 
 // Exclusive prefix sums of one value per thread of a block of W warps.
 template <int W>

@@ -45,11 +45,10 @@ struct FewCfg {
   static constexpr int o_meta = o_ml + PF_WARPS * RT * 8;
   static constexpr int o_bar = o_meta + QSLOTS * 48;
   static constexpr int o_pre = o_bar + 8 * (2 * STAGES + 2 * QSLOTS) + 64;
-  static constexpr int total(int n) { return o_pre + 4 * (n + 1); }
+  static constexpr int total(int n) { return o_pre + Kept::bytes(n); }
+  static constexpr int most = o_pre + KEPT_MOST;
 };
-static_assert(FewCfg<128, 1>::total(MK_PAGED_MAX_REQUESTS) <= 232448 &&
-                  FewCfg<128, 2>::total(MK_PAGED_MAX_REQUESTS) <= 232448 &&
-                  FewCfg<128, 4>::total(MK_PAGED_MAX_REQUESTS) <= 232448,
+static_assert(FewCfg<128, 1>::most <= 232448 && FewCfg<128, 2>::most <= 232448 && FewCfg<128, 4>::most <= 232448,
               "shared memory of a CTA");
 
 // One part of a (request, kv head): blocks [blk, blk + nblk) of its `of`.
@@ -134,11 +133,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   uint64_t* qempty = qfull + C::QSLOTS;
   volatile int* dead = reinterpret_cast<volatile int*>(qempty + C::QSLOTS);
   int* scan_tmp = const_cast<int*>(dead) + 1;
-  int* pre = reinterpret_cast<int*>(smem + C::o_pre);
+  const Kept kept(smem + C::o_pre, P.n);
+  int* pre = kept.pre;
   Segment* meta = reinterpret_cast<Segment*>(smem + C::o_meta);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  grid_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -149,12 +148,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       mbar_init(&qempty[s], PF_WARPS);
     }
     *dead = 0;
-    W.desc[blockIdx.x].parts = 0;
     fence_mbar_init();
   }
   for (int i = tid; i < C::QSLOTS * RT * C::QROW / 16; i += PF_THREADS)
     reinterpret_cast<uint4*>(smem + C::o_q)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
+
+  grid_wait_prior();
+  grid_launch_dependents();
+  if (tid == 0) W.desc[blockIdx.x].parts = 0;
 
   // units: key blocks of all (request, kv head) pairs, pairs of a request end to end
   const int per = (P.n + PF_THREADS - 1) / PF_THREADS;
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
     if (r >= P.n) break;
-    const Request q = read_request(P, r);
+    const Request q = kept.read(P, r);
     bad |= q.bad;
     int u = 0;
     if (q.add > 0 && (int64_t)q.add * P.rep <= P.few_rows)
@@ -197,13 +199,24 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     uint32_t sphase = 1, qphase = 1;  // parities of the "empty" waits
     for (int u = u0; u < u1;) {
       while (pre[r + 1] <= u) ++r;
-      const Request q = read_request(P, r);
+      const Request q = kept.again(P, r);
       // units [x0, x1) of the pair: blocks [blk, blk + nblk)
       const int units = (pre[r + 1] - pre[r]) / P.hkv, local = u - pre[r], nb = units - PF_OVER;
       const int head = local / units, x0 = local - head * units, x1 = min(units, x0 + u1 - u);
       const int blk = max(0, x0 - PF_OVER), nblk = max(0, x1 - PF_OVER) - blk;
       if (nblk == 0) break;  // the run ends with the pair's overhead: the next CTA has it all
       const int b0 = q.lo / KS + blk, rows = q.add * P.rep;
+      const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
+      // page of this lane's box of a block; -1 where no row sees any of it
+      auto page_of = [&](int b) {
+        const int key = b * KS + lane * boxt;
+        if (lane >= nbox || key >= q.hi || key + boxt <= q.lo) return -1;
+        const int p = tab[key >> P.page_shift];
+        if (p >= 0 && p < P.n_pages) return p;
+        latch(P.status, MK_ERR_BOUNDS);
+        return -1;
+      };
+      int page = page_of(b0);
       const bool whole = blk == 0 && nblk == nb;
       if (blk == 0 && !whole) {  // joined by this CTA's block of the second launch
         const int last = (int)(((int64_t)(u - x0 + units) * G - 1) / T);  // CTA of the pair's last unit
@@ -230,17 +243,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                      (int64_t)(head * P.rep + lane % P.rep) * HD,
                  HD * 2, &qfull[slot]);
       if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
-      const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
-      // page of this lane's box of a block; -1 where no row sees any of it
-      auto page_of = [&](int b) {
-        const int key = b * KS + lane * boxt;
-        if (lane >= nbox || key >= q.hi || key + boxt <= q.lo) return -1;
-        const int p = tab[key >> P.page_shift];
-        if (p >= 0 && p < P.n_pages) return p;
-        latch(P.status, MK_ERR_BOUNDS);
-        return -1;
-      };
-      int page = page_of(b0);
       for (int i = 0; i < nblk; ++i) {
         const int next = i + 1 < nblk ? page_of(b0 + i + 1) : -1;
         wait_phase(&empty[stage], sphase, dead, P.status);
@@ -550,6 +552,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
                                                          const __grid_constant__ PagedParts B) {
   constexpr int LPR = HD / 4;  // threads of a row
   __shared__ uint2 rows_out[JOIN_ROWS][LPR + 1];
+  grid_launch_dependents();
   grid_wait_prior();
   const int tid = threadIdx.x, hqs = P.hkv * P.rep;
   if ((int)blockIdx.x < A.ctas) {
@@ -559,10 +562,19 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int d4 = (tid % LPR) * 4;
     for (int row = tid / LPR; row < d.rows; row += 256 / LPR) {
       Joined j;
-#pragma unroll 4
-      for (int k = 0; k < d.parts; ++k) {
-        const int64_t at = (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * A.rt + row;
-        j.add(A.ml[at], *reinterpret_cast<const float4*>(A.o + at * HD + d4));
+      for (int k0 = 0; k0 < d.parts; k0 += 8) {  // eight parts' reads in flight
+        float2 ml[8];
+        float4 o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = min(k0 + i, d.parts - 1);
+          const int64_t at = (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * A.rt + row;
+          ml[i] = A.ml[at];
+          o[i] = *reinterpret_cast<const float4*>(A.o + at * HD + d4);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (k0 + i < d.parts) j.add(ml[i], o[i]);
       }
       const int tok = d.row0 + row / P.rep, hq = d.head * P.rep + row % P.rep;
       *reinterpret_cast<uint2*>(P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD + d4) = j.out<BF>();
@@ -603,10 +615,9 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = paged_prepare((const void*)paged_few_kernel<HD, BF, NT>,
-                                      FewCfg<HD, NT>::total(MK_PAGED_MAX_REQUESTS), 0, p.device, &ready);
+                                      FewCfg<HD, NT>::most, 0, p.device, &ready);
   if (e != cudaSuccess) return e;
-  paged_few_kernel<HD, BF, NT><<<w.ctas, PF_THREADS, FewCfg<HD, NT>::total(p.n), st>>>(tk, tv, p, w);
-  return cudaGetLastError();
+  return paged_launch(paged_few_kernel<HD, BF, NT>, w.ctas, PF_THREADS, FewCfg<HD, NT>::total(p.n), st, tk, tv, p, w);
 }
 
 template <int HD, bool BF>
@@ -626,20 +637,12 @@ cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const 
 
 cudaError_t paged_join_launch(const PagedAttnParams& p, const PagedParts& a, const PagedParts& b, int d,
                               bool bf, cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(a.ctas + b.ctas * (b.rt / JOIN_ROWS));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  const int grid = a.ctas + b.ctas * (b.rt / JOIN_ROWS);
   if (d == 128)
-    return bf ? cudaLaunchKernelEx(&cfg, paged_join_kernel<128, true>, p, a, b)
-              : cudaLaunchKernelEx(&cfg, paged_join_kernel<128, false>, p, a, b);
-  return bf ? cudaLaunchKernelEx(&cfg, paged_join_kernel<64, true>, p, a, b)
-            : cudaLaunchKernelEx(&cfg, paged_join_kernel<64, false>, p, a, b);
+    return bf ? paged_launch(paged_join_kernel<128, true>, grid, 256, 0, st, p, a, b)
+              : paged_launch(paged_join_kernel<128, false>, grid, 256, 0, st, p, a, b);
+  return bf ? paged_launch(paged_join_kernel<64, true>, grid, 256, 0, st, p, a, b)
+            : paged_launch(paged_join_kernel<64, false>, grid, 256, 0, st, p, a, b);
 }
 
 }  // namespace mk
