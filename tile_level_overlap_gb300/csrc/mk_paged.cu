@@ -259,12 +259,15 @@ cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool 
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   p.device = dev;
+  p.rep_inv = (65536 + p.rep - 1) / p.rep;
   // The few-row kernel has the rows of the longest request where it takes them
   // all, else those of a single token (its products cost by the row).
   const int64_t most = (int64_t)p.max_new * p.rep;
   const bool all_few = most <= 32;
   const int want = all_few ? (int)most : p.rep;
   p.few_rows = want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 ? 32 : 0;
+  // rows a pair has at most: a warp each in the join, or several for one
+  p.join_shares = !all_few || want > 4 ? 0 : want > 2 ? 1 : want > 1 ? 2 : 3;
   // workspace: descriptions, maxima and sums, outputs of the two kernels' parts
   const int ctas = std::min(sms, 224);
   uint8_t* w = (uint8_t*)workspace;

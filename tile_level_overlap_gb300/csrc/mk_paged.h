@@ -39,7 +39,14 @@ struct PagedAttnParams {
   int hkv, rep, window;  // window 0x7fffffff: none
   int device;
   int few_rows;  // requests of at most this many rows (new tokens x rep) go to the few-row kernel
+  int rep_inv;  // ceil(2^16 / rep)
+  int join_shares;  // log2 of the warps that join one row of the few-row kernel
   float scale;
+#ifdef __CUDACC__
+  // token of a tile's row (row < 256, rep <= 64: the error, row / 2^16, stays
+  // below 1 / rep)
+  __device__ __forceinline__ int token_of(int row) const { return (row * rep_inv) >> 16; }
+#endif
 };
 
 // The cache as the tensor maps see it.
@@ -51,7 +58,7 @@ struct PagedKv {
 
 // A pair's (or tile's) rows whose keys were divided among CTAs: `parts` of them
 // from CTA desc index on; 0: none.
-struct PartDesc {
+struct alignas(16) PartDesc {
   int row0, rows, head, parts;
 };
 // Workspace of one kernel's divided rows: part 2 c (+ 1) is CTA c's first (second)

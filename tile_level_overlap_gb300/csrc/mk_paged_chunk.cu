@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   constexpr uint32_t T_S = 0, T_O = 256;
 
   const int G = min((int)gridDim.x, T), c = blockIdx.x;
-  const int u0 = c < G ? (int)((int64_t)c * T / G) : 0, u1 = c < G ? (int)((int64_t)(c + 1) * T / G) : 0;
+  const Runs runs(T, max(G, 1));
+  const int u0 = c < G ? runs.start(c) : 0, u1 = c < G ? runs.start(c + 1) : 0;
 
   if (warp >= PC_LOAD) {
     setmaxnreg_dec<PC_REGS_REST>();
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (nblk == 0) break;  // the run ends with the tile's overhead: the next CTA has it all
         const bool whole = blk == 0 && nblk == nb;
         if (blk == 0 && !whole && lane == 0) {
-          const int last = (int)(((int64_t)end * G - 1) / T);  // CTA of the tile's last unit
+          const int last = runs.of(end - 1);  // CTA of the tile's last unit
           PartDesc d;
           d.row0 = q.row0 + t * TT; d.rows = ntok * P.rep; d.head = head; d.parts = last - c + 1;
           W.desc[c] = d;
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_t = T_S + 128u * half + lanes, o_t = T_O + 128u * half + lanes;
-    const int tok_in = row / P.rep, hq_in = row - tok_in * P.rep;
+    const int tok_in = P.token_of(row), hq_in = row - tok_in * P.rep;
     const float cs = fabsf(P.scale) * 1.4426950408889634f;
     const bool neg = P.scale < 0.f;
     uint32_t blkn = 0, sn = 0, on = 0;
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         bool put[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int rw = (row & ~3) + i, tk = rw / P.rep;
+          const int rw = (row & ~3) + i, tk = P.token_of(rw);
           put[i] = tk < ntok;
           dst[i] = P.out + (int64_t)(m.row0 + tok0 + tk) * P.o_stride +
                    (int64_t)(m.head * P.rep + rw - tk * P.rep) * HD + (lane & 3) * 8;

@@ -158,6 +158,17 @@ constexpr int KEPT_MOST = Kept::bytes(REQ_KEPT) > Kept::bytes(MK_PAGED_MAX_REQUE
                               ? Kept::bytes(REQ_KEPT)
                               : Kept::bytes(MK_PAGED_MAX_REQUESTS);
 
+// T units in G runs of equal length (the first T % G one longer).
+struct Runs {
+  int len, more;
+  __device__ __forceinline__ Runs(int T, int G) : len(T / G), more(T - len * G) {}
+  __device__ __forceinline__ int start(int c) const { return c * len + min(c, more); }
+  __device__ __forceinline__ int of(int u) const {  // run of unit u
+    const int split = more * (len + 1);
+    return u < split ? u / (len + 1) : more + (u - split) / len;
+  }
+};
+
 // Exclusive prefix sums of one value per thread of a block of W warps.
 template <int W>
 __device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {

@@ -120,8 +120,10 @@ __device__ __noinline__ void let_copies_land() {
   }
 }
 
+// (The bound for few rows keeps the kernel to 128 registers, so that the blocks
+// of the join fit beside it and are set up before it ends.)
 template <int HD, bool BF, int NT>
-__global__ void __launch_bounds__(PF_THREADS, 1)
+__global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                      const __grid_constant__ PagedAttnParams P, const __grid_constant__ PagedParts W) {
   using C = FewCfg<HD, NT>;
@@ -186,15 +188,16 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   if (bad && blockIdx.x == 0) latch(P.status, MK_ERR_BOUNDS);
   __syncthreads();
 
-  // this CTA's run of units: [c T / G, (c + 1) T / G) of the G CTAs in use
+  // this CTA's run of units, of the G CTAs in use
   const int G = min((int)gridDim.x, T), c = blockIdx.x;
   if (c >= G) return;
-  const int u0 = (int)((int64_t)c * T / G), u1 = (int)((int64_t)(c + 1) * T / G);
+  const Runs runs(T, G);
+  const int u0 = runs.start(c), u1 = runs.start(c + 1);
 
   if (warp == PF_WARPS) {
     // ------------------------------------------------------------ producer
     const int boxt = min(KS, 1 << P.page_shift), nbox = KS / boxt;
-    const int mask = (1 << P.page_shift) - 1;
+    const int mask = (1 << P.page_shift) - 1, my_tok = P.token_of(lane);
     int r = find_le(pre, P.n, u0), stage = 0, slot = 0;
     uint32_t sphase = 1, qphase = 1;  // parities of the "empty" waits
     for (int u = u0; u < u1;) {
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       int page = page_of(b0);
       const bool whole = blk == 0 && nblk == nb;
       if (blk == 0 && !whole) {  // joined by this CTA's block of the second launch
-        const int last = (int)(((int64_t)(u - x0 + units) * G - 1) / T);  // CTA of the pair's last unit
+        const int last = runs.of(u - x0 + units - 1);  // CTA of the pair's last unit
         if (lane == 0) {
           PartDesc d;
           d.row0 = q.row0; d.rows = rows; d.head = head; d.parts = last - c + 1;
@@ -239,8 +242,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       __syncwarp();
       if (lane < rows)
         bulk_row(smem + C::o_q + (slot * RT + lane) * C::QROW,
-                 P.q + (int64_t)(q.row0 + lane / P.rep) * P.q_stride +
-                     (int64_t)(head * P.rep + lane % P.rep) * HD,
+                 P.q + (int64_t)(q.row0 + my_tok) * P.q_stride + (int64_t)(head * P.rep + lane - my_tok * P.rep) * HD,
                  HD * 2, &qfull[slot]);
       if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
       for (int i = 0; i < nblk; ++i) {
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = nt * 8 + 2 * t + e, pos = s.pos0 + (row < s.rows ? row / P.rep : 0);
+        const int row = nt * 8 + 2 * t + e, pos = s.pos0 + (row < s.rows ? P.token_of(row) : 0);
         last[nt][e] = min(pos, s.hi - 1);
         first[nt][e] = pos >= P.window ? pos - P.window + 1 : 0;
       }
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
     }
     // every row sees the keys [all_lo, all_hi)
-    const int end = s.pos0 + (s.rows - 1) / P.rep;
+    const int end = s.pos0 + P.token_of(s.rows - 1);
     const int all_lo = end >= P.window ? end - P.window + 1 : 0, all_hi = min(s.pos0 + 1, s.hi);
     for (int i = 0; i < s.nblk; ++i) {
       // both groups see every block's phase, also of those they leave to the
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
         }
         if (s.part < 0) {
-          const int tok = s.row0 + irow / P.rep, hq = s.head * P.rep + irow % P.rep;
+          const int ti = P.token_of(irow), tok = s.row0 + ti, hq = s.head * P.rep + irow - ti * P.rep;
           const float inv = ll > 0.f ? 1.f / ll : 0.f;
           *reinterpret_cast<uint2*>(P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD + d4) =
               make_uint2(down2<BF>(acc.x * inv, acc.y * inv), down2<BF>(acc.z * inv, acc.w * inv));
@@ -521,89 +523,165 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 // ---------------------------------------------------------------- join
 // The parts of the pair (tile) that CTA c of a kernel left open, in the order
 // of their keys: its own second part and the first parts of the CTAs after it.
-// The few-row kernel's parts are [row][dimension], a block joins 8 (16) rows at
-// a time; the tile kernel's are [4 dimensions][row], a block joins 32 rows.
-struct Joined {
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  __device__ __forceinline__ void add(float2 ml, float4 v) {
-    const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-    const float a = ex2(m - ref), f = ex2(ml.x - ref);
-    l = l * a + ml.y * f;
-    o.x = o.x * a + v.x * f; o.y = o.y * a + v.y * f;
-    o.z = o.z * a + v.z * f; o.w = o.w * a + v.w * f;
-    m = mn;
-  }
-  template <bool BF>
-  __device__ __forceinline__ uint2 out() const {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    return make_uint2(down2<BF>(o.x * inv, o.y * inv), down2<BF>(o.z * inv, o.w * inv));
-  }
-  __device__ __forceinline__ float lse() const {
-    return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-  }
-};
-
+// Latency bound: few bytes, read right after the launch that wrote them.
 constexpr int JOIN_ROWS = 32;  // of a tile, a block
+constexpr int JOIN_THREADS = 256;
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
 
 template <int HD, bool BF>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams P,
-                                                         const __grid_constant__ PagedParts A,
-                                                         const __grid_constant__ PagedParts B) {
-  constexpr int LPR = HD / 4;  // threads of a row
+__global__ void __launch_bounds__(JOIN_THREADS, 4) paged_join_kernel(const __grid_constant__ PagedAttnParams P,
+                                                                  const __grid_constant__ PagedParts A,
+                                                                  const __grid_constant__ PagedParts B) {
+  constexpr int LPR = HD / 4, WARPS = JOIN_THREADS / 32, E = HD / 32;
   __shared__ uint2 rows_out[JOIN_ROWS][LPR + 1];
+  __shared__ float shared_o[WARPS][HD];
+  __shared__ float2 shared_ml[WARPS];
   grid_launch_dependents();
-  grid_wait_prior();
-  const int tid = threadIdx.x, hqs = P.hkv * P.rep;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hqs = P.hkv * P.rep;
   if ((int)blockIdx.x < A.ctas) {
-    const int c = blockIdx.x;
-    const PartDesc d = A.desc[c];
-    if (d.parts == 0) return;
-    const int d4 = (tid % LPR) * 4;
-    for (int row = tid / LPR; row < d.rows; row += 256 / LPR) {
-      Joined j;
-      for (int k0 = 0; k0 < d.parts; k0 += 8) {  // eight parts' reads in flight
-        float2 ml[8];
-        float4 o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = min(k0 + i, d.parts - 1);
-          const int64_t at = (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * A.rt + row;
-          ml[i] = A.ml[at];
-          o[i] = *reinterpret_cast<const float4*>(A.o + at * HD + d4);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (k0 + i < d.parts) j.add(ml[i], o[i]);
+    // few-row kernel, parts [row][dimension]: a warp joins a row, lanes on the
+    // dimensions; where the rows are fewer than the warps, 2^sh warps take
+    // every 2^sh-th part.  A round trip to L2 takes most of a microsecond: the
+    // first N parts are read with the description, before it says how many
+    // there are (any part's place can be read).
+    // While the launch before still runs, the block goes through the same code
+    // once with what the workspace happens to hold and stores nothing: its
+    // instructions, which the last kernels have pushed out of the SM's caches,
+    // are fetched then (all reads here bypass L1).
+    constexpr int N = 5;
+    const int c = blockIdx.x, sh = P.join_shares, share = warp >> (3 - sh), step = WARPS >> sh;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass) grid_wait_prior();
+      PartDesc d;
+      *reinterpret_cast<int4*>(&d) = __ldcg(reinterpret_cast<const int4*>(A.desc + c));
+      if (!pass) {
+        d.rows = step;
+        d.parts = N;
       }
-      const int tok = d.row0 + row / P.rep, hq = d.head * P.rep + row % P.rep;
-      *reinterpret_cast<uint2*>(P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD + d4) = j.out<BF>();
-      if (P.lse && d4 == 0) P.lse[(int64_t)tok * hqs + hq] = j.lse();
+      for (int row0 = 0, rows = step; row0 < rows; row0 += step) {
+        const int row = row0 + (warp & (step - 1));
+        auto at = [&](int k) {
+          const int part = k == 0 ? 2 * c + 1 : 2 * min(c + k, A.ctas - 1);
+          return (int64_t)part * A.rt + row;
+        };
+        float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int i0 = 0, n = N; i0 < n; i0 += N) {
+          float2 ml[N];
+          float v[N][E];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int64_t x = at(share + ((i0 + i) << sh));
+            ml[i] = __ldcg(A.ml + x);
+            const float* src = A.o + x * HD + lane * E;
+            if constexpr (E == 4) *reinterpret_cast<float4*>(v[i]) = __ldcg(reinterpret_cast<const float4*>(src));
+            else *reinterpret_cast<float2*>(v[i]) = __ldcg(reinterpret_cast<const float2*>(src));
+          }
+          n = (d.parts - share + (1 << sh) - 1) >> sh;  // parts of this share
+          float mn = m;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (i0 + i < n) mn = fmaxf(mn, ml[i].x);
+          const float ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - ref);
+          l *= f0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] *= f0;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            if (i0 + i < n) {
+              const float f = ex2(ml[i].x - ref);
+              l += ml[i].y * f;
+#pragma unroll
+              for (int e = 0; e < E; ++e) o[e] += v[i][e] * f;
+            }
+          }
+          m = mn;
+        }
+        if (d.parts == 0) return;
+        rows = d.rows;
+        if (sh > 0) {  // (one pass over the rows)
+#pragma unroll
+          for (int e = 0; e < E; ++e) shared_o[warp][lane * E + e] = o[e];
+          if (lane == 0) shared_ml[warp] = make_float2(m, l);
+          __syncthreads();
+          float mm = -INFINITY;
+          for (int s = 0; s < 1 << sh; ++s) mm = fmaxf(mm, shared_ml[(warp & (step - 1)) + s * step].x);
+          const float ref = mm == -INFINITY ? 0.f : mm;
+          l = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = 0.f;
+          for (int s = 0; s < 1 << sh; ++s) {
+            const int w = (warp & (step - 1)) + s * step;
+            const float f = ex2(shared_ml[w].x - ref);
+            l += shared_ml[w].y * f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += shared_o[w][lane * E + e] * f;
+          }
+          m = mm;
+          __syncthreads();
+        }
+        if (pass && row < d.rows && share == 0) {
+          const int t = P.token_of(row), hq = d.head * P.rep + row - t * P.rep;
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(P.out + (int64_t)(d.row0 + t) * P.o_stride + (int64_t)hq * HD) + lane * (E / 2);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) dst[e / 2] = down2<BF>(o[e] * inv, o[e + 1] * inv);
+          if (P.lse && lane == 0) P.lse[(int64_t)(d.row0 + t) * hqs + hq] = lse_of(m, l);
+        }
+      }
     }
     return;
   }
-  const int per = B.rt / JOIN_ROWS, c = (blockIdx.x - A.ctas) / per;
-  const int row0 = ((blockIdx.x - A.ctas) % per) * JOIN_ROWS, lane = tid & 31, row = row0 + lane;
+  grid_wait_prior();
+  // tile kernel, parts [4 dimensions][row]: a block joins 32 rows, lanes on the
+  // rows, each warp Q groups of four dimensions at once
+  constexpr int Q = LPR / WARPS;
+  const int per = B.rt / JOIN_ROWS, b = blockIdx.x - A.ctas, c = b / per, row0 = (b - c * per) * JOIN_ROWS;
+  const int row = row0 + lane;
   const PartDesc d = B.desc[c];
   if (d.parts == 0 || row0 >= d.rows) return;
-#pragma unroll 1
-  for (int q = tid >> 5; q < LPR; q += 8) {  // four dimensions a warp, lanes on rows
-    Joined j;
-#pragma unroll 4
-    for (int k = 0; k < d.parts; ++k) {
-      const int64_t part = k == 0 ? 2 * c + 1 : 2 * (c + k);
-      j.add(B.ml[part * B.rt + row], *reinterpret_cast<const float4*>(B.o + part * B.rt * HD + (q * B.rt + row) * 4));
+  float m = -INFINITY, l = 0.f;
+  float4 o[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = 0; k < d.parts; ++k) {
+    const int64_t part = k == 0 ? 2 * c + 1 : 2 * (c + k);
+    const float2 ml = B.ml[part * B.rt + row];
+    float4 v[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      v[q] = *reinterpret_cast<const float4*>(B.o + part * B.rt * HD + ((warp * Q + q) * B.rt + row) * 4);
+    const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+    const float x = ex2(m - ref), f = ex2(ml.x - ref);
+    l = l * x + ml.y * f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      o[q].x = o[q].x * x + v[q].x * f; o[q].y = o[q].y * x + v[q].y * f;
+      o[q].z = o[q].z * x + v[q].z * f; o[q].w = o[q].w * x + v[q].w * f;
     }
-    rows_out[lane][q] = j.out<BF>();
-    if (q == 0 && P.lse && row < d.rows)
-      P.lse[(int64_t)(d.row0 + row / P.rep) * hqs + d.head * P.rep + row % P.rep] = j.lse();
+    m = mn;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    rows_out[lane][warp * Q + q] = make_uint2(down2<BF>(o[q].x * inv, o[q].y * inv), down2<BF>(o[q].z * inv, o[q].w * inv));
+  if (warp == 0 && P.lse && row < d.rows) {
+    const int t = P.token_of(row);
+    P.lse[(int64_t)(d.row0 + t) * hqs + d.head * P.rep + row - t * P.rep] = lse_of(m, l);
   }
   __syncthreads();
-  for (int i = tid; i < JOIN_ROWS * LPR; i += 256) {
+  for (int i = tid; i < JOIN_ROWS * LPR; i += JOIN_THREADS) {
     const int rw = row0 + i / LPR, q = i % LPR;
     if (rw >= d.rows) break;
-    *reinterpret_cast<uint2*>(P.out + (int64_t)(d.row0 + rw / P.rep) * P.o_stride +
-                              (int64_t)(d.head * P.rep + rw % P.rep) * HD + q * 4) = rows_out[i / LPR][q];
+    const int t = P.token_of(rw);
+    *reinterpret_cast<uint2*>(P.out + (int64_t)(d.row0 + t) * P.o_stride +
+                              (int64_t)(d.head * P.rep + rw - t * P.rep) * HD + q * 4) = rows_out[i / LPR][q];
   }
 }
 
@@ -639,10 +717,10 @@ cudaError_t paged_join_launch(const PagedAttnParams& p, const PagedParts& a, con
                               bool bf, cudaStream_t st) {
   const int grid = a.ctas + b.ctas * (b.rt / JOIN_ROWS);
   if (d == 128)
-    return bf ? paged_launch(paged_join_kernel<128, true>, grid, 256, 0, st, p, a, b)
-              : paged_launch(paged_join_kernel<128, false>, grid, 256, 0, st, p, a, b);
-  return bf ? paged_launch(paged_join_kernel<64, true>, grid, 256, 0, st, p, a, b)
-            : paged_launch(paged_join_kernel<64, false>, grid, 256, 0, st, p, a, b);
+    return bf ? paged_launch(paged_join_kernel<128, true>, grid, JOIN_THREADS, 0, st, p, a, b)
+              : paged_launch(paged_join_kernel<128, false>, grid, JOIN_THREADS, 0, st, p, a, b);
+  return bf ? paged_launch(paged_join_kernel<64, true>, grid, JOIN_THREADS, 0, st, p, a, b)
+            : paged_launch(paged_join_kernel<64, false>, grid, JOIN_THREADS, 0, st, p, a, b);
 }
 
 }  // namespace mk
