@@ -486,7 +486,7 @@ int mk_rope_init(mk_rope *rope, int rotary_dim, double theta, const double *inv_
  *   rope            or NULL (no rotation; positions is then not read)
  *   positions       device int32 [n_axes][...], pos_stride words from axis to axis
  *   slots           device int32 [n_tokens]: page * page_size + offset.  A token of
- *                   slot < 0 is left out (nothing of it is read or written).  One
+ *                   slot < 0 is left out (none of its outputs is written).  One
  *                   past the last page likewise, with MK_ERR_BOUNDS latched.  No two
  *                   tokens of a call may share a slot.
  * n_tokens >= 0 (0: nothing is launched). */

@@ -148,7 +148,11 @@ def slots_and_caches(t, hkv, page, d, typ, layout, rng):
     (37, 32, 8, 128, 128, 3, True, True, 32, "ph", "bf16"), (70, 7, 1, 64, 32, 2, True, False, 64, "pad", "fp16"),
     (129, 4, 2, 64, 64, 4, False, True, 128, "pad", "bf16"), (300, 12, 4, 128, 64, 1, False, False, 16, "hp", "fp16"),
     (33, 5, 5, 128, 16, 1, True, True, 16, "hp", "bf16"), (33, 6, 3, 128, 96, 3, True, False, 32, "pad", "bf16"),
-    (65, 8, 8, 64, 48, 1, False, True, 16, "ph", "fp16"), (20, 40, 8, 128, 0, 1, True, True, 16, "hp", "bf16")])
+    (65, 8, 8, 64, 48, 1, False, True, 16, "ph", "fp16"), (20, 40, 8, 128, 0, 1, True, True, 16, "hp", "bf16"),
+    # many tokens: rings of 32, 16 and 8 rows that go round, rows that the ring does not take
+    (2500, 32, 8, 128, 128, 3, True, True, 64, "hp", "bf16"), (9000, 2, 1, 64, 64, 1, False, False, 16, "ph", "fp16"),
+    (1999, 6, 3, 64, 32, 2, True, False, 32, "pad", "bf16"), (3001, 64, 16, 128, 128, 1, True, True, 16, "hp", "fp16"),
+    (400, 96, 16, 128, 64, 4, True, False, 16, "ph", "bf16"), (305, 4, 4, 128, 0, 1, False, True, 256, "hp", "bf16")])
 def test_append_matches_the_oracle(t, hq, hkv, d, rot, axes, norm, packed, page, layout, typ):
     rng = np.random.default_rng(t * 7 + hq)
     typ = TYPES[typ]
@@ -198,6 +202,18 @@ def test_append_matches_the_oracle(t, hq, hkv, d, rot, axes, norm, packed, page,
     kc[at[sel] // page, :, at[sel] % page] = 0
     vc[at[sel] // page, :, at[sel] % page] = 0
     assert torch.equal(now, whole)
+
+
+@pytest.mark.parametrize("slots_of", [lambda rng, t: np.full(t, -1), lambda rng, t: np.where(rng.random(t) < 0.5, -1, 2 ** 31 - 1)])
+def test_append_of_left_out_and_refused_tokens_writes_nothing(slots_of):
+    for t in (40, 3000):
+        g = torch.Generator().manual_seed(t)
+        q, k, v = (torch.randn(t, h, 64, generator=g).to(torch.float16).to(DEV) for h in (4, 2, 2))
+        kc, vc = (torch.full((9, 2, 16, 64), 2.0, dtype=torch.float16, device=DEV) for _ in range(2))
+        cache, out, slots = mk.PagedCache(kc, vc, n_q_heads=4), torch.full_like(q, 4.0), slots_of(np.random.default_rng(t), t)
+        cache.append(q, k, v, ints(slots), ints(np.arange(t)), mk.Rope(64), q_out=out)
+        assert cache.status() == (mk.MK_ERR_BOUNDS if (slots > 0).any() else 0)
+        assert (out == 4).all() and (kc == 2).all() and (vc == 2).all()
 
 
 def test_append_in_place_and_far_slots_refused():

@@ -10,6 +10,11 @@
 namespace mk {
 namespace {
 
+cudaError_t device_sms(int* device, int* sms) {
+  const cudaError_t e = cudaGetDevice(device);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *device);
+}
+
 // ---------------------------------------------------------------- tables
 // Every CTA scans all requests (n <= 4096: a few KB, from L2) into shared
 // memory, so that no CTA waits on another, and then fills its share of the
@@ -156,96 +161,322 @@ __global__ void __launch_bounds__(PT_THREADS) paged_tables_kernel(const PagedTab
 // ---------------------------------------------------------------- append
 // One pass: every head row is read once, normed and turned in registers and
 // written once (HBM bound).  Lane j of a group of HD/16 lanes holds the two
-// 16-byte chunks j and j + rotary/16 of a head, whose elements are each
-// other's pairs, so the rotation needs no exchange.
-constexpr int PA_THREADS = 256;
+// 16-byte chunks j and j + rotary/16 of a head, whose elements are each other's
+// pairs, so the rotation needs no exchange; a warp takes 32 / (HD/16) heads at a
+// time, and a lane's cosines, sines and gains are the same for all of them.
+constexpr int PA_THREADS = 256, PA_WARPS = PA_THREADS / 32;
 
+// cos and sin of a pair's angle.  Whole turns drop out of the low 64 bits of the
+// product; the top 32 of those, signed, are the angle in [-1/2, 1/2) turns to
+// 2^-33.
+__device__ __forceinline__ float2 pair_turn(int pos, uint64_t turn) {
+  const int32_t frac = (int32_t)(((uint64_t)(int64_t)pos * turn) >> 32);
+  float s, c;
+  sincospif((float)frac * 4.656612873077393e-10f, &s, &c);  // 2 * frac / 2^32 half turns
+  return make_float2(c, s);
+}
+
+// A lane's share of a head: two chunks, the angles of their pairs (1, 0 where
+// they do not turn) and the gains.  Packed pairs of floats, two IEEE operations
+// an instruction.
+template <int HD, bool BF>
+struct HeadLane {
+  static constexpr int G = HD / 16;
+  int ca, cb;
+  bool turn;
+  u64 c[4], s[4];  // cos, sin of the eight pairs
+  uint4 gq[2], gk[2];
+  static __device__ __forceinline__ u64 widen(uint32_t w) {
+    const float2 f = up2<BF>(w);
+    return pack_f32x2(f.x, f.y);
+  }
+  static __device__ __forceinline__ uint32_t narrow(u64 x) {
+    return down2<BF>(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
+  }
+  __device__ __forceinline__ HeadLane(const PagedAppendParams& P, int lane) {
+    const int j = lane % G, hc = P.rope.rotary_dim / 16;
+    turn = j < hc;
+    ca = turn ? j : 2 * hc + 2 * (j - hc);
+    cb = turn ? j + hc : ca + 1;
+    gq[0] = gq[1] = gk[0] = gk[1] = make_uint4(0, 0, 0, 0);
+    if (P.q_gain) {
+      gq[0] = reinterpret_cast<const uint4*>(P.q_gain)[ca];
+      gq[1] = reinterpret_cast<const uint4*>(P.q_gain)[cb];
+    }
+    if (P.k_gain) {
+      gk[0] = reinterpret_cast<const uint4*>(P.k_gain)[ca];
+      gk[1] = reinterpret_cast<const uint4*>(P.k_gain)[cb];
+    }
+  }
+  // cs holds pair p at (p % 8) * G + p / 8: a lane's eight are G apart, the
+  // lanes of a head end to end
+  static __device__ __forceinline__ int place(int pair) { return (pair & 7) * G + (pair >> 3); }
+  __device__ __forceinline__ void angles(const float2* cs, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 x = make_float2(1.f, 0.f), y = x;
+      if (turn) {
+        x = cs[2 * i * G + lane % G];
+        y = cs[(2 * i + 1) * G + lane % G];
+      }
+      c[i] = pack_f32x2(x.x, y.x);
+      s[i] = pack_f32x2(x.y, y.y);
+    }
+  }
+  // Norm and turn a head's chunks in place (whole warp; is_q: a query head).
+  __device__ __forceinline__ void apply(const PagedAppendParams& P, uint4& wa, uint4& wb, bool is_q) {
+    const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
+    u64 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = widen(ua[i]);
+      b[i] = widen(ub[i]);
+    }
+    if (P.q_gain || P.k_gain) {
+      u64 acc = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc = fma_f32x2(a[i], a[i], fma_f32x2(b[i], b[i], acc));
+      float ss = pair_sum(acc);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (is_q ? P.q_gain != nullptr : P.k_gain != nullptr) {
+        const float inv = rsqrtf(ss * (1.f / HD) + P.eps);
+        const u64 inv2 = pack_f32x2(inv, inv);
+        const uint4 x = is_q ? gq[0] : gk[0], y = is_q ? gq[1] : gk[1];
+        const uint32_t ga[4] = {x.x, x.y, x.z, x.w}, gb[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = mul_f32x2(mul_f32x2(a[i], inv2), widen(ga[i]));
+          b[i] = mul_f32x2(mul_f32x2(b[i], inv2), widen(gb[i]));
+        }
+      }
+    }
+    uint32_t oa[4], ob[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u64 minus = s[i] ^ 0x8000000080000000ull;
+      oa[i] = narrow(fma_f32x2(b[i], minus, mul_f32x2(a[i], c[i])));
+      ob[i] = narrow(fma_f32x2(a[i], s[i], mul_f32x2(b[i], c[i])));
+    }
+    wa = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+    wb = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+  }
+};
+
+// Where the heads of a token go.
+template <int HD>
+struct TokenOut {
+  uint16_t *q, *k, *v;
+  __device__ __forceinline__ TokenOut(const PagedAppendParams& P, int t, int slot) {
+    const int64_t at = (int64_t)(slot >> P.page_shift) * P.page_stride +
+                       (int64_t)(slot & ((1 << P.page_shift) - 1)) * P.token_stride;
+    q = P.q_out + t * P.qo_stride;
+    k = P.kc + at - P.hq * P.head_stride;
+    v = P.vc + at - (P.hq + P.hkv) * P.head_stride;
+  }
+  __device__ __forceinline__ uint4* head(const PagedAppendParams& P, int h) const {
+    return reinterpret_cast<uint4*>(h < P.hq ? q + h * HD : (h < P.hq + P.hkv ? k : v) + h * P.head_stride);
+  }
+};
+
+// Few tokens: a block each.  Latency bound (3.5 us for 32 tokens of 32 + 16
+// heads of 128): every warp works the angles out for itself, while its first
+// rows are on their way, so that no barrier stands between.
 template <int HD, bool BF>
 __global__ void __launch_bounds__(PA_THREADS) paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
-  __shared__ float2 cs[HD / 2];  // cos, sin of the token's pairs
-  const int t = blockIdx.x, tid = threadIdx.x;
+  using Lane = HeadLane<HD, BF>;
+  constexpr int HPW = 32 / Lane::G, BATCH = 2;
+  __shared__ float2 cs[PA_WARPS][HD / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.x, half = P.rope.rotary_dim / 2;
   grid_launch_dependents();
   grid_wait_prior();
-  const int slot = P.slot[t];
-  if (slot < 0) return;
-  if (slot >= P.n_slots) {
-    if (tid == 0) latch(P.status, MK_ERR_BOUNDS);
-    return;
-  }
-  const int half = P.rope.rotary_dim / 2;
-  if (tid < half) {
-    const int pos = P.pos[P.rope.axis[tid] * P.pos_stride + t];
-    // whole turns drop out of the low 64 bits; the top 32 of those, signed, are
-    // the angle in [-1/2, 1/2) turns to 2^-33
-    const int32_t frac = (int32_t)(((uint64_t)(int64_t)pos * P.rope.turn[tid]) >> 32);
-    float s, c;
-    sincospif((float)frac * 4.656612873077393e-10f, &s, &c);  // 2 * frac / 2^32 half turns
-    cs[tid] = make_float2(c, s);
-  }
-  __syncthreads();
-  constexpr int G = HD / 16;  // lanes of a head
-  const int j = tid % G, hc = half / 8;
-  const bool turn = j < hc;
-  // chunks of this lane: a pair of the rotated part, or two of the rest
-  const int ca = turn ? j : 2 * hc + 2 * (j - hc), cb = turn ? j + hc : ca + 1;
-  const int heads = P.hq + 2 * P.hkv;
-  const int page = slot >> P.page_shift, off = slot & ((1 << P.page_shift) - 1);
-  const int64_t crow = (int64_t)page * P.page_stride + (int64_t)off * P.token_stride;
-  for (int h0 = 0; h0 < heads; h0 += PA_THREADS / G) {
-    const int h = h0 + tid / G;
-    const bool live = h < heads;
-    const bool is_q = h < P.hq, is_k = !is_q && h < P.hq + P.hkv;
-    const uint16_t* src = is_q ? P.q + t * P.q_stride + (int64_t)h * HD
-                         : is_k ? P.k + t * P.k_stride + (int64_t)(h - P.hq) * HD
-                                : P.v + t * P.v_stride + (int64_t)(h - P.hq - P.hkv) * HD;
-    uint16_t* dst = is_q ? P.q_out + t * P.qo_stride + (int64_t)h * HD
-                   : is_k ? P.kc + crow + (int64_t)(h - P.hq) * P.head_stride
-                          : P.vc + crow + (int64_t)(h - P.hq - P.hkv) * P.head_stride;
-    uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
-    if (live) {
-      wa = reinterpret_cast<const uint4*>(src)[ca];
-      wb = reinterpret_cast<const uint4*>(src)[cb];
-    }
-    const uint16_t* gain = is_q ? P.q_gain : is_k ? P.k_gain : nullptr;
-    float a[8], b[8];
-    up8<BF>(wa, a);
-    up8<BF>(wb, b);
-    float ss = 0.f;
+  const int heads = P.hq + 2 * P.hkv, slot = P.slot[t];
+  const uint16_t *q = P.q + t * P.q_stride, *k = P.k + t * P.k_stride, *v = P.v + t * P.v_stride;
+  Lane L(P, lane);
+  for (int h0 = warp * HPW; h0 < heads; h0 += PA_WARPS * HPW * BATCH) {
+    uint4 wa[BATCH], wb[BATCH];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
-#pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (gain) {
-      const float inv = rsqrtf(ss / HD + P.eps);
-      float ga[8], gb[8];
-      up8<BF>(reinterpret_cast<const uint4*>(gain)[ca], ga);
-      up8<BF>(reinterpret_cast<const uint4*>(gain)[cb], gb);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] *= inv * ga[i];
-        b[i] *= inv * gb[i];
+    for (int u = 0; u < BATCH; ++u) {
+      const int h = h0 + u * PA_WARPS * HPW + lane / Lane::G;
+      wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
+      if (h < heads) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            h < P.hq ? q + h * HD : h < P.hq + P.hkv ? k + (h - P.hq) * HD : v + (h - P.hq - P.hkv) * HD);
+        wa[u] = src[L.ca];
+        wb[u] = src[L.cb];
       }
     }
-    if (turn && (is_q || is_k)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 w = cs[8 * j + i];
-        const float x = a[i], y = b[i];
-        a[i] = x * w.x - y * w.y;
-        b[i] = y * w.x + x * w.y;
+    if (h0 == warp * HPW) {
+      for (int i = lane; i < half; i += 32)
+        cs[warp][Lane::place(i)] = pair_turn(P.pos[P.rope.axis[i] * P.pos_stride + t], P.rope.turn[i]);
+      __syncwarp();
+      L.angles(cs[warp], lane);
+      if (slot < 0) return;  // left out
+      if (slot >= P.n_slots) {
+        if (lane == 0) latch(P.status, MK_ERR_BOUNDS);
+        return;
       }
     }
-    if (live) {
-      reinterpret_cast<uint4*>(dst)[ca] = down8<BF>(a);
-      reinterpret_cast<uint4*>(dst)[cb] = down8<BF>(b);
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int hb = h0 + u * PA_WARPS * HPW, h = hb + lane / Lane::G;  // the step's first head, this lane's
+      if (hb >= heads) break;
+      uint4 a = wa[u], b = wb[u];
+      if (hb < P.hq + P.hkv) L.apply(P, a, b, h < P.hq);
+      if (h < heads) {
+        const bool value = h >= P.hq + P.hkv;  // values stay as they are
+        uint4* dst = TokenOut<HD>(P, t, slot).head(P, h);
+        dst[L.ca] = value ? wa[u] : a;
+        dst[L.cb] = value ? wb[u] : b;
+      }
     }
   }
 }
 
-template <int HD>
-cudaError_t append_launch(const PagedAppendParams& p, int dtype, cudaStream_t st) {
-  return dtype == MK_BF16 ? paged_launch(paged_append_kernel<HD, true>, p.n_tokens, PA_THREADS, 0, st, p)
-                          : paged_launch(paged_append_kernel<HD, false>, p.n_tokens, PA_THREADS, 0, st, p);
+// Many tokens: persistent blocks, one per SM.  A warp loads whole tokens into a
+// ring in shared memory (bulk copies: what is in flight costs no registers and
+// is there however the other warps are placed), teams of four warps take the
+// tokens in turn.  (Rows loaded to registers, three 16-byte pairs a lane in
+// flight: 46-49 us for 8190 tokens of 32 + 16 heads of 128.)
+constexpr int PR_WARPS = 2, PR_LOADERS = 4;  // warps of a team; loading warps
+constexpr int PR_TEAMS = 16 / PR_WARPS, PR_TEAM = 32 * PR_WARPS;
+constexpr int PR_THREADS = PR_TEAMS * PR_TEAM + 32 * PR_LOADERS, PR_MOST = 32;
+
+struct PrSmem {
+  uint64_t full[PR_MOST], empty[PR_MOST];
+  int slot[PR_MOST];
+  int dead, pad[3];
+  float2 cs[PR_TEAMS][2][64];
+};
+// Depth of the ring for rows of `row` bytes: a multiple of the teams and of the
+// loading warps, so that a slot always has the same ones.  (One that came to a
+// slot only every other round would not see all phases of its barriers, and
+// could take the last but one for the one it waits for.)  0: the other kernel.
+static_assert(PR_TEAMS % PR_LOADERS == 0 && PR_MOST % PR_TEAMS == 0, "ring");
+inline int ring_depth(int row) {
+  return std::min(PR_MOST, (int)((232448 - sizeof(PrSmem)) / row) / PR_TEAMS * PR_TEAMS);
+}
+
+template <int HD, bool BF>
+__global__ void __launch_bounds__(PR_THREADS, 1)
+    paged_append_ring_kernel(const __grid_constant__ PagedAppendParams P, int depth) {
+  using Lane = HeadLane<HD, BF>;
+  constexpr int HPW = 32 / Lane::G;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  PrSmem& S = *reinterpret_cast<PrSmem*>(smem_raw);
+  uint8_t* ring = smem_raw + sizeof(PrSmem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = P.rope.rotary_dim / 2;
+  const int heads = P.hq + 2 * P.hkv, row = heads * HD * 2;
+  volatile int* dead = &S.dead;
+  if (tid == 0) {
+    for (int s = 0; s < depth; ++s) {
+      mbar_init(&S.full[s], 1);
+      mbar_init(&S.empty[s], PR_WARPS);
+    }
+    S.dead = 0;
+    fence_mbar_init();
+  }
+  grid_launch_dependents();
+  grid_wait_prior();
+  __syncthreads();
+  // tokens blockIdx.x + i gridDim.x, i = 0, 1, ...
+  const int mine = (P.n_tokens - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  if (warp >= PR_TEAMS * PR_WARPS) {
+    // Each loading warp takes every PR_LOADERS-th token (a turn of the loop
+    // costs it a quarter of a microsecond or more); it reads 32 of its tokens'
+    // slots at once, and lanes 0, 1, 2 copy q, k, v.
+    const int first = warp - PR_TEAMS * PR_WARPS;
+    auto slot_of = [&](int n) {  // of this warp's n-th token
+      const int i = first + n * PR_LOADERS;
+      return i < mine ? P.slot[blockIdx.x + i * gridDim.x] : -1;
+    };
+    int s = first, slots = -1, ahead = slot_of(lane);
+    uint32_t phase = 1;
+    const uint16_t* src = lane == 0 ? P.q : lane == 1 ? P.k : P.v;
+    const int64_t stride = lane == 0 ? P.q_stride : lane == 1 ? P.k_stride : P.v_stride;
+    const int bytes = (lane == 0 ? P.hq : P.hkv) * HD * 2;
+    const int dst = (lane == 0 ? 0 : lane == 1 ? P.hq : P.hq + P.hkv) * HD * 2;
+    for (int i = first, n = 0; i < mine; i += PR_LOADERS, ++n) {
+      if ((n & 31) == 0) {
+        slots = ahead;
+        ahead = slot_of(n + 32 + lane);
+      }
+      const int t = blockIdx.x + i * gridDim.x, slot = __shfl_sync(0xffffffffu, slots, n & 31);
+      wait_phase(&S.empty[s], phase, dead, P.status);
+      if (*dead) break;
+      const bool use = slot >= 0 && slot < P.n_slots;
+      if (lane == 0) {
+        if (slot >= P.n_slots) latch(P.status, MK_ERR_BOUNDS);
+        S.slot[s] = use ? slot : -1;
+        if (use) mbar_arrive_expect_tx(&S.full[s], row);
+        else mbar_arrive(&S.full[s]);
+      }
+      __syncwarp();
+      if (use && lane < 3) bulk_in(ring + (size_t)s * row + dst, src + t * stride, bytes, &S.full[s]);
+      s += PR_LOADERS;
+      if (s >= depth) {
+        s -= depth;
+        phase ^= 1;
+      }
+    }
+    if (*dead) {
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 1000000ull) {  // the copies in flight land
+      }
+    }
+    return;
+  }
+  const int team = warp / PR_WARPS, sub = warp % PR_WARPS, tt = tid % PR_TEAM;
+  Lane L(P, lane);
+  // this thread's pair (read once: the words lie in the constant bank, which
+  // gives a warp's 32 different words one after another)
+  const bool turns = tt < half;
+  const uint64_t turn = turns ? P.rope.turn[tt] : 0;
+  const int32_t* pos_row = P.pos + (turns ? P.rope.axis[tt] * P.pos_stride : 0) + blockIdx.x;
+  auto position = [&](int i) { return turns && i < mine ? pos_row[i * gridDim.x] : 0; };
+  int pos = position(team), buf = 0;
+  for (int i = team; i < mine; i += PR_TEAMS, buf ^= 1) {
+    const int t = blockIdx.x + i * gridDim.x, s = i % depth;
+    if (turns) S.cs[team][buf][Lane::place(tt)] = pair_turn(pos, turn);
+    pos = position(i + PR_TEAMS);
+    named_bar(1 + team, PR_TEAM);
+    L.angles(S.cs[team][buf], lane);
+    wait_phase(&S.full[s], (i / depth) & 1, dead, P.status);
+    const int slot = S.slot[s];
+    if (slot >= 0 && !*dead) {
+      const uint8_t* src = ring + (size_t)s * row;
+      const TokenOut<HD> out(P, t, slot);
+#pragma unroll 1
+      for (int hb = sub * HPW; hb < heads; hb += PR_WARPS * HPW) {
+        const int h = hb + lane / Lane::G;
+        const uint4* w = reinterpret_cast<const uint4*>(src + min(h, heads - 1) * HD * 2);
+        const uint4 wa = w[L.ca], wb = w[L.cb];
+        uint4 a = wa, b = wb;
+        if (hb < P.hq + P.hkv) L.apply(P, a, b, h < P.hq);
+        if (h < heads) {
+          const bool value = h >= P.hq + P.hkv;
+          uint4* dst = out.head(P, h);
+          dst[L.ca] = value ? wa : a;
+          dst[L.cb] = value ? wb : b;
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.empty[s]);
+  }
+}
+
+// The ring from two tokens an SM on (400 tokens of 32 + 16 heads of 128: 5.6 us
+// against 7.2 us; 304: 5.3 against 4.8), for rows of which it holds eight.
+template <int HD, bool BF>
+cudaError_t append_launch(const PagedAppendParams& p, int device, int sms, cudaStream_t st) {
+  const int row = (p.hq + 2 * p.hkv) * HD * 2, depth = ring_depth(row);
+  if (p.n_tokens <= 2 * sms || depth == 0)
+    return paged_launch(paged_append_kernel<HD, BF>, p.n_tokens, PA_THREADS, 0, st, p);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = paged_prepare((const void*)paged_append_ring_kernel<HD, BF>, 232448, 0, device, &ready);
+  if (e != cudaSuccess) return e;
+  return paged_launch(paged_append_ring_kernel<HD, BF>, sms, PR_THREADS, (int)sizeof(PrSmem) + depth * row, st, p, depth);
 }
 
 // ---------------------------------------------------------------- attention
@@ -255,8 +486,7 @@ cudaError_t append_launch(const PagedAppendParams& p, int dtype, cudaStream_t st
 cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool bf, void* workspace,
                              cudaStream_t st) {
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   p.device = dev;
   p.rep_inv = (65536 + p.rep - 1) / p.rep;
@@ -436,8 +666,15 @@ extern "C" int mk_paged_append(const mk_paged_cache* c, const void* q, int64_t q
   p.n_slots = c->n_pages * c->page_size; p.page_shift = log2_page(c->page_size);
   p.eps = eps;
   if (rope) p.rope = *rope;
-  const cudaError_t e = c->head_dim == 128 ? append_launch<128>(p, c->dtype, (cudaStream_t)stream)
-                                           : append_launch<64>(p, c->dtype, (cudaStream_t)stream);
+  cudaStream_t st = (cudaStream_t)stream;
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e == cudaSuccess) {
+    if (c->dtype == MK_BF16)
+      e = c->head_dim == 128 ? append_launch<128, true>(p, dev, sms, st) : append_launch<64, true>(p, dev, sms, st);
+    else
+      e = c->head_dim == 128 ? append_launch<128, false>(p, dev, sms, st) : append_launch<64, false>(p, dev, sms, st);
+  }
   return done(e);
 }
 

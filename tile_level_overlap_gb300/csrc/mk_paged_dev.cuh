@@ -42,20 +42,10 @@ __device__ __forceinline__ uint32_t down2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-template <bool BF>
-__device__ __forceinline__ void up8(const uint4 w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = up2<BF>(u[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-template <bool BF>
-__device__ __forceinline__ uint4 down8(const float (&x)[8]) {
-  return make_uint4(down2<BF>(x[0], x[1]), down2<BF>(x[2], x[3]), down2<BF>(x[4], x[5]),
-                    down2<BF>(x[6], x[7]));
+__device__ __forceinline__ u64 mul_f32x2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -99,7 +89,15 @@ __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, volat
   }
 }
 
-// ---------------------------------------------------------------- page loads
+// ---------------------------------------------------------------- loads
+// Untiled copy into shared memory (addresses and size: multiples of 16 bytes).
+__device__ __forceinline__ void bulk_in(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 // Box of 64 elements x tokens x parts of one head and page, from part `part` on
 // (the map's dimensions: element, token, part, head, page).  A page outside the
 // map reads as zeros.

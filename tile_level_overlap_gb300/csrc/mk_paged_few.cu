@@ -91,15 +91,6 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
   }
 }
 
-// Untiled copy of one query row into shared memory.
-__device__ __forceinline__ void bulk_row(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Whether any of the barrier's threads says so.
 __device__ __forceinline__ bool any_of(int id, int n, bool x) {
   uint32_t r;
@@ -241,7 +232,7 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
       }
       __syncwarp();
       if (lane < rows)
-        bulk_row(smem + C::o_q + (slot * RT + lane) * C::QROW,
+        bulk_in(smem + C::o_q + (slot * RT + lane) * C::QROW,
                  P.q + (int64_t)(q.row0 + my_tok) * P.q_stride + (int64_t)(head * P.rep + lane - my_tok * P.rep) * HD,
                  HD * 2, &qfull[slot]);
       if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
