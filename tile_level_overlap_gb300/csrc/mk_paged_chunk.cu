@@ -9,8 +9,8 @@
 // joined as in the few-row kernel.
 //
 // Warps of a CTA: one loads (TMA: queries, then K and V blocks page by page,
-// 128-byte swizzle), one issues tcgen05.mma, two groups of four own a half each
-// (thread = row).  Per half and block: S = Q K^T into 128 TMEM columns; its
+// 128-byte swizzle), one for each half issues tcgen05.mma, two groups of four own
+// a half each (thread = row).  Per half and block: S = Q K^T into 128 TMEM columns; its
 // group reads the row, masks it where the block crosses a bound, exponentiates
 // relative to a running maximum and writes P over S in the cache's type; O += P V
 // with P read from TMEM.  The two halves alternate on the tensor cores: while
@@ -27,7 +27,7 @@ namespace mk {
 namespace {
 
 constexpr int PC_THREADS = 384;
-constexpr int PC_LOAD = 8, PC_MMA = 9;       // warps; 0-3 and 4-7 own the halves
+constexpr int PC_LOAD = 8, PC_MMA = 9;       // warps (9, 10: products); 0-3 and 4-7 own the halves
 constexpr int PC_REGS = 168, PC_REGS_SOFT = 216, PC_REGS_REST = 72;
 static_assert(2 * PC_REGS_SOFT + PC_REGS_REST == 3 * PC_REGS, "registers of the three warpgroups");
 // What a tile costs beside its blocks (filling the pipeline, writing the rows),
@@ -115,13 +115,13 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);
     }
     mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
+    mbar_init(qempty, 2);
     for (int s = 0; s < C::SLOTS; ++s) {
       mbar_init(&mfull[s], 1);
-      mbar_init(&mempty[s], 9);
+      mbar_init(&mempty[s], 10);
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sfull[h], 1);
@@ -317,77 +317,84 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         meta[slot].nblk = 0;
         mbar_arrive(&mfull[slot]);
       }
-    } else if (warp == PC_MMA) {
+    } else if (warp >= PC_MMA && warp < PC_MMA + 2) {
       // ---------------------------------------------------------- products
-      // The whole warp walks the run (addresses and descriptors stay in uniform
+      // A warp for each half: to issue a half's 16 products and their commits
+      // takes one thread most of the time that the products of both take.  The
+      // whole warp walks the run (addresses and descriptors stay in uniform
       // registers); one elected thread issues.
+      const int h = warp - PC_MMA;
       constexpr uint32_t id_s = idesc_f16(128, 128, BF), id_o = idesc_f16(128, HD, BF, true);
-      const uint64_t dq = sdesc_sw128(smem_u32(smem)), dk = sdesc_sw128(smem_u32(smem + C::o_kv));
+      const uint64_t dq = sdesc_sw128(smem_u32(smem + h * C::TILE)), dk = sdesc_sw128(smem_u32(smem + C::o_kv));
       const uint64_t dv = sdesc_sw128_mn(smem_u32(smem + C::o_kv), 16384u);
-      uint32_t blkn = 0, pn[2] = {0, 0}, qn = 0;  // blocks loaded, P's and tiles seen
+      const uint32_t t_s = T_S + 128u * h, t_o = T_O + 128u * h;
+      uint32_t blkn = 0, pn = 0, qn = 0;  // blocks loaded, P's and tiles seen
       int slot = 0;
       uint32_t mphase = 0;
       auto kst = [](uint32_t b) { return (2 * b) % ST; };
       auto kph = [](uint32_t b) { return ((2 * b) / ST) & 1; };
-      // S of half h from the K block in stage st
-      auto s_product = [&](int h, uint32_t st) {
+      // S from the K block in stage st
+      auto s_product = [&](uint32_t st) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint32_t off = ((uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u) >> 4;
-          tc_mma(T_S + 128u * h, dq + (h * C::TILE / 16 + off), dk + (st * (C::TILE / 16) + off), id_s, kk != 0);
+          tc_mma(t_s, dq + off, dk + (st * (C::TILE / 16) + off), id_s, kk != 0);
         }
         tc_commit(&sfull[h]);
       };
       for (;;) {
         wait_phase(&mfull[slot], mphase, dead, P.status);
         if (*dead) break;
-        const int nblk = meta[slot].nblk, halves = meta[slot].ntok > TS ? 2 : 1;
+        const int nblk = meta[slot].nblk;
+        const bool mine = h == 0 || meta[slot].ntok > TS;
         __syncwarp();
         if (lane == 0) mbar_arrive(&mempty[slot]);
         if (nblk == 0) break;
         if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
         wait_phase(qfull, qn & 1, dead, P.status);
         ++qn;
+        if (!mine) {  // a tile of one half: see every phase, use nothing
+          if (lane == 0) mbar_arrive(qempty);
+          for (int j = 0; j < 2 * nblk; ++j) {
+            const uint32_t st = kst(blkn) + (j & 1);
+            wait_phase(&full[st], kph(blkn), dead, P.status);
+            if (lane == 0) mbar_arrive(&empty[st]);
+            blkn += j & 1;
+          }
+          if (*dead) break;
+          continue;
+        }
         wait_phase(&full[kst(blkn)], kph(blkn), dead, P.status);
         tc_fence_after();
         if (elect_one()) {
-          s_product(0, kst(blkn));
-          if (halves == 2) s_product(1, kst(blkn));
+          s_product(kst(blkn));
           tc_commit(&empty[kst(blkn)]);
           if (nblk == 1) tc_commit(qempty);
         }
         for (int j = 0; j < nblk; ++j, ++blkn) {
           const uint32_t vst = kst(blkn) + 1, nst = kst(blkn + 1);
           const bool more = j + 1 < nblk;
+          // (a wait that is met already costs 150 cycles: not behind P's)
+          wait_phase(&full[vst], kph(blkn), dead, P.status);
+          if (more) wait_phase(&full[nst], kph(blkn + 1), dead, P.status);
+          wait_phase(&pfull[h], pn & 1, dead, P.status);
+          ++pn;
+          if (*dead) break;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == halves) break;
-            wait_phase(&pfull[h], pn[h] & 1, dead, P.status);
-            ++pn[h];
-            if (h == 0) {
-              wait_phase(&full[vst], kph(blkn), dead, P.status);
-              if (more) wait_phase(&full[nst], kph(blkn + 1), dead, P.status);
-            }
-            if (*dead) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_ta(T_O + 128u * h, T_S + 128u * h + 8u * kk, dv + (vst * (C::TILE / 16) + 128u * kk), id_o,
-                          (j | kk) != 0);
-              if (h + 1 == halves) tc_commit(&empty[vst]);
-              if (more) {
-                s_product(h, nst);
-                if (h + 1 == halves) {
-                  tc_commit(&empty[nst]);
-                  if (j + 2 == nblk) tc_commit(qempty);
-                }
-              } else {
-                tc_commit(&ofull[h]);
-              }
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_ta(t_o, t_s + 8u * kk, dv + (vst * (C::TILE / 16) + 128u * kk), id_o, (j | kk) != 0);
+            if (more) {
+              s_product(nst);
+              tc_commit(&empty[vst]);
+              tc_commit(&empty[nst]);
+              if (j + 2 == nblk) tc_commit(qempty);
+            } else {
+              tc_commit(&ofull[h]);
+              tc_commit(&empty[vst]);
             }
           }
-          if (*dead) break;
         }
         if (*dead) break;
       }
@@ -443,13 +450,17 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           for (int i = 0; i < 128; ++i)
             if ((uint32_t)(i - c0) >= w) s[i] = -INFINITY;
         }
-        float t0 = max3(s[0], s[1], s[2]), t1 = max3(s[3], s[4], s[5]);
+        float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
 #pragma unroll
-        for (int i = 6; i < 126; i += 4) {
+        for (int i = 4; i < 124; i += 8) {
           t0 = max3(t0, s[i], s[i + 1]);
           t1 = max3(t1, s[i + 2], s[i + 3]);
+          t2 = max3(t2, s[i + 4], s[i + 5]);
+          t3 = max3(t3, s[i + 6], s[i + 7]);
         }
-        const float bm = max3(fmaxf(t0, t1), s[126], s[127]);
+        t0 = max3(t0, s[124], s[125]);
+        t1 = max3(t1, s[126], s[127]);
+        const float bm = max3(t0, t1, fmaxf(t2, t3));
         const float mn = fmaxf(mx, bm);
         if (__any_sync(0xffffffffu, (mn - mx) * cs > 8.f)) {
           const float a = mx == -INFINITY ? 0.f : ex2((mx - mn) * cs);
@@ -484,9 +495,9 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           tmem_st16(s_t + 16 * q, pk);
         }
         l += pair_sum(add_f32x2(sum0, sum1));
-        // values of keys that no row sees may be anything: the first half's
-        // group makes them zero before the block's first product with V
-        if (half == 0 && (key0 < m.lo || key0 + 128 > m.hi)) {
+        // values of keys that no row sees may be anything: each half's group
+        // makes them zero before its product with V (both write the same)
+        if (key0 < m.lo || key0 + 128 > m.hi) {
           const uint32_t vst = (2 * blkn) % ST + 1;
           wait_phase(&full[vst], ((2 * blkn) / ST) & 1, dead, P.status);
           const int key = key0 + row;  // rows of 128 threads
