@@ -8,8 +8,8 @@
 // SM) takes an equal run of it, and rows whose keys lie in several runs are
 // joined as in the few-row kernel.
 //
-// Warps of a CTA: one loads (TMA: queries, then K and V blocks page by page,
-// 128-byte swizzle), one for each half issues tcgen05.mma, two groups of four own
+// Warps of a CTA: two load (TMA: queries, K and V blocks page by page, 128-byte
+// swizzle), one for each half issues tcgen05.mma, two groups of four own
 // a half each (thread = row).  Per half and block: S = Q K^T into 128 TMEM columns; its
 // group reads the row, masks it where the block crosses a bound, exponentiates
 // relative to a running maximum and writes P over S in the cache's type; O += P V
@@ -27,7 +27,8 @@ namespace mk {
 namespace {
 
 constexpr int PC_THREADS = 384;
-constexpr int PC_LOAD = 8, PC_MMA = 9;       // warps (9, 10: products); 0-3 and 4-7 own the halves
+constexpr int PC_LOAD = 8, PC_MMA = 9, PC_LOAD_V = 11;  // warps (9, 10: products); 0-3 and 4-7 own the halves
+constexpr int PC_SPLIT_V = 5;                // log2 of the page size from which one warp loads K and V
 constexpr int PC_REGS = 168, PC_REGS_SOFT = 216, PC_REGS_REST = 72;
 static_assert(2 * PC_REGS_SOFT + PC_REGS_REST == 3 * PC_REGS, "registers of the three warpgroups");
 // What a tile costs beside its blocks (filling the pipeline, writing the rows),
@@ -55,7 +56,8 @@ struct Tile {
   int pos0;                // position of the first token
   int lo, hi;              // keys the request's rows may see
   int part;                // workspace part, -1: all of the tile's blocks
-  int pad[7];
+  int req;                 // its request
+  int pad[6];
 };
 static_assert(sizeof(Tile) == 64, "meta slot");
 
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   int* pre = kept.pre;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int TS = 128 / P.rep, TT = 2 * TS;  // tokens of a half, of a tile
+  const bool split_v = P.page_shift < PC_SPLIT_V;
 
   grid_launch_dependents();
   if (tid == 0) {
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     mbar_init(qempty, 2);
     for (int s = 0; s < C::SLOTS; ++s) {
       mbar_init(&mfull[s], 1);
-      mbar_init(&mempty[s], 10);
+      mbar_init(&mempty[s], split_v ? 11 : 10);
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sfull[h], 1);
@@ -194,14 +197,69 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   const Runs runs(T, max(G, 1));
   const int u0 = c < G ? runs.start(c) : 0, u1 = c < G ? runs.start(c + 1) : 0;
 
+  // Values are loaded by a warp of their own where pages are of 16 tokens: a
+  // block's keys and values are then 32 boxes of 2 KB, which one warp does not
+  // issue in the block's time (2 x 512 tokens over 4-12K: 102 against 120 us;
+  // 8192-token prompt: 366 against 448).  With larger boxes one warp is enough,
+  // and the keys' and values' loads in turn disturb the products' reads of shared
+  // memory less (prompt, pages of 32: 371 against 381 us, of 64: 374 against 411).
   if (warp >= PC_LOAD) {
     setmaxnreg_dec<PC_REGS_REST>();
-    if (warp == PC_LOAD) {
-      // ---------------------------------------------------------- loads
-      const int boxt = min(128, 1 << P.page_shift), nbox = 128 / boxt;
-      const int mask = (1 << P.page_shift) - 1;
+    const int boxt = min(128, 1 << P.page_shift), nbox = 128 / boxt;
+    // page of this lane's box of a block; -1 where no row of the request sees any of it
+    auto page_of = [&](const int32_t* tab, int b, int lo, int hi) {
+      const int key = b * 128 + lane * boxt;
+      if (lane >= nbox || key >= hi || key + boxt <= lo) return -1;
+      const int p = tab[key >> P.page_shift];
+      if (p >= 0 && p < P.n_pages) return p;
+      latch(P.status, MK_ERR_BOUNDS);
+      return -1;
+    };
+    // a block's keys or values into a stage
+    auto load = [&](const CUtensorMap* tm, int stage, uint32_t phase, int b, int head, int page) {
+      wait_phase(&empty[stage], phase, dead, P.status);
+      if (*dead) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::TILE);
+      __syncwarp();
+      if (lane < nbox) {
+        uint8_t* dst = smem + C::o_kv + stage * C::TILE + lane * boxt * 128;
+        const int tok = (b * 128 + lane * boxt) & ((1 << P.page_shift) - 1);
+#pragma unroll
+        for (int x = 0; x < HD / 64; ++x) tma_page(dst + x * 16384, tm, tok, x, head, page, &full[stage]);
+      }
+      return true;
+    };
+    if (warp == PC_LOAD_V && split_v) {
+      // ---------------------------------------------------------- loads of V
+      int stage = 1, slot = 0;
+      uint32_t sphase = 1, mphase = 0;
+      for (;;) {
+        wait_phase(&mfull[slot], mphase, dead, P.status);
+        if (*dead) break;
+        const Tile m = meta[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mempty[slot]);
+        if (m.nblk == 0) break;
+        if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
+        const int32_t* tab = P.table + (int64_t)m.req * P.max_blocks;
+        const int b0 = m.key0 / 128;
+        int page = page_of(tab, b0, m.lo, m.hi);
+        bool up = true;
+        for (int i = 0; i < m.nblk && up; ++i) {
+          const int next = i + 1 < m.nblk ? page_of(tab, b0 + i + 1, m.lo, m.hi) : -1;
+          up = load(&tv, stage, sphase, b0 + i, m.head, page);
+          stage += 2;
+          if (stage > ST) { stage = 1; sphase ^= 1; }
+          page = next;
+        }
+        if (!up) break;
+      }
+      if (*dead) let_land();
+    } else if (warp == PC_LOAD) {
+      // ---------------------------------------------------------- tiles, loads of Q and K
       int stage = 0, slot = 0;
       uint32_t sphase = 1, mphase = 1, qphase = 1;
+      const int step = split_v ? 2 : 1;
       int r = u0 < u1 ? find_le(pre, P.n, u0) : 0, t = -1, head = 0;
       bool up = true;
       for (int u = u0; u < u1 && up;) {
@@ -254,39 +312,18 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           m.key0 = (b0 + blk) * 128; m.nblk = nblk; m.row0 = q.row0 + t * TT; m.ntok = ntok; m.head = head;
           m.pos0 = q.pos0 + t * TT; m.lo = q.lo; m.hi = q.hi;
           m.part = whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
+          m.req = r;
           meta[slot] = m;
           mbar_arrive(&mfull[slot]);
         }
         if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
         const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
-        auto page_of = [&](int b) {  // of this lane's box; -1 where no row of the request sees any of it
-          const int key = b * 128 + lane * boxt;
-          if (lane >= nbox || key >= q.hi || key + boxt <= q.lo) return -1;
-          const int p = tab[key >> P.page_shift];
-          if (p >= 0 && p < P.n_pages) return p;
-          latch(P.status, MK_ERR_BOUNDS);
-          return -1;
-        };
-        auto load = [&](const CUtensorMap* tm, int b, int page) {
-          wait_phase(&empty[stage], sphase, dead, P.status);
-          if (*dead) return false;
-          if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::TILE);
-          __syncwarp();
-          if (lane < nbox) {
-            uint8_t* dst = smem + C::o_kv + stage * C::TILE + lane * boxt * 128;
-            const int tok = (b * 128 + lane * boxt) & mask;
-#pragma unroll
-            for (int x = 0; x < HD / 64; ++x)
-              tma_page(dst + x * 16384, tm, tok, x, head, page, &full[stage]);
-          }
-          if (++stage == ST) { stage = 0; sphase ^= 1; }
-          return true;
-        };
-        int page = page_of(b0 + blk);
+        int page = page_of(tab, b0 + blk, q.lo, q.hi);
         for (int i = 0; i < nblk && up; ++i) {
           const int b = b0 + blk + i;
-          const int next = i + 1 < nblk ? page_of(b + 1) : -1;
-          up = load(&tk, b, page);
+          const int next = i + 1 < nblk ? page_of(tab, b + 1, q.lo, q.hi) : -1;
+          up = load(&tk, stage, sphase, b, head, page);
+          stage += step;
           if (up && i == 0) {
             wait_phase(qempty, qphase, dead, P.status);
             qphase ^= 1;
@@ -301,7 +338,11 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             }
             __syncwarp();
           }
-          if (up) up = load(&tv, b, page);
+          if (up && !split_v) {
+            up = load(&tv, stage, sphase, b, head, page);
+            ++stage;
+          }
+          if (stage >= ST) { stage = 0; sphase ^= 1; }
           page = next;
         }
         u += x1 - x0;
