@@ -422,7 +422,8 @@ typedef struct {
   int32_t *positions;   /* [max_tokens], mk_paged_tables only                 */
   int32_t *slots;       /* [max_tokens] page * page_size + offset, or -1      */
   int n;                /* 1 .. MK_PAGED_MAX_REQUESTS                         */
-  int max_blocks;       /* n * max_blocks * page_size bounds: see the calls   */
+  int max_blocks;       /* n * max_blocks < 2^31, max_blocks * page_size <=
+                           2^30                                               */
   int max_tokens;       /* rows of the step's buffers (rows past cu_new[n] are
                            padding: they are read by nothing and left alone)  */
   int max_new;          /* no request has more new tokens (attention only)    */
@@ -450,7 +451,7 @@ typedef struct {
  * Pages are taken as they are named; the operators that use a page check it (one
  * that no cache can have gives the slot 2^31 - 1).  *n_free outside 0 .. free_capacity is latched and clamped.
  * All pointers device; n_left must not be n_free.  n * max_blocks < 2^31 and
- * max_blocks * page_size < 2^31. */
+ * max_blocks * page_size <= 2^30. */
 int mk_paged_tables(const mk_paged_batch *batch, const int32_t *ctx_lens, const int32_t *new_lens,
                     const int32_t *free_pages, int free_capacity, const int32_t *n_free,
                     int32_t *n_left, int32_t *status, void *stream);
@@ -513,7 +514,9 @@ int mk_paged_append(const mk_paged_cache *cache, const void *q, int64_t q_stride
  *   lse     float [rows][n_q_heads] or NULL
  *   scale   0: 1 / sqrt(head_dim)
  *   window  0: none
- * n_q_heads a multiple of n_kv_heads, at most 64 query heads per kv head.
+ * n_q_heads a multiple of n_kv_heads, at most 64 query heads per kv head;
+ * (max_tokens * n_q_heads / 64 + n * n_kv_heads) * (max_blocks * page_size / 64 +
+ * 4) < 2^31 (blocks of work are counted in 32 bits).
  * batch->max_tokens = rows of q, out and lse; batch->max_new bounds the new
  * tokens of a request; positions and slots are not read.  MK_ERR_BOUNDS is latched
  * in cache->status, and nothing out of range is touched, where kv_lens[r] is

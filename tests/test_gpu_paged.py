@@ -16,6 +16,9 @@ Tolerances (u = half a step of the cache's type, torch.finfo(t).eps / 2):
       u (|o| + A) 1.01 + A (2 ds + (n / 8 + 64) 2^-23) [+ n 2^-25 vmax + 2^-24]
   lse: ds + (n / 8 + 64) 2^-23 + 2^-20 |lse|.
 """
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -513,6 +516,69 @@ def test_on_another_stream_and_in_graphs(workspace):
     torch.cuda.synchronize()
     want2, _ = check_attention(t, workspace=workspace)
     assert torch.equal(outs[0], want2)
+
+
+@pytest.mark.parametrize("new", [[1, 2], [70, 2]])
+def test_a_nan_stays_with_its_row(new, workspace):
+    s = make_attention([300, 200], new, 8, 2, 128, 16, torch.bfloat16, seed=30, garbage=0.0)
+    batch = mk.PagedBatch(ints(s["table"]), ints(s["cu"]), ints(s["kv"]), page_size=16, max_new=max(new))
+    cache = mk.PagedCache(s["k"], s["v"], n_q_heads=8, workspace=workspace)
+    outs = []
+    for spoil in (False, True):
+        q = s["q"].clone()
+        if spoil:
+            q[0, 3, 5] = float("nan")
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device=DEV)
+        cache.attention(q, batch, out, lse=lse)
+        outs.append((out, lse))
+    (a, la), (b, lb) = outs
+    assert torch.isnan(b[0, 3]).all() and torch.isnan(lb[0, 3])
+    b[0, 3], lb[0, 3] = a[0, 3], la[0, 3]
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+FIRST_IN_CAPTURE = """
+import sys, torch
+sys.path.insert(0, %r)
+from tile_level_overlap_gb300 import mk
+dev = "cuda:0"
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+k, v = (torch.randn(40, 2, 16, 64, device=dev).to(torch.bfloat16) for _ in range(2))
+cache = mk.PagedCache(k, v, n_q_heads=4, workspace=torch.empty(mk.MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=dev))
+t = 400
+q, kn, vn = (torch.randn(t, h, 64, device=dev).to(torch.bfloat16) for h in (4, 2, 2))
+batch = mk.PagedBatch(i32([[-1] * 30, [-1] * 30]), i32([0] * 3), i32([0] * 2), i32([0] * t), i32([0] * t), page_size=16, max_new=399)
+ctx, new, free, n_free, left = i32([0, 0]), i32([399, 1]), i32(list(range(40))), i32([40]), i32([0])
+out, qo, rope = torch.zeros_like(q), torch.zeros_like(q), mk.Rope(64)
+def step():
+    batch.build(ctx, new, free, n_free, left)
+    cache.append(q, kn, vn, batch.slots, batch.positions, rope, q_out=qo)
+    cache.attention(qo, batch, out)
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+got = out.clone()
+bare = mk.PagedCache(k, v, n_q_heads=4)
+with torch.cuda.graph(torch.cuda.CUDAGraph()):
+    try:
+        bare.attention(qo, batch, out)
+        print("accepted")
+    except ValueError:
+        pass
+out.zero_()
+step()
+torch.cuda.synchronize()
+assert torch.equal(got, out) and cache.status() == 0 and got.abs().sum() > 0
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_in_a_capture():
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE % build.ROOT], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["same"], r.stdout + r.stderr
 
 
 def test_python_refusals():

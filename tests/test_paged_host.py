@@ -61,7 +61,8 @@ def test_bad_caches_are_refused(lib, kw, code):
     (dict(block_table=None), 1), (dict(cu_new=None), 1), (dict(kv_lens=None), 1), (dict(cu_new=ADDR + 2), 1),
     (dict(n=0), 1), (dict(n=mk.MK_PAGED_MAX_REQUESTS + 1), 5), (dict(max_blocks=0), 1),
     (dict(max_tokens=-1), 1), (dict(max_new=0), 1), (dict(page_size=32), 1), (dict(page_size=17), 5),
-    (dict(n=4096, max_blocks=1 << 20), 5), (dict(n=1, max_blocks=1 << 27), 5),
+    (dict(n=4096, max_blocks=1 << 20), 5), (dict(n=1, max_blocks=1 << 27), 5), (dict(n=1, max_blocks=(1 << 26) + 1), 5),
+    (dict(n=4, max_blocks=1 << 26, max_tokens=400), 5),
 ])
 def test_bad_batches_are_refused(lib, kw, code):
     assert attention(lib, cache(), batch(**kw)) == code
@@ -69,7 +70,7 @@ def test_bad_batches_are_refused(lib, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), 1), (dict(out=None), 1), (dict(out=ADDR), 1), (dict(q=ADDR + 4), 1), (dict(out=ADDR + 8), 1),
-    (dict(qs=4000), 1), (dict(os=4090), 1), (dict(qs=4100), 1), (dict(lse=ADDR + 2), 1), (dict(window=-1), 1),
+    (dict(qs=4000), 1), (dict(os=4090), 1), (dict(qs=4100), 1), (dict(qs=1 << 38), 1), (dict(lse=ADDR + 2), 1), (dict(window=-1), 1),
     (dict(scale=math.nan), 1), (dict(scale=math.inf), 1),
 ])
 def test_bad_attention_arguments_are_refused(lib, kw, code):

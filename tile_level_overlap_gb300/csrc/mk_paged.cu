@@ -558,8 +558,7 @@ int check_batch(const mk_paged_batch* b) {
   if (!al4(b->block_table) || !al4(b->cu_new) || !al4(b->kv_lens)) return MK_ERR_INVALID_ARG;
   if (b->n < 1 || b->max_blocks < 1 || b->max_tokens < 0) return MK_ERR_INVALID_ARG;
   if (b->n > MK_PAGED_MAX_REQUESTS || log2_page(b->page_size) < 0) return MK_ERR_UNSUPPORTED;
-  if ((int64_t)b->n * b->max_blocks > 0x7fffffffll ||
-      (int64_t)b->max_blocks * b->page_size > 0x7fffffffll)
+  if ((int64_t)b->n * b->max_blocks > 0x7fffffffll || (int64_t)b->max_blocks * b->page_size > (1ll << 30))
     return MK_ERR_UNSUPPORTED;
   return MK_OK;
 }
@@ -689,7 +688,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch*
       !al16(c->workspace))
     return MK_ERR_INVALID_ARG;
   const int64_t qw = (int64_t)c->n_q_heads * c->head_dim;
-  if (((q_stride | out_stride) & 7) || q_stride < qw || out_stride < qw || window < 0 ||
+  if (((q_stride | out_stride) & 7) || q_stride < qw || out_stride < qw || q_stride >= (1ll << 38) || window < 0 ||
       !std::isfinite(scale) || b->page_size != c->page_size || b->max_new < 1)
     return MK_ERR_INVALID_ARG;
   if (c->n_q_heads % c->n_kv_heads) return MK_ERR_INVALID_ARG;
@@ -704,9 +703,9 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch*
   p.hkv = c->n_kv_heads; p.rep = c->n_q_heads / c->n_kv_heads;
   p.window = window ? window : 0x7fffffff;
   p.scale = scale != 0.f ? scale : 1.0f / sqrtf((float)c->head_dim);
-  // units of work are counted in 32 bits (64 keys x (128 rows or a request))
+  // units of work (key blocks and overheads of tiles or requests) are counted in 32 bits
   const int64_t tiles = (int64_t)b->max_tokens * p.rep / 64 + b->n;
-  if (tiles * c->n_kv_heads * ((int64_t)b->max_blocks * b->page_size / 64 + 1) > 0x7fffffffll)
+  if (tiles * c->n_kv_heads * ((int64_t)b->max_blocks * b->page_size / 64 + 4) > 0x7fffffffll)
     return MK_ERR_UNSUPPORTED;
   const PagedKv kv = {c->k, c->v, c->page_stride, c->head_stride, c->token_stride,
                       c->n_pages, c->n_kv_heads, c->page_size};

@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         // Four lanes exchange 16-byte pieces so that a store writes 64
         // contiguous bytes of a row: lane 4 a + b then has piece b of the rows
         // 4 a + i (16 scattered bytes a lane took three times as long).
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = inv_of(l);
         uint16_t* dst[4];
         bool put[4];
 #pragma unroll
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         }
         if (live && P.lse)
           P.lse[(int64_t)(m.row0 + tok0 + tok_in) * (P.hkv * P.rep) + m.head * P.rep + hq_in] =
-              l > 0.f ? (mx * cs + log2f(l)) * 0.6931471805599453f : -INFINITY;
+              lse_of(mx * cs, l);
       } else {
         // a part: [4 columns][row], a warp's lanes end to end
         float* dst = W.o + (int64_t)m.part * W.rt * HD + prow * 4;

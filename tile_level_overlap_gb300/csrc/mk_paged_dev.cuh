@@ -54,6 +54,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A row's factor and log-sum-exp from its maximum (base 2) and sum: 0 and -inf
+// where it saw no key; a NaN among its scores stays one.
+__device__ __forceinline__ float inv_of(float l) { return l != 0.f ? 1.f / l : 0.f; }
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
 // ---------------------------------------------------------------- dependent launches
 // Every kernel here is launched as a programmatic dependent of what precedes it
 // in the stream: it may be set up while that one's last blocks run, and touches

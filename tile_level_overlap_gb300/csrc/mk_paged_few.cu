@@ -496,12 +496,11 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
         }
         if (s.part < 0) {
           const int ti = P.token_of(irow), tok = s.row0 + ti, hq = s.head * P.rep + irow - ti * P.rep;
-          const float inv = ll > 0.f ? 1.f / ll : 0.f;
+          const float inv = inv_of(ll);
           *reinterpret_cast<uint2*>(P.out + (int64_t)tok * P.o_stride + (int64_t)hq * HD + d4) =
               make_uint2(down2<BF>(acc.x * inv, acc.y * inv), down2<BF>(acc.z * inv, acc.w * inv));
           if (P.lse && d4 == 0)
-            P.lse[(int64_t)tok * (P.hkv * P.rep) + hq] =
-                ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            P.lse[(int64_t)tok * (P.hkv * P.rep) + hq] = lse_of(mm, ll);
         } else {
           *reinterpret_cast<float4*>(W.o + ((int64_t)s.part * W.rt + irow) * HD + d4) = acc;
           if (d4 == 0) W.ml[(int64_t)s.part * W.rt + irow] = make_float2(mm, ll);
@@ -517,10 +516,6 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
 // Latency bound: few bytes, read right after the launch that wrote them.
 constexpr int JOIN_ROWS = 32;  // of a tile, a block
 constexpr int JOIN_THREADS = 256;
-
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-}
 
 template <int HD, bool BF>
 __global__ void __launch_bounds__(JOIN_THREADS, 4) paged_join_kernel(const __grid_constant__ PagedAttnParams P,
@@ -618,7 +613,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) paged_join_kernel(const __gri
         }
         if (pass && row < d.rows && share == 0) {
           const int t = P.token_of(row), hq = d.head * P.rep + row - t * P.rep;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float inv = inv_of(l);
           uint32_t* dst = reinterpret_cast<uint32_t*>(P.out + (int64_t)(d.row0 + t) * P.o_stride + (int64_t)hq * HD) + lane * (E / 2);
 #pragma unroll
           for (int e = 0; e < E; e += 2) dst[e / 2] = down2<BF>(o[e] * inv, o[e + 1] * inv);
@@ -658,7 +653,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) paged_join_kernel(const __gri
     }
     m = mn;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = inv_of(l);
 #pragma unroll
   for (int q = 0; q < Q; ++q)
     rows_out[lane][warp * Q + q] = make_uint2(down2<BF>(o[q].x * inv, o[q].y * inv), down2<BF>(o[q].z * inv, o[q].w * inv));

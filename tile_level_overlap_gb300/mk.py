@@ -573,6 +573,8 @@ class PagedCache(_OnDevice):
         [rows, n_q_heads] or None."""
         if self.workspace is None:
             import torch
+            _need(not torch.cuda.is_current_stream_capturing(),
+                  "workspace: give one, or call once before the capture (it would belong to the graph)")
             self._set_workspace(torch.empty(MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device))
         hq, d, dev, typ = self.n_q_heads, self.head_dim, self._dev, self.dtype
         n = q.shape[0]
@@ -593,7 +595,8 @@ class PagedCache(_OnDevice):
                    None if lse is None else lse.data_ptr(), scale, window)
 
     def status(self) -> int:
-        """The status word (waits for the device work that writes it)."""
+        """The status word: MK_OK or the first error latched by the cache's calls
+        (waits for the current stream; calls on others have to be waited for)."""
         return int(self._status.item())
 
     def reset(self) -> None:
