@@ -388,20 +388,17 @@ class _OnDevice:
         import torch
         self.device, self._dev = device, device.index
         self._i32, self._f32 = torch.int32, torch.float32
-        self._current, self._guard = torch.cuda.current_device, torch.cuda.device
+        self._guard = torch.cuda.device
+        # None where there is no other device that could be current
+        self._current = torch.cuda.current_device if torch.cuda.device_count() > 1 else None
         # the current stream as an address, without a Stream object for it
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda d: torch.cuda.current_stream(d).cuda_stream)
 
-    def _call(self, what: str, fn, stream, *args) -> None:
-        raw = self._raw_stream(self._dev) if stream is None else int(stream.cuda_stream)
-        if self._current() == self._dev:
-            rc = fn(*args, raw)
-        else:
-            with self._guard(self._dev):
-                rc = fn(*args, raw)
-        if rc:
-            raise MkError(rc, what)
+    def _elsewhere(self, fn, *args) -> int:
+        """fn(*args) with the tensors' device current, which it is not."""
+        with self._guard(self._dev):
+            return fn(*args)
 
 
 class Rope:
@@ -460,7 +457,7 @@ class PagedBatch(_OnDevice):
                                 None if slots is None else _ptr(positions),
                                 None if slots is None else _ptr(slots), n, block_table.shape[1],
                                 self.max_tokens, self.max_new, page_size)
-        self._p = ctypes.addressof(self.c)
+        self._p, self._build = ctypes.addressof(self.c), lib().mk_paged_tables
 
     def build(self, ctx_lens, new_lens, free_pages, n_free, n_left, status=None, stream=None) -> None:
         """mk_paged_tables: fill the tables from device int32 lengths [n], taking
@@ -480,10 +477,18 @@ class PagedBatch(_OnDevice):
             _tensors(self.device, ctx_lens=(ctx_lens, i32, (n,)), new_lens=(new_lens, i32, (n,)),
                      free_pages=(free_pages, i32, None), n_free=(n_free, i32, (1,)),
                      n_left=(n_left, i32, (1,)), status=(status, i32, (1,)))
-        self.c.max_tokens = self.max_tokens
-        self._call("mk_paged_tables", _lib.mk_paged_tables, stream, self._p, ctx_lens.data_ptr(),
-                   new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
-                   n_left.data_ptr(), None if status is None else status.data_ptr())
+        if self.c.max_tokens != self.max_tokens:
+            self.c.max_tokens = self.max_tokens
+        args = (self._p, ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+                free_pages.numel(), n_free.data_ptr(), n_left.data_ptr(),
+                None if status is None else status.data_ptr(),
+                self._raw_stream(dev) if stream is None else int(stream.cuda_stream))
+        if self._current is None or self._current() == dev:
+            rc = self._build(*args)
+        else:
+            rc = self._elsewhere(self._build, *args)
+        if rc:
+            raise MkError(rc, "mk_paged_tables")
 
 
 class PagedCache(_OnDevice):
@@ -512,6 +517,7 @@ class PagedCache(_OnDevice):
                                 n_q_heads, hkv, d, page, n_pages,
                                 MK_BF16 if k.dtype == torch.bfloat16 else MK_FP16)
         self._p = ctypes.addressof(self.c)
+        self._append, self._attention = lib().mk_paged_append, lib().mk_paged_attention
         if workspace is not None:
             _need(workspace.device == k.device and workspace.is_contiguous() and
                   workspace.numel() * workspace.element_size() >= MK_PAGED_WORKSPACE_BYTES,
@@ -533,11 +539,12 @@ class PagedCache(_OnDevice):
         n = q.shape[0]
         qs, ks, vs, os = q.stride(), k.stride(), v.stride(), q_out.stride()
         wide, narrow = (n, hq, d), (n, hkv, d)
-        if not (q.shape == wide and k.shape == narrow and v.shape == narrow and q_out.shape == wide
-                and q.dtype is typ and k.dtype is typ and v.dtype is typ and q_out.dtype is typ
+        if not (q.shape == wide and k.shape == narrow and v.shape == narrow
+                and q.dtype is typ and k.dtype is typ and v.dtype is typ
                 and q.get_device() == dev and k.get_device() == dev and v.get_device() == dev
-                and q_out.get_device() == dev and qs[2] == 1 and ks[2] == 1 and vs[2] == 1 and os[2] == 1
-                and (hq == 1 or (qs[1] == d and os[1] == d)) and (hkv == 1 or (ks[1] == d and vs[1] == d))
+                and (q_out is q or (q_out.shape == wide and q_out.dtype is typ and q_out.get_device() == dev))
+                and qs[2] == ks[2] == vs[2] == os[2] == 1
+                and (hq == 1 or qs[1] == os[1] == d) and (hkv == 1 or ks[1] == vs[1] == d)
                 and slots.dtype is i32 and slots.get_device() == dev and slots.numel() == n
                 and slots.is_contiguous()):
             _heads(self.device, typ, q=(q, wide), k=(k, narrow), v=(v, narrow), q_out=(q_out, wide))
@@ -560,12 +567,18 @@ class PagedCache(_OnDevice):
                 pos_stride = positions.stride(0)
         if n == 0:
             return
-        # the stride of a lone token joins nothing and may be any number
-        self._call("mk_paged_append", _lib.mk_paged_append, stream, self._p,
-                   q.data_ptr(), qs[0] if n > 1 else hq * d, k.data_ptr(), ks[0] if n > 1 else hkv * d,
-                   v.data_ptr(), vs[0] if n > 1 else hkv * d, q_out.data_ptr(), os[0] if n > 1 else hq * d,
-                   None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
-                   eps, rp, pos, pos_stride, slots.data_ptr(), n)
+        if n == 1:  # the stride of a lone token joins nothing and may be any number
+            qs, ks, vs, os = (hq * d,), (hkv * d,), (hkv * d,), (hq * d,)
+        args = (self._p, q.data_ptr(), qs[0], k.data_ptr(), ks[0], v.data_ptr(), vs[0], q_out.data_ptr(), os[0],
+                None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                eps, rp, pos, pos_stride, slots.data_ptr(), n,
+                self._raw_stream(dev) if stream is None else int(stream.cuda_stream))
+        if self._current is None or self._current() == dev:
+            rc = self._append(*args)
+        else:
+            rc = self._elsewhere(self._append, *args)
+        if rc:
+            raise MkError(rc, "mk_paged_append")
 
     def attention(self, q, batch: PagedBatch, out, lse=None, scale: float = 0.0, window: int = 0,
                   stream=None) -> None:
@@ -590,9 +603,15 @@ class PagedCache(_OnDevice):
         if n == 0:
             return
         batch.c.max_tokens = n
-        self._call("mk_paged_attention", _lib.mk_paged_attention, stream, self._p, batch._p, q.data_ptr(),
-                   qs[0] if n > 1 else hq * d, out.data_ptr(), os[0] if n > 1 else hq * d,
-                   None if lse is None else lse.data_ptr(), scale, window)
+        args = (self._p, batch._p, q.data_ptr(), qs[0] if n > 1 else hq * d, out.data_ptr(),
+                os[0] if n > 1 else hq * d, None if lse is None else lse.data_ptr(), scale, window,
+                self._raw_stream(dev) if stream is None else int(stream.cuda_stream))
+        if self._current is None or self._current() == dev:
+            rc = self._attention(*args)
+        else:
+            rc = self._elsewhere(self._attention, *args)
+        if rc:
+            raise MkError(rc, "mk_paged_attention")
 
     def status(self) -> int:
         """The status word: MK_OK or the first error latched by the cache's calls
