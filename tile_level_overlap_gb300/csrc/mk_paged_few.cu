@@ -9,10 +9,12 @@
 // maximum, sum and unnormalised output in the workspace, and a second launch
 // joins the parts of each pair in the order of their keys.
 //
-// A producer warp walks the run: it posts each pair's description and query
-// rows (bulk copies) to a small ring and loads the key blocks (32 KB of keys
-// and values: 64 keys at head_dim 128, 128 at 64) page by page through a
-// ring with TMA, 128-byte swizzle.  Eight consumer warps in two groups take
+// A warp walks the run: it posts each pair's description and query rows (bulk
+// copies) to a small ring and loads the key blocks (32 KB of keys and values: 64
+// keys at head_dim 128, 128 at 64) page by page through a ring with TMA, 128-byte
+// swizzle; another loads the values (one warp for both took longer to issue the
+// small pages' boxes than HBM takes for them: 64 x 4096 keys in pages of 16 174
+// against 169 us, 32 ragged rows of heads of 64 23.8 against 20.7).  Eight consumer warps in two groups take
 // the blocks in turn, 16 (32) keys each warp, with a softmax state of their
 // own: S^T = K Q^T and O^T += V^T P^T by warp-level products, keys and
 // dimensions on the 16-row side and the query rows on the 8-column side, so
@@ -27,7 +29,7 @@ namespace mk {
 namespace {
 
 constexpr int PF_WARPS = 8;             // consumers
-constexpr int PF_THREADS = 32 * (PF_WARPS + 1);
+constexpr int PF_THREADS = 32 * (PF_WARPS + 2);  // and two that load
 constexpr int PF_STAGE = 32768;         // one block's keys, then its values
 constexpr int PF_OVER = 1;              // what a pair costs beside its blocks, in blocks
 
@@ -44,7 +46,7 @@ struct FewCfg {
   static constexpr int o_ml = o_merge + PF_WARPS * 8 * OROW * 4;
   static constexpr int o_meta = o_ml + PF_WARPS * RT * 8;
   static constexpr int o_bar = o_meta + QSLOTS * 48;
-  static constexpr int o_pre = o_bar + 8 * (2 * STAGES + 2 * QSLOTS) + 64;
+  static constexpr int o_pre = o_bar + 8 * (2 * STAGES + 3 * QSLOTS) + 64;
   static constexpr int total(int n) { return o_pre + Kept::bytes(n); }
   static constexpr int most = o_pre + KEPT_MOST;
 };
@@ -57,7 +59,8 @@ struct Segment {
   int row0, rows, head;
   int pos0, lo, hi;          // Request's
   int part;                  // workspace part, -1: all of the pair's blocks
-  int pad[3];
+  int req;                   // its request
+  int pad[2];
 };
 static_assert(sizeof(Segment) == 48, "meta slot");
 
@@ -124,7 +127,8 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
   uint64_t* empty = full + C::STAGES;
   uint64_t* qfull = empty + C::STAGES;
   uint64_t* qempty = qfull + C::QSLOTS;
-  volatile int* dead = reinterpret_cast<volatile int*>(qempty + C::QSLOTS);
+  uint64_t* mfull = qempty + C::QSLOTS;  // the description alone, for the warp that loads values
+  volatile int* dead = reinterpret_cast<volatile int*>(mfull + C::QSLOTS);
   int* scan_tmp = const_cast<int*>(dead) + 1;
   const Kept kept(smem + C::o_pre, P.n);
   int* pre = kept.pre;
@@ -133,12 +137,13 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);
       mbar_init(&empty[s], PF_WARPS);
     }
     for (int s = 0; s < C::QSLOTS; ++s) {
       mbar_init(&qfull[s], 1);
-      mbar_init(&qempty[s], PF_WARPS);
+      mbar_init(&mfull[s], 1);
+      mbar_init(&qempty[s], PF_WARPS + 1);
     }
     *dead = 0;
     fence_mbar_init();
@@ -185,12 +190,56 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
   const Runs runs(T, G);
   const int u0 = runs.start(c), u1 = runs.start(c + 1);
 
-  if (warp == PF_WARPS) {
-    // ------------------------------------------------------------ producer
+  if (warp >= PF_WARPS) {
+    // ------------------------------------------------------------- loads
     const int boxt = min(KS, 1 << P.page_shift), nbox = KS / boxt;
     const int mask = (1 << P.page_shift) - 1, my_tok = P.token_of(lane);
-    int r = find_le(pre, P.n, u0), stage = 0, slot = 0;
-    uint32_t sphase = 1, qphase = 1;  // parities of the "empty" waits
+    // page of this lane's box of a block; -1 where no row sees any of it
+    auto page_of = [&](const int32_t* tab, int b, int lo, int hi) {
+      const int key = b * KS + lane * boxt;
+      if (lane >= nbox || key >= hi || key + boxt <= lo) return -1;
+      const int p = tab[key >> P.page_shift];
+      if (p >= 0 && p < P.n_pages) return p;
+      latch(P.status, MK_ERR_BOUNDS);
+      return -1;
+    };
+    int stage = 0, slot = 0;
+    uint32_t sphase = 1;
+    // blocks [b0, b0 + nblk) of a head: their keys (at 0 of a stage) or values
+    const CUtensorMap* tm = warp == PF_WARPS ? &tk : &tv;
+    uint8_t* ring = smem + (warp == PF_WARPS ? 0 : PF_STAGE / 2);
+    auto load = [&](const int32_t* tab, int b0, int nblk, int head, int lo, int hi, int page) {
+      for (int i = 0; i < nblk; ++i) {
+        const int next = i + 1 < nblk ? page_of(tab, b0 + i + 1, lo, hi) : -1;
+        wait_phase(&empty[stage], sphase, dead, P.status);
+        if (*dead) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], PF_STAGE / 2);
+        __syncwarp();
+        if (lane < nbox)
+          tma_page(ring + stage * PF_STAGE + lane * boxt * (2 * HD), tm, ((b0 + i) * KS + lane * boxt) & mask, 0, head,
+                   page, &full[stage]);
+        if (++stage == C::STAGES) { stage = 0; sphase ^= 1; }
+        page = next;
+      }
+      return true;
+    };
+    if (warp > PF_WARPS) {  // values
+      uint32_t mphase = 0;
+      for (;;) {
+        wait_phase(&mfull[slot], mphase, dead, P.status);
+        if (*dead) return let_copies_land();
+        const Segment s = meta[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qempty[slot]);
+        if (s.nblk == 0) return;
+        if (++slot == C::QSLOTS) { slot = 0; mphase ^= 1; }
+        const int32_t* tab = P.table + (int64_t)s.req * P.max_blocks;
+        const int b0 = s.key0 / KS;
+        if (!load(tab, b0, s.nblk, s.head, s.lo, s.hi, page_of(tab, b0, s.lo, s.hi))) return let_copies_land();
+      }
+    }
+    int r = find_le(pre, P.n, u0);
+    uint32_t qphase = 1;  // parity of the "empty" waits
     for (int u = u0; u < u1;) {
       while (pre[r + 1] <= u) ++r;
       const Request q = kept.again(P, r);
@@ -201,16 +250,7 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
       if (nblk == 0) break;  // the run ends with the pair's overhead: the next CTA has it all
       const int b0 = q.lo / KS + blk, rows = q.add * P.rep;
       const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
-      // page of this lane's box of a block; -1 where no row sees any of it
-      auto page_of = [&](int b) {
-        const int key = b * KS + lane * boxt;
-        if (lane >= nbox || key >= q.hi || key + boxt <= q.lo) return -1;
-        const int p = tab[key >> P.page_shift];
-        if (p >= 0 && p < P.n_pages) return p;
-        latch(P.status, MK_ERR_BOUNDS);
-        return -1;
-      };
-      int page = page_of(b0);
+      const int page = page_of(tab, b0, q.lo, q.hi);
       const bool whole = blk == 0 && nblk == nb;
       if (blk == 0 && !whole) {  // joined by this CTA's block of the second launch
         const int last = runs.of(u - x0 + units - 1);  // CTA of the pair's last unit
@@ -227,7 +267,9 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
         s.key0 = b0 * KS; s.nblk = nblk; s.row0 = q.row0; s.rows = rows; s.head = head;
         s.pos0 = q.pos0; s.lo = q.lo; s.hi = q.hi;
         s.part = whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
+        s.req = r;
         meta[slot] = s;
+        mbar_arrive(&mfull[slot]);
         mbar_arrive_expect_tx(&qfull[slot], (uint32_t)rows * HD * 2);
       }
       __syncwarp();
@@ -236,21 +278,7 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
                  P.q + (int64_t)(q.row0 + my_tok) * P.q_stride + (int64_t)(head * P.rep + lane - my_tok * P.rep) * HD,
                  HD * 2, &qfull[slot]);
       if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
-      for (int i = 0; i < nblk; ++i) {
-        const int next = i + 1 < nblk ? page_of(b0 + i + 1) : -1;
-        wait_phase(&empty[stage], sphase, dead, P.status);
-        if (*dead) return let_copies_land();
-        if (lane == 0) mbar_arrive_expect_tx(&full[stage], PF_STAGE);
-        __syncwarp();
-        if (lane < nbox) {
-          uint8_t* dst = smem + stage * PF_STAGE + lane * boxt * (2 * HD);
-          const int tok = ((b0 + i) * KS + lane * boxt) & mask;
-          tma_page(dst, &tk, tok, 0, head, page, &full[stage]);
-          tma_page(dst + PF_STAGE / 2, &tv, tok, 0, head, page, &full[stage]);
-        }
-        if (++stage == C::STAGES) { stage = 0; sphase ^= 1; }
-        page = next;
-      }
+      if (!load(tab, b0, nblk, head, q.lo, q.hi, page)) return let_copies_land();
       u += x1 - x0;
     }
     // the end of the run
@@ -258,6 +286,7 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
     if (*dead) return let_copies_land();
     if (lane == 0) {
       meta[slot].nblk = 0;
+      mbar_arrive(&mfull[slot]);
       mbar_arrive(&qfull[slot]);
     }
     return;
