@@ -491,20 +491,23 @@ cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool 
   p.device = dev;
   p.rep_inv = (65536 + p.rep - 1) / p.rep;
   // The few-row kernel has the rows of the longest request where it takes them
-  // all, else those of a single token (its products cost by the row).
+  // all, else those of a single token (its products cost by the row: with 32 rows
+  // 16 requests of 8 drafted tokens over 3-8K keys took it 105 us, the tile kernel
+  // 67; with 9 to 16 rows it is ahead, 16 query heads on a kv head at 4096 keys 19
+  // against 27 us).
   const int64_t most = (int64_t)p.max_new * p.rep;
-  const bool all_few = most <= 32;
+  const bool all_few = most <= 16;
   const int want = all_few ? (int)most : p.rep;
-  p.few_rows = want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 ? 32 : 0;
+  p.few_rows = want <= 8 ? 8 : want <= 16 ? 16 : 0;
   // rows a pair has at most: a warp each in the join, or several for one
   p.join_shares = !all_few || want > 4 ? 0 : want > 2 ? 1 : want > 1 ? 2 : 3;
   // workspace: descriptions, maxima and sums, outputs of the two kernels' parts
   const int ctas = std::min(sms, 224);
   uint8_t* w = (uint8_t*)workspace;
   PagedParts few{}, chunk{};
-  few.rt = 32;
+  few.rt = 16;
   chunk.rt = 256;
-  few.ctas = ctas;
+  few.ctas = p.few_rows ? ctas : 0;
   chunk.ctas = all_few ? 0 : ctas;
   few.desc = (PartDesc*)w;
   chunk.desc = few.desc + ctas;
@@ -512,8 +515,8 @@ cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool 
   chunk.ml = few.ml + (size_t)2 * ctas * few.rt;
   few.o = (float*)(chunk.ml + (size_t)2 * ctas * chunk.rt);
   chunk.o = few.o + (size_t)2 * ctas * few.rt * d;
-  static_assert(224 * (2 * 16 + 2 * (32 + 256) * (8 + 128 * 4)) <= MK_PAGED_WORKSPACE_BYTES, "workspace");
-  e = paged_few_launch(p, kv, few, d, bf, st);
+  static_assert(224 * (2 * 16 + 2 * (16 + 256) * (8 + 128 * 4)) <= MK_PAGED_WORKSPACE_BYTES, "workspace");
+  if (few.ctas) e = paged_few_launch(p, kv, few, d, bf, st);
   if (e == cudaSuccess && !all_few) e = paged_chunk_launch(p, kv, chunk, d, bf, st);
   if (e == cudaSuccess) e = paged_join_launch(p, few, chunk, d, bf, st);
   return e;

@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   const int TS = 128 / P.rep, TT = 2 * TS;  // tokens of a half, of a tile
   const bool split_v = P.page_shift < PC_SPLIT_V;
 
+  if (P.few_rows == 0) grid_wait_prior();  // no few-row kernel before it that has waited
   grid_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {

@@ -65,8 +65,8 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // Every kernel here is launched as a programmatic dependent of what precedes it
 // in the stream: it may be set up while that one's last blocks run, and touches
 // global memory only after grid_wait_prior() has seen it complete.  (The tile
-// kernel waits later: it is started by the few-row kernel, which lets it go
-// only after its own wait.)
+// kernel waits only at its end where the few-row kernel comes before it: that one
+// lets it go after its own wait.)
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

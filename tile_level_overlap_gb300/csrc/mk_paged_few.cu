@@ -1,5 +1,5 @@
 // Attention over a paged cache for requests with few rows (new tokens x query
-// heads per kv head <= 32): decode steps and drafted tokens.
+// heads per kv head <= 16): decode steps and drafted tokens.
 //
 // Bound by HBM: every key and value of a (request, kv head) is read once, 4
 // head_dim bytes, for 4 head_dim flops per row.  The work is the list of key
@@ -38,9 +38,9 @@ struct FewCfg {
   static constexpr int KS = HD == 128 ? 64 : 128;  // keys of a block
   static constexpr int RT = 8 * NT;                // rows of an item
   static constexpr int QROW = HD * 2 + 16;         // padded: conflict-free row reads
-  static constexpr int QSLOTS = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int QSLOTS = NT == 1 ? 4 : 3;
   static constexpr int OROW = HD + 4;              // floats; conflict-free column pairs
-  static constexpr int STAGES = NT == 4 ? 4 : 5;
+  static constexpr int STAGES = 5;
   static constexpr int o_q = STAGES * PF_STAGE;
   static constexpr int o_merge = o_q + QSLOTS * RT * QROW;
   static constexpr int o_ml = o_merge + PF_WARPS * 8 * OROW * 4;
@@ -50,8 +50,7 @@ struct FewCfg {
   static constexpr int total(int n) { return o_pre + Kept::bytes(n); }
   static constexpr int most = o_pre + KEPT_MOST;
 };
-static_assert(FewCfg<128, 1>::most <= 232448 && FewCfg<128, 2>::most <= 232448 && FewCfg<128, 4>::most <= 232448,
-              "shared memory of a CTA");
+static_assert(FewCfg<128, 1>::most <= 232448 && FewCfg<128, 2>::most <= 232448, "shared memory of a CTA");
 
 // One part of a (request, kv head): blocks [blk, blk + nblk) of its `of`.
 struct Segment {
@@ -321,20 +320,19 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
     const Segment s = meta[slot];
     if (s.nblk == 0) break;
     const uint32_t qs = smem_u32(smem + C::o_q + slot * RT * C::QROW);
-    uint32_t qf[NT <= 2 ? NT : 1][HD / 16][2];
-    if constexpr (NT <= 2) {
+    uint32_t qf[NT][HD / 16][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k2 = 0; k2 < HD / 32; ++k2) {
-          uint32_t r4[4];
-          ldsm4(r4, qs + (nt * 8 + (lane & 7)) * C::QROW + k2 * 64 + (lane >> 3) * 16);
-          qf[nt][2 * k2][0] = r4[0]; qf[nt][2 * k2][1] = r4[1];
-          qf[nt][2 * k2 + 1][0] = r4[2]; qf[nt][2 * k2 + 1][1] = r4[3];
-        }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&qempty[slot]);
-    }
+      for (int k2 = 0; k2 < HD / 32; ++k2) {
+        uint32_t r4[4];
+        ldsm4(r4, qs + (nt * 8 + (lane & 7)) * C::QROW + k2 * 64 + (lane >> 3) * 16);
+        qf[nt][2 * k2][0] = r4[0]; qf[nt][2 * k2][1] = r4[1];
+        qf[nt][2 * k2 + 1][0] = r4[2]; qf[nt][2 * k2 + 1][1] = r4[3];
+      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&qempty[slot]);
+    if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
     // keys [first, last] are what this lane's rows see
     int first[NT][2], last[NT][2];
 #pragma unroll
@@ -375,26 +373,13 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
             for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
-          uint32_t b4[NT <= 2 ? 1 : NT][2];
-          if constexpr (NT > 2) {
-#pragma unroll
-            for (int n2 = 0; n2 < NT / 2; ++n2) {
-              uint32_t r4[4];
-              ldsm4(r4, qs + (n2 * 16 + (lane & 7) + (lane >> 4) * 8) * C::QROW + ks * 32 + ((lane >> 3) & 1) * 16);
-              b4[2 * n2][0] = r4[0]; b4[2 * n2][1] = r4[1];
-              b4[2 * n2 + 1][0] = r4[2]; b4[2 * n2 + 1][1] = r4[3];
-            }
-          }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t a[4];
             const int ch = 2 * ks + lc;
             ldsm4(a, kb + k_at[mt] + (ks >= 4 ? part : 0u) + (((ch & 7) ^ (lr & 7)) << 4));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (NT <= 2) mma16<BF>(sc[mt][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-              else mma16<BF>(sc[mt][nt], a, b4[nt][0], b4[nt][1]);
-            }
+            for (int nt = 0; nt < NT; ++nt) mma16<BF>(sc[mt][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
           }
         }
         // softmax of the block's columns: this lane has keys g, g + 8 of each
@@ -476,11 +461,6 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
       turn ^= 1;
       if (++stage == C::STAGES) { stage = 0; sphase ^= 1; }
     }
-    if constexpr (NT > 2) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&qempty[slot]);
-    }
-    if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
 
     // join the eight warps' states, eight rows at a time
 #pragma unroll
@@ -715,9 +695,7 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
 
 template <int HD, bool BF>
 cudaError_t launch_rows(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
-  return p.few_rows <= 8    ? launch<HD, BF, 1>(p, kv, w, st)
-         : p.few_rows <= 16 ? launch<HD, BF, 2>(p, kv, w, st)
-                            : launch<HD, BF, 4>(p, kv, w, st);
+  return p.few_rows <= 8 ? launch<HD, BF, 1>(p, kv, w, st) : launch<HD, BF, 2>(p, kv, w, st);
 }
 
 }  // namespace
