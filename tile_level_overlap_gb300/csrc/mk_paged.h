@@ -76,9 +76,10 @@ struct PagedParts {
 // compiled to, 0: any.  `done` is the kernel's own word, a bit per device.
 cudaError_t paged_prepare(const void* kernel, int smem, int regs, int device, std::atomic<uint64_t>* done);
 
-// Launch as a programmatic dependent of what precedes in the stream.
+// Launch, as a programmatic dependent of what precedes in the stream or not.
 template <class... P, class... A>
-inline cudaError_t paged_launch(void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t st, A&&... args) {
+inline cudaError_t paged_launch_if(bool dependent, void (*kernel)(P...), int grid, int threads, int smem,
+                                   cudaStream_t st, A&&... args) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -88,8 +89,12 @@ inline cudaError_t paged_launch(void (*kernel)(P...), int grid, int threads, int
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = dependent ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+template <class... P, class... A>
+inline cudaError_t paged_launch(void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t st, A&&... args) {
+  return paged_launch_if(true, kernel, grid, threads, smem, st, std::forward<A>(args)...);
 }
 
 cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,

@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   const int TS = 128 / P.rep, TT = 2 * TS;  // tokens of a half, of a tile
   const bool split_v = P.page_shift < PC_SPLIT_V;
 
-  if (P.few_rows == 0) grid_wait_prior();  // no few-row kernel before it that has waited
   grid_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
@@ -635,7 +634,10 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
   const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF>,
                                       ChunkCfg<HD>::most, PC_REGS, p.device, &ready);
   if (e != cudaSuccess) return e;
-  return paged_launch(paged_chunk_kernel<HD, BF>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st, tq, tk, tv, p, w);
+  // without the few-row kernel before it, which waits for what is before both, it
+  // is launched behind that as a whole
+  return paged_launch_if(p.few_rows > 0, paged_chunk_kernel<HD, BF>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
+                         tq, tk, tv, p, w);
 }
 
 }  // namespace
