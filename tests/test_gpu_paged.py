@@ -468,6 +468,15 @@ def test_keys_past_32_bit_offsets(workspace):
     assert torch.equal(kc[pages - 1, :, 255], qkv[0, 16:32]) and torch.equal(kv[1, 0, :, 5], qkv[1, 32:])
 
 
+def test_requests_that_share_pages(workspace):
+    # one prefix in the tables of all, also twice in one of them
+    s = make_attention([400, 400, 400], [1, 2, 40], 8, 2, 128, 16, torch.bfloat16, seed=17)
+    s["table"][1, :20] = s["table"][0, :20]
+    s["table"][2, :20] = s["table"][0, :20]
+    s["table"][2, 21] = s["table"][2, 20]
+    check_attention(s, workspace=workspace)
+
+
 def test_many_requests(workspace):
     rng = np.random.default_rng(4)
     for n, hi in ((4096, 40), (1000, 300)):

@@ -6,7 +6,10 @@
 // them all.  The work is the list of key blocks (128 keys) of all tiles, end
 // to end, after the causal bound and the window; each persistent CTA (one per
 // SM) takes an equal run of it, and rows whose keys lie in several runs are
-// joined as in the few-row kernel.
+// joined as in the few-row kernel.  Measured with 32 query heads on 8 kv heads of
+// 128: a prompt of 8192 tokens 363 us (1514 TFLOP/s), of 16384 1403 us (1567), 2 x
+// 512 tokens over 4-12K cached keys 102 us; a block of keys takes 3050 cycles, 2048
+// of them products.
 //
 // Warps of a CTA: two load (TMA: queries, K and V blocks page by page, 128-byte
 // swizzle), one for each half issues tcgen05.mma, two groups of four own
