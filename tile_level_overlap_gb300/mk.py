@@ -380,20 +380,31 @@ def _heads(device, dtype, **wanted):
         _need(s[2] == 1 and (shape[1] == 1 or s[1] == shape[2]), f"{name}: heads that lie end to end")
 
 
+_torch_parts = None
+
+
+def _parts():
+    """What calls on tensors need of torch, looked up once: int32, float32, the
+    device guard, the current device's index (None where there is no other device
+    that could be current) and the current stream's address by device index."""
+    global _torch_parts
+    if _torch_parts is None:
+        import torch
+        _torch_parts = (torch.int32, torch.float32, torch.cuda.device,
+                        torch.cuda.current_device if torch.cuda.device_count() > 1 else None,
+                        # without a Stream object for it
+                        getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                            lambda d: torch.cuda.current_stream(d).cuda_stream))
+    return _torch_parts
+
+
 class _OnDevice:
     """Calls on one device's tensors: its current stream, or a given one, with
     that device current."""
 
     def _place(self, device):
-        import torch
         self.device, self._dev = device, device.index
-        self._i32, self._f32 = torch.int32, torch.float32
-        self._guard = torch.cuda.device
-        # None where there is no other device that could be current
-        self._current = torch.cuda.current_device if torch.cuda.device_count() > 1 else None
-        # the current stream as an address, without a Stream object for it
-        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda d: torch.cuda.current_stream(d).cuda_stream)
+        self._i32, self._f32, self._guard, self._current, self._raw_stream = _parts()
 
     def _elsewhere(self, fn, *args) -> int:
         """fn(*args) with the tensors' device current, which it is not."""
@@ -412,6 +423,9 @@ class Rope:
                  sections=None, interleaved: bool = False, axis_of_pair=None, inv_freq=None):
         rot = head_dim if rotary_dim is None else int(rotary_dim)
         half = rot // 2
+        if axis_of_pair is None and sections is not None and len(sections) == 1:
+            sections, half_of = None, sections[0]
+            _need(half_of == half, "sections: rotary_dim / 2 pairs in all are wanted")
         if axis_of_pair is None and sections is not None:
             _need(sum(sections) == half, "sections: rotary_dim / 2 pairs in all are wanted")
             n = len(sections)
@@ -426,7 +440,7 @@ class Rope:
         _need(inv_freq is None or len(inv_freq) == half, "inv_freq: one per pair")
         _need(rot <= head_dim, "rotary_dim: at most head_dim")
         self.c = mk_rope()
-        axes = None if axis_of_pair is None else (ctypes.c_uint8 * half)(*[int(a) for a in axis_of_pair])
+        axes = None if axis_of_pair is None else bytes(axis_of_pair)
         freq = None if inv_freq is None else (ctypes.c_double * half)(*[float(f) for f in inv_freq])
         _check(lib().mk_rope_init(ctypes.byref(self.c), rot, float(theta), freq, self.n_axes, axes),
                "mk_rope_init")
