@@ -17,13 +17,13 @@
 // keys at head_dim 128, 128 at 64) page by page through a ring with TMA, 128-byte
 // swizzle; another loads the values (one warp for both took longer to issue the
 // small pages' boxes than HBM takes for them: 64 x 4096 keys in pages of 16 174
-// against 169 us, 32 ragged rows of heads of 64 23.8 against 20.7).  Eight consumer warps in two groups take
-// the blocks in turn, 16 (32) keys each warp, with a softmax state of their
-// own: S^T = K Q^T and O^T += V^T P^T by warp-level products, keys and
-// dimensions on the 16-row side and the query rows on the 8-column side, so
-// that 8 rows fill a product that would be half empty the other way round,
-// and the softmax of a row stays in the lanes that rescale its output.  The
-// legacy tensor path is ample here (a block costs its four warps 16 products
+// against 169 us, 32 ragged rows of heads of 64 23.8 against 20.7).  Eight
+// consumer warps in two groups take the blocks in turn, 16 (32) keys each warp,
+// with a softmax state of their own: S^T = K Q^T and O^T += V^T P^T by warp-level
+// products, keys and dimensions on the 16-row side and the query rows on the
+// 8-column side, so that 8 rows fill a product that would be half empty the other
+// way round, and the softmax of a row stays in the lanes that rescale its output.
+// The legacy tensor path is ample here (a block costs its four warps 16 products
 // each).  At the end of a pair the eight states are joined in shared memory.
 #include "mk_paged_dev.cuh"
 #include "mk_tmap.h"
