@@ -450,7 +450,9 @@ typedef struct {
  *     one that needs no page is still served).
  * Pages are taken as they are named; the operators that use a page check it (one
  * that no cache can have gives the slot 2^31 - 1).  *n_free outside 0 .. free_capacity is latched and clamped.
- * All pointers device; n_left must not be n_free.  n * max_blocks < 2^31 and
+ * All pointers device.  The arrays written (the batch's, *n_left, *status) may
+ * overlap neither one another nor those read: a step whose ctx_lens are the last
+ * one's kv_lens needs two buffers in turn.  n * max_blocks < 2^31 and
  * max_blocks * page_size <= 2^30. */
 int mk_paged_tables(const mk_paged_batch *batch, const int32_t *ctx_lens, const int32_t *new_lens,
                     const int32_t *free_pages, int free_capacity, const int32_t *n_free,

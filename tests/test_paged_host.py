@@ -132,6 +132,22 @@ def test_bad_table_arguments_are_refused(lib):
     assert lib.mk_paged_tables(None, *ok.values(), None) == 1
 
 
+@pytest.mark.parametrize("batch_kw,call_kw", [
+    (dict(), dict(ctx=12 * ADDR)),                       # the batch's own kv_lens as the cached lengths
+    (dict(), dict(ctx=12 * ADDR + 12)),                  # one word in common
+    (dict(), dict(new=12 * ADDR - 12)), (dict(), dict(new=11 * ADDR + 16)), (dict(), dict(free=10 * ADDR + 124)),
+    (dict(), dict(free=14 * ADDR - 36)), (dict(), dict(n_left=5 * ADDR)), (dict(), dict(n_left=4 * ADDR + 36)),
+    (dict(), dict(n_left=2 * ADDR + 12)), (dict(), dict(status=5 * ADDR)), (dict(), dict(status=6 * ADDR)),
+    (dict(slots=13 * ADDR), dict()), (dict(slots=13 * ADDR + 2396), dict()), (dict(cu_new=12 * ADDR - 16), dict()),
+])
+def test_tables_that_overlap_are_refused(lib, batch_kw, call_kw):
+    # (free_pages at 14 * ADDR - 36 meets the slots with its last word)
+    b = batch(**{**dict(block_table=10 * ADDR, cu_new=11 * ADDR, kv_lens=12 * ADDR, positions=13 * ADDR,
+                        slots=14 * ADDR, max_tokens=600), **batch_kw})
+    ok = dict(ctx=2 * ADDR, new=3 * ADDR, free=4 * ADDR, cap=10, n_free=5 * ADDR, n_left=6 * ADDR, status=None)
+    assert lib.mk_paged_tables(ctypes.byref(b), *{**ok, **call_kw}.values(), None) == 1
+
+
 @pytest.mark.parametrize("rot,theta,axes", [(16, 1e4, 1), (64, 5e5, 1), (128, 1e6, 3), (96, 1e4, 4)])
 def test_rope_table_is_the_fraction_of_a_turn(lib, rot, theta, axes):
     half = rot // 2

@@ -592,12 +592,25 @@ extern "C" int mk_paged_tables(const mk_paged_batch* b, const int32_t* ctx_lens,
                                int32_t* status, void* stream) {
   const int rc = check_batch(b);
   if (rc != MK_OK) return rc;
-  if (!ctx_lens || !new_lens || !n_free || !n_left || n_left == n_free || free_capacity < 0 ||
+  if (!ctx_lens || !new_lens || !n_free || !n_left || free_capacity < 0 ||
       (free_capacity > 0 && !free_pages) || (b->max_tokens > 0 && (!b->positions || !b->slots)))
     return MK_ERR_INVALID_ARG;
   const void* ptrs[] = {ctx_lens, new_lens, free_pages, n_free, n_left, status, b->positions, b->slots};
   for (const void* p : ptrs)
     if (!al4(p)) return MK_ERR_INVALID_ARG;
+  // A block may still read the lengths when another has written its part: what
+  // is written shares no word with anything else of the call.
+  const struct { const int32_t* at; int64_t words; } arrays[] = {
+      {b->block_table, (int64_t)b->n * b->max_blocks}, {b->cu_new, b->n + 1}, {b->kv_lens, b->n},
+      {b->positions, b->max_tokens}, {b->slots, b->max_tokens}, {n_left, 1}, {status, status ? 1 : 0},
+      {ctx_lens, b->n}, {new_lens, b->n}, {free_pages, free_capacity}, {n_free, 1}};
+  constexpr int n_arrays = sizeof(arrays) / sizeof(arrays[0]), n_written = 7;
+  for (int i = 0; i < n_written; ++i)
+    for (int j = i + 1; j < n_arrays; ++j)
+      if (arrays[i].words > 0 && arrays[j].words > 0 &&
+          (uintptr_t)arrays[i].at < (uintptr_t)arrays[j].at + 4 * arrays[j].words &&
+          (uintptr_t)arrays[j].at < (uintptr_t)arrays[i].at + 4 * arrays[i].words)
+        return MK_ERR_INVALID_ARG;
   PagedTablesParams p{};
   p.ctx = ctx_lens; p.add = new_lens; p.free_pages = free_pages; p.n_free = n_free;
   p.table = b->block_table; p.cu = b->cu_new; p.kv = b->kv_lens; p.pos = b->positions;

@@ -477,7 +477,8 @@ class PagedBatch(_OnDevice):
         """mk_paged_tables: fill the tables from device int32 lengths [n], taking
         pages from the end of free_pages[0 : n_free[0]]; n_left[0] receives what
         remains.  `status` (int32 [1]) receives MK_ERR_BOUNDS where a request is
-        refused."""
+        refused.  No tensor that is written may be, or overlap, another of the
+        call's (ctx_lens is not the batch's own kv_lens)."""
         i32, dev, n = self._i32, self._dev, self.n
         if not (ctx_lens.dtype is i32 and ctx_lens.get_device() == dev and ctx_lens.numel() == n
                 and ctx_lens.is_contiguous() and new_lens.dtype is i32 and new_lens.get_device() == dev
