@@ -391,6 +391,8 @@ enum { MK_BF16 = 0, MK_FP16 = 1 };
 
 /* Requests one call of the paged operators takes. */
 #define MK_PAGED_MAX_REQUESTS 4096
+/* Query (kv) heads a cache has at most. */
+#define MK_PAGED_MAX_HEADS 65536
 /* Scratch of mk_paged_attention, whatever the call's sizes.  Nothing in it
  * lives from one call to the next and it needs no initialisation; calls that
  * may overlap (two streams, two graphs replayed at once) need one each. */

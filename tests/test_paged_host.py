@@ -88,6 +88,21 @@ def test_attention_refusals_of_whole_structs(lib):
     assert attention(lib, cache(), batch()) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,rows,width", [
+    (65537, 65537, 1, 8), (1 << 23, 1, 700, 8), (1 << 24, 1 << 20, 1, 8), (0x7fffffff, 0x7fffffff, 1, 8),
+    # 2^31 rows on 2^16 heads over 2^30 keys: work whose count passes 64 bits
+    (1 << 16, 1 << 16, 0x7fffffff, 1 << 26), (1 << 16, 1 << 14, 1 << 30, 1 << 26),
+])
+def test_sizes_past_the_counters_are_refused(lib, hq, hkv, rows, width):
+    c = cache(n_q_heads=hq, n_kv_heads=hkv)
+    b = batch(n=1, max_blocks=width, max_tokens=rows)
+    assert attention(lib, c, b, qs=hq * 128 + 8, os=hq * 128 + 8) == 5
+    if hq > mk.MK_PAGED_MAX_HEADS:
+        args = (ADDR, hq * 128, ADDR, hkv * 128, ADDR, hkv * 128, ADDR, hq * 128, None, None, 1e-6, None, None, 0,
+                ADDR, rows, None)
+        assert lib.mk_paged_append(ctypes.byref(c), *args) == 5
+
+
 def test_bad_append_arguments_are_refused(lib):
     rope = mk.mk_rope()
     assert lib.mk_rope_init(ctypes.byref(rope), 128, 1e4, None, 1, None) == 0

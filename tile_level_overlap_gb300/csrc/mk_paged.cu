@@ -546,6 +546,8 @@ int check_cache(const mk_paged_cache* c) {
   for (int64_t s : strides)
     if ((s & 7) || s < c->head_dim || s >= (1ll << 38)) return MK_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return MK_ERR_UNSUPPORTED;
+  // a token's heads are counted in bytes in 32 bits
+  if (c->n_q_heads > MK_PAGED_MAX_HEADS || c->n_kv_heads > MK_PAGED_MAX_HEADS) return MK_ERR_UNSUPPORTED;
   if (log2_page(c->page_size) < 0) return MK_ERR_UNSUPPORTED;
   if ((int64_t)c->n_pages * c->page_size > 0x7fffffffll) return MK_ERR_UNSUPPORTED;
   return MK_OK;
@@ -722,9 +724,10 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch*
   p.hkv = c->n_kv_heads; p.rep = c->n_q_heads / c->n_kv_heads;
   p.window = window ? window : 0x7fffffff;
   p.scale = scale != 0.f ? scale : 1.0f / sqrtf((float)c->head_dim);
-  // units of work (key blocks and overheads of tiles or requests) are counted in 32 bits
-  const int64_t tiles = (int64_t)b->max_tokens * p.rep / 64 + b->n;
-  if (tiles * c->n_kv_heads * ((int64_t)b->max_blocks * b->page_size / 64 + 4) > 0x7fffffffll)
+  // units of work (key blocks and overheads of tiles or requests) are counted in 32
+  // bits; their bound itself may pass 64
+  const double tiles = (double)((int64_t)b->max_tokens * p.rep / 64 + b->n);
+  if (tiles * c->n_kv_heads * (double)((int64_t)b->max_blocks * b->page_size / 64 + 4) > 2147483647.0)
     return MK_ERR_UNSUPPORTED;
   const PagedKv kv = {c->k, c->v, c->page_stride, c->head_stride, c->token_stride,
                       c->n_pages, c->n_kv_heads, c->page_size};

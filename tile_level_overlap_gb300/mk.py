@@ -26,6 +26,7 @@ MK_PREFILL = 1
 MK_LM_FUSED, MK_LM_SEPARATE = 0, 1
 MK_BF16, MK_FP16 = 0, 1
 MK_PAGED_MAX_REQUESTS = 4096
+MK_PAGED_MAX_HEADS = 65536
 MK_PAGED_WORKSPACE_BYTES = 64 << 20  # scratch of mk_paged_attention
 TRACE_WORDS = 16  # u64 words per trace record (mk_trace_copy)
 MK_NOALLOC_SCRATCH_BYTES = 16 << 20  # static device scratch of mk_decode_step_noalloc
