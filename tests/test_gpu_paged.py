@@ -527,6 +527,28 @@ def test_on_another_stream_and_in_graphs(workspace):
     assert torch.equal(outs[0], want2)
 
 
+def test_the_workspace_is_of_the_calls_stream():
+    """Memory that the current stream has given back, and may still be using, is
+    not handed to a first call on another stream."""
+    s = make_attention([40, 0], [1, 3], 4, 2, 64, 16, torch.bfloat16)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    given_back = torch.empty(mk.MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    at = given_back.data_ptr()
+    del given_back
+    cache = mk.PagedCache(s["k"], s["v"], 4)
+    with torch.cuda.stream(other):
+        out = torch.empty_like(s["q"])
+    batch = mk.PagedBatch(ints(s["table"]), ints(s["cu"]), ints(s["kv"]), page_size=16, max_new=3)
+    other.wait_stream(torch.cuda.current_stream())
+    cache.attention(s["q"], batch, out, stream=other)
+    assert cache.workspace.data_ptr() != at
+    torch.cuda.synchronize()
+    want = torch.empty_like(s["q"])
+    cache.attention(s["q"], batch, want)
+    assert torch.equal(out, want) and cache.status() == 0
+
+
 @pytest.mark.parametrize("new", [[1, 2], [70, 2]])
 def test_a_nan_stays_with_its_row(new, workspace):
     s = make_attention([300, 200], new, 8, 2, 128, 16, torch.bfloat16, seed=30, garbage=0.0)

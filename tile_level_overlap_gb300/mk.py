@@ -513,7 +513,9 @@ class PagedCache(_OnDevice):
     shape with contiguous head_dim, equal strides for both).  `workspace`
     (uint8, MK_PAGED_WORKSPACE_BYTES) may be shared by caches whose calls do not
     overlap; without one the first attention call allocates it.  Holds
-    references to the tensors."""
+    references to the tensors.  The status word is cleared on the stream that is
+    current when the cache is made (outside of a capture); calls on other streams
+    are ordered behind that by the caller, as behind one another."""
 
     def __init__(self, k, v, n_q_heads: int, workspace=None):
         import torch
@@ -602,9 +604,12 @@ class PagedCache(_OnDevice):
         [rows, n_q_heads] or None."""
         if self.workspace is None:
             import torch
-            _need(not torch.cuda.is_current_stream_capturing(),
-                  "workspace: give one, or call once before the capture (it would belong to the graph)")
-            self._set_workspace(torch.empty(MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device))
+            # on the call's stream: memory that another one has given back may
+            # still be in use there
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                _need(not torch.cuda.is_current_stream_capturing(),
+                      "workspace: give one, or call once before the capture (it would belong to the graph)")
+                self._set_workspace(torch.empty(MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device))
         hq, d, dev, typ = self.n_q_heads, self.head_dim, self._dev, self.dtype
         n = q.shape[0]
         wide, qs, os = (n, hq, d), q.stride(), out.stride()
