@@ -482,7 +482,8 @@ int mk_rope_init(mk_rope *rope, int rotary_dim, double theta, const double *inv_
 /* The new tokens' q, k and v: RMSNorm of each q and k head where a gain is given
  * (x / sqrt(mean x^2 + eps) * gain, as the plan's qk_norm), rotary positions, q to
  * q_out, k and v to their slots of the cache; sums and angles in fp32 or more,
- * each output rounded once.
+ * each output rounded once.  Elements that have neither gain nor rotation are
+ * copied bit for bit.
  *   q [n_tokens][n_q_heads][head_dim], k, v [n_tokens][n_kv_heads][head_dim],
  *     q_out as q: *_stride elements from token to token (multiples of 8; heads
  *     lie end to end), so that q, k, v can be parts of one projection's rows.

@@ -1,0 +1,85 @@
+"""Edges of the paged-cache operators on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_paged as paged
+from tile_level_overlap_gb300 import build, mk
+
+pytestmark = pytest.mark.gpu
+DEV, TYPES = paged.DEV, paged.TYPES
+ints = paged.ints
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    build.build()
+    mk.lib()
+
+
+# ---------------------------------------------------------------- append
+
+def bits(t):
+    return t.contiguous().view(torch.int16)
+
+
+@pytest.mark.parametrize("t", [5, 700])                        # a block per token; the ring
+@pytest.mark.parametrize("d,rot,typ", [(128, 0, "bf16"), (128, 32, "bf16"), (64, 48, "fp16"), (64, 0, "fp16"), (128, 96, "fp16")])
+@pytest.mark.parametrize("gains", ["", "q", "k", "qk"])
+def test_elements_that_do_not_turn_stay(t, d, rot, typ, gains):
+    """Infinities, NaN (their payloads) and negative zeros outside the rotation:
+    copied where there is no gain, x / sqrt(mean x^2 + eps) * gain where there
+    is one, and nothing of them in their neighbours.  (A head with an infinity
+    or a NaN has a norm that is not finite: its elements are 0 and NaN, or all
+    NaN, as the formula says.)"""
+    typ, hq, hkv, page = TYPES[typ], 6, 3, 16
+    g = torch.Generator().manual_seed(t + d + rot)
+    x = torch.randn(t, hq + 2 * hkv, d, generator=g).to(typ)
+    spoil = torch.rand(t, hq + 2 * hkv, d, generator=g)
+    spoil[:, :, :rot] = 1.0
+    spoil[:, ::3] = 1.0                                         # every third head has finite values alone
+    plain = x.clone()
+    x[spoil < 0.02], x[(spoil >= 0.02) & (spoil < 0.04)] = float("inf"), -float("inf")
+    x[(spoil >= 0.04) & (spoil < 0.05)] = float("nan")
+    x[(spoil >= 0.05) & (spoil < 0.10)] = -0.0
+    raw = bits(x).view(t, hq + 2 * hkv, d)
+    raw[(spoil >= 0.10) & (spoil < 0.11)] = 0x7fc5 if typ == torch.bfloat16 else 0x7d23   # NaN with a payload
+    x = raw.view(typ).to(DEV)
+    gain = (1 + 0.1 * torch.randn(d, generator=g)).to(typ).to(DEV)
+    qn, kn = gain if "q" in gains else None, gain if "k" in gains else None
+    rope, pos = (mk.Rope(d, rotary_dim=rot), ints(np.arange(t) + 1)) if rot else (None, None)
+    pages = -(-t // page)
+    slots = ints(np.arange(t))
+
+    def run(rows):
+        kc, vc = (torch.zeros(pages, page, hkv, d, dtype=typ, device=DEV) for _ in range(2))
+        out = torch.zeros(t, hq, d, dtype=typ, device=DEV)
+        cache = mk.PagedCache(kc.transpose(1, 2), vc.transpose(1, 2), n_q_heads=hq)
+        cache.append(rows[:, :hq], rows[:, hq:hq + hkv], rows[:, hq + hkv:], slots, pos, rope, q_out=out, q_norm=qn, k_norm=kn, eps=1e-6)
+        assert cache.status() == 0
+        flat = [c.reshape(-1, hkv, d)[:t] for c in (kc, vc)]
+        return out, *flat
+
+    got = run(x)
+    clean = run(plain.to(DEV))
+    parts = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    assert torch.equal(bits(got[2]), bits(parts[2]))
+    for out, ref, part, gn in zip(got[:2], clean[:2], parts, (qn, kn)):
+        if gn is None:
+            assert torch.equal(bits(out[..., rot:]), bits(part[..., rot:]))
+            assert torch.equal(bits(out[..., :rot]), bits(ref[..., :rot]))    # pairs of finite elements
+            continue
+        x64 = part[..., :].double()
+        want = x64 / torch.sqrt((x64 * x64).mean(-1, keepdim=True) + 1e-6) * gn.double()
+        same = torch.isfinite(x64).all(-1)                      # heads whose norm is finite
+        u = torch.finfo(typ).eps / 2
+        o64, w = out[..., rot:].double(), want[..., rot:]
+        assert torch.equal(torch.isnan(o64), torch.isnan(w))
+        # one rounding, and the norm's sum of d squares, rsqrt and two products in fp32
+        err = (o64 - w).abs() - (u * w.abs() + (d + 8) * 2.0 ** -24 * w.abs() + 2.0 ** -24)
+        assert (err[same] <= 0).all()
+        assert torch.equal(torch.signbit(out[..., rot:])[same], torch.signbit(w)[same])
+        zero = w == 0
+        assert (o64[zero] == 0).all()

@@ -177,9 +177,9 @@ __device__ __forceinline__ float2 pair_turn(int pos, uint64_t turn) {
   return make_float2(c, s);
 }
 
-// A lane's share of a head: two chunks, the angles of their pairs (1, 0 where
-// they do not turn) and the gains.  Packed pairs of floats, two IEEE operations
-// an instruction.
+// A lane's share of a head: two chunks, the angles of their pairs where they
+// turn, and the gains.  Packed pairs of floats, two IEEE operations an
+// instruction.
 template <int HD, bool BF>
 struct HeadLane {
   static constexpr int G = HD / 16;
@@ -213,18 +213,17 @@ struct HeadLane {
   // lanes of a head end to end
   static __device__ __forceinline__ int place(int pair) { return (pair & 7) * G + (pair >> 3); }
   __device__ __forceinline__ void angles(const float2* cs, int lane) {
+    if (!turn) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float2 x = make_float2(1.f, 0.f), y = x;
-      if (turn) {
-        x = cs[2 * i * G + lane % G];
-        y = cs[(2 * i + 1) * G + lane % G];
-      }
+      const float2 x = cs[2 * i * G + lane % G], y = cs[(2 * i + 1) * G + lane % G];
       c[i] = pack_f32x2(x.x, y.x);
       s[i] = pack_f32x2(x.y, y.y);
     }
   }
   // Norm and turn a head's chunks in place (whole warp; is_q: a query head).
+  // Chunks that do not turn pass through no rotation (0 times an infinity is a
+  // NaN); without a gain either they stay bit for bit.
   __device__ __forceinline__ void apply(const PagedAppendParams& P, uint4& wa, uint4& wb, bool is_q) {
     const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
     u64 a[4], b[4];
@@ -233,6 +232,7 @@ struct HeadLane {
       a[i] = widen(ua[i]);
       b[i] = widen(ub[i]);
     }
+    const bool gain = is_q ? P.q_gain != nullptr : P.k_gain != nullptr;
     if (P.q_gain || P.k_gain) {
       u64 acc = 0;
 #pragma unroll
@@ -240,7 +240,7 @@ struct HeadLane {
       float ss = pair_sum(acc);
 #pragma unroll
       for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (is_q ? P.q_gain != nullptr : P.k_gain != nullptr) {
+      if (gain) {
         const float inv = rsqrtf(ss * (1.f / HD) + P.eps);
         const u64 inv2 = pack_f32x2(inv, inv);
         const uint4 x = is_q ? gq[0] : gk[0], y = is_q ? gq[1] : gk[1];
@@ -253,6 +253,17 @@ struct HeadLane {
       }
     }
     uint32_t oa[4], ob[4];
+    if (!turn) {
+      if (!gain) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        oa[i] = narrow(a[i]);
+        ob[i] = narrow(b[i]);
+      }
+      wa = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+      wb = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const u64 minus = s[i] ^ 0x8000000080000000ull;
