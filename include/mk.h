@@ -509,7 +509,9 @@ int mk_paged_append(const mk_paged_cache *cache, const void *q, int64_t q_stride
  *   out = sum_j exp(scale q.k_j - lse) v_j,  lse = log sum_j exp(scale q.k_j)
  * A row that sees no key (kv_lens[r] less than the new tokens) gives out = 0 and
  * lse = -inf.  Sums and the softmax are fp32; the weights of a row enter the
- * product with V relative to a running maximum, rounded to the cache's type.
+ * product with V relative to a running maximum, rounded to the cache's type (in
+ * fp16 scaled up, so that weights down to 2^-21 of a row's largest keep all bits
+ * and weights above 2^-32 of it count).
  * Keys that no row of the request sees (the tail of its last page, pages before
  * the window) are not read into any sum, whatever they hold; table entries of
  * pages that hold no such key are not looked at.  Within the keys a request

@@ -3,12 +3,13 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import test_gpu_paged as paged
 from tile_level_overlap_gb300 import build, mk
 
 pytestmark = pytest.mark.gpu
 DEV, TYPES = paged.DEV, paged.TYPES
-ints = paged.ints
+ints, f64 = paged.ints, paged.f64
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -17,6 +18,11 @@ def _built():
         pytest.skip("needs a CUDA device")
     build.build()
     mk.lib()
+
+
+@pytest.fixture(scope="module")
+def workspace():
+    return torch.full((mk.MK_PAGED_WORKSPACE_BYTES // 4,), float("nan"), device=DEV)
 
 
 # ---------------------------------------------------------------- append
@@ -83,3 +89,39 @@ def test_elements_that_do_not_turn_stay(t, d, rot, typ, gains):
         assert torch.equal(torch.signbit(out[..., rot:])[same], torch.signbit(w)[same])
         zero = w == 0
         assert (o64[zero] == 0).all()
+
+
+# ---------------------------------------------------------------- attention: small weights
+
+@pytest.mark.parametrize("new,ctx,d", [([1], [4000], 128), ([2, 1], [3000, 700], 64), ([90], [4000], 128), ([40, 3], [2000, 900], 64)])
+def test_weights_far_below_the_largest_count_in_fp16(new, ctx, d, workspace):
+    """Every 16th key has weight 1 and value 0, the others weight 2^-25.5, which
+    fp16 does not hold, and values of about 3e4: the output is those alone.
+    Tolerance, A the softmax-weighted mean of |v|: output and weights rounded
+    (u |o| + u A), fp32 sums as in the other tests, and what is below fp16's
+    normal range once weights are scaled by 2^7 or more: 2^-32 of a row's
+    largest weight each, of at most 17 keys for each weight of 1."""
+    typ, hq, hkv = torch.float16, 8, 2
+    s = paged.make_attention(ctx, new, hq, hkv, d, 16, typ, seed=d + sum(new), garbage=float("nan"))
+    s["q"].zero_()
+    s["q"][..., 0] = 1.0
+    g = torch.Generator().manual_seed(3)
+    for r in range(len(ctx)):
+        for j in range(-(-int(s["kv"][r]) // 16)):
+            p, m = int(s["table"][r, j]), min(16, int(s["kv"][r]) - 16 * j)
+            s["k"][p, :, :m] = 0
+            s["k"][p, :, 0, 0] = 25.5
+            s["v"][p, :, :m] = (2e4 + 2e4 * torch.rand(hkv, m, d, generator=g)).to(typ).to(DEV)
+            s["v"][p, :, 0] = 0
+    scale = float(np.log(2.0))
+    out, lse = torch.zeros_like(s["q"]), torch.zeros(s["q"].shape[:2], device=DEV)
+    cache = mk.PagedCache(s["k"], s["v"], n_q_heads=hq, workspace=workspace)
+    cache.attention(s["q"], mk.PagedBatch(ints(s["table"]), ints(s["cu"]), ints(s["kv"]), page_size=16, max_new=max(new)), out, lse=lse, scale=scale)
+    assert cache.status() == 0
+    ref, rlse, wabs, smag, vmax = oracle.paged_attention(f64(s["q"]), f64(s["k"]), f64(s["v"]), s["table"], s["cu"], s["kv"], scale)
+    u, keys = torch.finfo(typ).eps / 2, int(s["kv"].max())
+    ds, sums = d * 2.0 ** -22 * smag, (keys / 8 + 64) * 2.0 ** -23
+    tol = u * 1.01 * (np.abs(ref) + wabs) + wabs * (2 * ds[..., None] + sums) + 17 * 2.0 ** -32 * vmax[..., None] + 2.0 ** -24
+    assert ref[..., :].max() > 4e-3 and (tol < 0.1 * np.maximum(ref, 4e-3)).all()
+    assert (np.abs(f64(out) - ref) <= tol).all()
+    assert (np.abs(f64(lse) - rlse) <= ds + sums + 2.0 ** -20 * np.abs(rlse)).all()

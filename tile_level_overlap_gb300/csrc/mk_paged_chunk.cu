@@ -15,11 +15,13 @@
 // swizzle), one for each half issues tcgen05.mma, two groups of four own
 // a half each (thread = row).  Per half and block: S = Q K^T into 128 TMEM columns; its
 // group reads the row, masks it where the block crosses a bound, exponentiates
-// relative to a running maximum and writes P over S in the cache's type; O += P V
-// with P read from TMEM.  The two halves alternate on the tensor cores: while
+// relative to a running maximum and writes P over S in the cache's type (one
+// rounding a weight: a second product for what it drops would cost half of the
+// tensor time); O += P V with P read from TMEM.  The two halves alternate on the tensor cores: while
 // one's softmax runs the other's products do.  The maximum that P is relative
-// to is only moved when it has grown by more than 2^8 (P stays far inside the
-// 16-bit range and sums are fp32), so O, which lives in TMEM, is seldom rescaled.
+// to is only moved when it has grown by more than 2^8 (the known lazy form of the
+// online softmax: P stays inside the 16-bit range and sums are fp32), so O, which
+// lives in TMEM, is seldom rescaled.
 // No wait on O is needed for that: S of block j is issued behind P V of block
 // j - 1, so when S is complete O is at rest.
 #include "mk_paged_dev.cuh"
@@ -38,6 +40,10 @@ static_assert(2 * PC_REGS_SOFT + PC_REGS_REST == 3 * PC_REGS, "registers of the 
 // in blocks: without it the SMs with the short tiles of a prompt's start ended
 // a quarter later than the others.
 constexpr int PC_OVER = 2;
+// P is relative to a maximum that may lag by 2^PC_LAG.  In fp16 it is scaled by
+// 2^PC_TOP_FP16 besides (together 2^15): weights lose bits only 2^21 or more below
+// the row's largest, and are lost 2^32 or more below it, instead of 2^14 and 2^25.
+constexpr float PC_LAG = 8.f, PC_TOP_FP16 = 7.f;
 
 template <int HD>
 struct ChunkCfg {
@@ -454,6 +460,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     const int tok_in = P.token_of(row), hq_in = row - tok_in * P.rep;
     const float cs = fabsf(P.scale) * 1.4426950408889634f;
     const bool neg = P.scale < 0.f;
+    constexpr float top = BF ? 0.f : PC_TOP_FP16;
     uint32_t blkn = 0, sn = 0, on = 0;
     int slot = 0;
     uint32_t mphase = 0;
@@ -506,7 +513,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         t1 = max3(t1, s[126], s[127]);
         const float bm = max3(t0, t1, fmaxf(t2, t3));
         const float mn = fmaxf(mx, bm);
-        if (__any_sync(0xffffffffu, (mn - mx) * cs > 8.f)) {
+        if (__any_sync(0xffffffffu, (mn - mx) * cs > PC_LAG)) {
           const float a = mx == -INFINITY ? 0.f : ex2((mx - mn) * cs);
           l *= a;
           mx = mn;
@@ -522,7 +529,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             }
           }
         }
-        const float ref = mx == -INFINITY ? 0.f : mx * cs;
+        const float ref = (mx == -INFINITY ? 0.f : mx * cs) - top;
         const u64 cs2 = pack_f32x2(cs, cs), ref2 = pack_f32x2(-ref, -ref);
         u64 sum0 = 0, sum1 = 0;
 #pragma unroll
@@ -596,7 +603,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         }
         if (live && P.lse)
           P.lse[(int64_t)(m.row0 + tok0 + tok_in) * (P.hkv * P.rep) + m.head * P.rep + hq_in] =
-              lse_of(mx * cs, l);
+              lse_of(mx * cs - top, l);
       } else {
         // a part: [4 columns][row], a warp's lanes end to end
         float* dst = W.o + (int64_t)m.part * W.rt * HD + prow * 4;
@@ -610,7 +617,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
               *reinterpret_cast<float4*>(dst + (x + i) * W.rt) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
-        if (live) W.ml[(int64_t)m.part * W.rt + prow] = make_float2(mx * cs, l);
+        if (live) W.ml[(int64_t)m.part * W.rt + prow] = make_float2(mx * cs - top, l);
       }
       tc_fence_before();  // the next tile's first P V is issued behind this group's next P
     }

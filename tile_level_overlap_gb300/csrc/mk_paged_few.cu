@@ -35,6 +35,10 @@ constexpr int PF_WARPS = 8;             // consumers
 constexpr int PF_THREADS = 32 * (PF_WARPS + 2);  // and two that load
 constexpr int PF_STAGE = 32768;         // one block's keys, then its values
 constexpr int PF_OVER = 1;              // what a pair costs beside its blocks, in blocks
+// log2 of a row's largest weight in the product with V (its maximum is exact):
+// weights lose bits only 2^28 below it, and are lost 2^39 below it, where fp16
+// from 1 on has 2^14 and 2^25.
+constexpr float PF_TOP_FP16 = 14.f;
 
 template <int HD, int NT>
 struct FewCfg {
@@ -297,6 +301,7 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
   // -------------------------------------------------------------- consumers
   const int grp = warp >> 2, kw = warp & 3, g = lane >> 2, t = lane & 3;
   const float cs = P.scale * 1.4426950408889634f;
+  constexpr float top = BF ? 0.f : PF_TOP_FP16;
   float* merge = reinterpret_cast<float*>(smem + C::o_merge);
   float2* mls = reinterpret_cast<float2*>(smem + C::o_ml);
   // row and 16-byte chunk that this lane addresses in a 16 x 16 matrix load
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float p = ex2(sc[mt][nt][2 * h + e] - ref);
+                const float p = ex2(sc[mt][nt][2 * h + e] - (ref - top));
                 sc[mt][nt][2 * h + e] = p;
                 sum += p;
               }
@@ -479,8 +484,8 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
       }
       named_bar(1, 32 * PF_WARPS);  // the previous rows have been read
       if (g == 0) {
-        mls[warp * RT + nt * 8 + 2 * t] = make_float2(m[nt][0], l[nt][0]);
-        mls[warp * RT + nt * 8 + 2 * t + 1] = make_float2(m[nt][1], l[nt][1]);
+        mls[warp * RT + nt * 8 + 2 * t] = make_float2(m[nt][0] - top, l[nt][0]);
+        mls[warp * RT + nt * 8 + 2 * t + 1] = make_float2(m[nt][1] - top, l[nt][1]);
       }
       float* mine_o = merge + warp * 8 * C::OROW;
 #pragma unroll
