@@ -528,11 +528,11 @@ int mk_paged_append(const mk_paged_cache *cache, const void *q, int64_t q_stride
  * tokens of a request; positions and slots are not read.  MK_ERR_BOUNDS is latched
  * in cache->status, and nothing out of range is touched, where kv_lens[r] is
  * negative (taken as 0) or passes max_blocks * page_size (the keys past it are
- * taken as absent), a page is not
- * one of the cache's (its keys and values count as zeros), or a request's rows
- * are more than max_new, not ordered or past max_tokens (they are left as they
- * were).  The result of a row depends on the batch only through the order in
- * which partial sums of its keys are joined; equal calls give equal bits. */
+ * taken as absent), a page is not one of the cache's (its keys and values count
+ * as zeros), or a request's rows are more than max_new, past max_tokens or out of
+ * order (cu_new falls there, or they begin below an earlier offset): such rows are
+ * left as they were.  The result of a row depends on the batch only through the
+ * order in which partial sums of its keys are joined; equal calls give equal bits. */
 int mk_paged_attention(const mk_paged_cache *cache, const mk_paged_batch *batch, const void *q,
                        int64_t q_stride, void *out, int64_t out_stride, float *lse, float scale,
                        int window, void *stream);

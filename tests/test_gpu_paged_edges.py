@@ -125,3 +125,69 @@ def test_weights_far_below_the_largest_count_in_fp16(new, ctx, d, workspace):
     assert ref[..., :].max() > 4e-3 and (tol < 0.1 * np.maximum(ref, 4e-3)).all()
     assert (np.abs(f64(out) - ref) <= tol).all()
     assert (np.abs(f64(lse) - rlse) <= ds + sums + 2.0 ** -20 * np.abs(rlse)).all()
+
+
+# ---------------------------------------------------------------- attention: offsets and lengths that do not fit
+
+def attend(s, workspace, max_new, window=0):
+    """out, lse (filled with 5 before the call) and the status."""
+    out, lse = torch.full_like(s["q"], 5.0), torch.full(s["q"].shape[:2], 5.0, device=DEV)
+    cache = mk.PagedCache(s["k"], s["v"], n_q_heads=s["q"].shape[1], workspace=workspace)
+    cache.attention(s["q"], mk.PagedBatch(ints(s["table"]), ints(s["cu"]), ints(s["kv"]), page_size=s["page"], max_new=max_new), out, lse=lse, window=window)
+    return f64(out), f64(lse), cache.status()
+
+
+def check_rows(s, got, glse, r, row0, rows, kv, room=1 << 30):
+    """Rows row0 .. row0 + rows as request r's last ones of kv tokens, keys past
+    `room` absent; the tolerance of the other tests (bf16)."""
+    q, d = f64(s["q"]), s["q"].shape[2]
+    u, sums = 2.0 ** -8, (min(kv, room) / 8 + 64) * 2.0 ** -23
+    for i in range(rows):
+        seen = min(kv - rows + i + 1, room)
+        ref, rl, wabs, smag, _ = oracle.paged_attention(q[row0 + i:row0 + i + 1], f64(s["k"]), f64(s["v"]), s["table"][r:r + 1], [0, 1], [seen], d ** -0.5)
+        ds = d * 2.0 ** -22 * smag
+        assert (np.abs(got[row0 + i] - ref[0]) <= (u * 1.01 * (np.abs(ref) + wabs) + wabs * (2 * ds[..., None] + sums))[0]).all(), (r, i)
+        assert (np.abs(glse[row0 + i] - rl[0]) <= (ds + sums + 2.0 ** -20 * np.abs(rl))[0]).all(), (r, i)
+
+
+@pytest.mark.parametrize("cu,served,rows", [
+    ([0, 3, 2, 6], [(0, 0, 3)], 7),                              # the third begins inside the first
+    ([0, 2, 2, 7], [(0, 0, 2)], 6),                              # past the rows
+    ([0, 2, 1, 1, 2, 5, 5, 8], [(0, 0, 2), (4, 2, 3), (6, 5, 3)], 8),   # (the third rests, the fourth begins inside the first)
+    ([0, 4, 0, 4, 0, 4, 0, 4], [(0, 0, 4)], 5),                  # a saw: the first alone
+    ([0, 90, 40, 130], [(0, 0, 90)], 130),                       # the same with tiles
+    ([0, 70, 0, 70, 0, 70, 70, 99], [(0, 0, 70), (6, 70, 29)], 110),
+    ([-2, 3, 1, 4, 30], [(3, 4, 26)], 31),                       # (the first ends at 3)
+    ([0, 30, 33, 20, 50, 50, 52], [(0, 0, 30), (1, 30, 3), (5, 50, 2)], 60),
+])
+def test_offsets_out_of_order(cu, served, rows, workspace):
+    """Where offsets fall, requests that begin below an earlier offset are left
+    out and latched, the others are answered, and rows of no answered one are as
+    they were."""
+    n = len(cu) - 1
+    s = paged.make_attention([60 + 7 * r for r in range(n)], [100] * n, 8, 2, 64, 16, torch.bfloat16, seed=n, garbage=0.0)
+    s["q"], s["cu"] = s["q"][:rows].contiguous(), np.array(cu)
+    got, glse, status = attend(s, workspace, 100)
+    few, flse, fstatus = attend(s, workspace, 4) if max(k for _, _, k in served) <= 4 else (None, None, None)
+    assert status == mk.MK_ERR_BOUNDS and fstatus in (None, mk.MK_ERR_BOUNDS)
+    for o, l in ((got, glse), (few, flse)):
+        if o is None:
+            continue
+        left = np.ones(rows, bool)
+        for r, row0, k in served:
+            left[row0:row0 + k] = False
+            check_rows(s, o, l, r, row0, k, int(s["kv"][r]))
+        assert (o[left] == 5).all() and (l[left] == 5).all()
+
+
+def test_a_long_saw_of_offsets(workspace):
+    # every second request claims all rows: of 2000 the first is answered
+    n, rows = 2000, 300
+    one = paged.make_attention([50], [rows], 8, 2, 64, 16, torch.bfloat16, seed=2, garbage=0.0)
+    table = np.full((n, one["table"].shape[1]), -1)
+    table[0] = one["table"][0]
+    s = dict(one, table=table, cu=np.array([0, rows] * (n // 2) + [0]), kv=np.array([50 + rows] * n))
+    got, glse, status = attend(s, workspace, rows)
+    want, wlse, ok = attend(one, workspace, rows)
+    assert status == mk.MK_ERR_BOUNDS and ok == 0
+    assert np.array_equal(got, want) and np.array_equal(glse, wlse)

@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   // units: the tiles' blocks and overheads.  A thread counts its requests'
   // tiles; a warp together those of a request with many.
   const int per = (P.n + PC_THREADS - 1) / PC_THREADS;
-  int mine = 0;
-  bool bad = false;
+  uint32_t mine = 0;
+  bool bad = false, falls = false;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
     int u = 0, ntile = 0, b0;
@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     if (r < P.n) {
       q = kept.read(P, r);
       bad |= q.bad;
+      falls |= q.falls;
       if ((int64_t)q.add * P.rep > P.few_rows) ntile = (q.add + TT - 1) / TT;
     }
     if (ntile <= 8)
@@ -183,17 +184,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     if (r < P.n) pre[r] = u;
     mine += u;
   }
-  int T;
   int* scan_tmp = reinterpret_cast<int*>(smem + C::o_kv);  // not loaded to yet
-  int at = block_scan<PC_THREADS / 32>(mine, scan_tmp, &T);
-  for (int i = 0; i < per; ++i) {
-    const int r = tid * per + i;
-    if (r >= P.n) break;
-    const int u = pre[r];
-    pre[r] = at;
-    at += u;
-  }
-  if (tid == 0) pre[P.n] = T;
+  const int T = place_units<PC_THREADS / 32>(P, pre, per, mine, falls, scan_tmp);
   if (bad && blockIdx.x == 0) latch(P.status, MK_ERR_BOUNDS);
   fence_proxy_async_smem();  // the scan's words, before a load takes their place
   tc_fence_before();

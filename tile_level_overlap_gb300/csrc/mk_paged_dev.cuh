@@ -123,7 +123,7 @@ __device__ __forceinline__ void tma_page(void* dst, const void* tmap, int token,
 // its first row stands at pos0.
 struct Request {
   int row0, add, pos0, lo, hi;
-  bool bad;
+  bool bad, falls;
 };
 __device__ __forceinline__ Request make_request(const PagedAttnParams& P, int c0, int c1, int kv) {
   Request q;
@@ -132,6 +132,7 @@ __device__ __forceinline__ Request make_request(const PagedAttnParams& P, int c0
   q.bad = kv < 0 || kvp > room;
   q.row0 = c0;
   q.add = 0;
+  q.falls = c1 < c0;
   if (c0 < 0 || c1 < c0 || c1 > P.rows || c1 - c0 > P.max_new) q.bad = true;
   else q.add = c1 - c0;
   q.pos0 = kvp - q.add;
@@ -174,27 +175,75 @@ struct Runs {
   }
 };
 
-// Exclusive prefix sums of one value per thread of a block of W warps.
+// Exclusive prefix sums of one value per thread of a block of W warps; whether
+// any thread says `flag`.  (Unsigned: the sums wrap where the flag discards them.)
 template <int W>
-__device__ __forceinline__ int block_scan(int v, int* tmp, int* total) {
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, bool flag, int* tmp, int* total, bool* any) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  uint32_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, x, o);
+    const uint32_t u = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += u;
   }
-  if (lane == 31) tmp[warp] = x;
-  __syncthreads();
-  int before = 0, all = 0;
+  if (lane == 31) tmp[warp] = (int)x;
+  *any = __syncthreads_or(flag);
+  uint32_t before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
-    const int t = tmp[w];
+    const uint32_t t = (uint32_t)tmp[w];
     before += w < warp ? t : 0;
     all += t;
   }
-  *total = all;
+  *total = (int)all;
   return before + x - v;
+}
+
+// The units of the requests, pre[r] (each thread's `per` consecutive ones, `mine`
+// of them together), to a request's first unit; returns their number.  `falls`:
+// cu falls at one of the thread's requests.  Where it falls anywhere, requests
+// that begin below an earlier offset are refused first: their rows may be another's,
+// and the units of overlapping requests have no bound (the launch's check counts
+// every row of the step once).
+template <int W>
+__device__ __forceinline__ int place_units(const PagedAttnParams& P, int* pre, int per, uint32_t mine, bool falls, int* tmp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r0 = min(tid * per, P.n), r1 = min(r0 + per, P.n);
+  int T;
+  bool any;
+  uint32_t at = block_scan<W>(mine, falls, tmp, &T, &any);
+  if (any) {
+    int top = -0x7fffffff - 1;  // the largest offset up to this thread's last request
+    for (int r = r0; r < r1; ++r) top = max(top, max(P.cu[r], P.cu[r + 1]));
+    int before = top;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before = max(before, u);
+    }
+    __syncthreads();
+    if (lane == 31) tmp[warp] = before;
+    before = __shfl_up_sync(0xffffffffu, before, 1);
+    if (lane == 0) before = -0x7fffffff - 1;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) before = max(before, tmp[w]);
+    __syncthreads();
+    mine = 0;
+    for (int r = r0; r < r1; ++r) {
+      const int c0 = P.cu[r];
+      if (c0 < before) pre[r] = 0;
+      mine += (uint32_t)pre[r];
+      before = max(before, max(c0, P.cu[r + 1]));
+    }
+    at = block_scan<W>(mine, false, tmp, &T, &any);
+  }
+  for (int r = r0; r < r1; ++r) {
+    const int u = pre[r];
+    pre[r] = (int)at;
+    at += (uint32_t)u;
+  }
+  if (tid == 0) pre[P.n] = T;
+  return T;
 }
 
 }  // namespace mk

@@ -164,29 +164,21 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
 
   // units: key blocks of all (request, kv head) pairs, pairs of a request end to end
   const int per = (P.n + PF_THREADS - 1) / PF_THREADS;
-  int mine = 0;
-  bool bad = false;
+  uint32_t mine = 0;
+  bool bad = false, falls = false;
   for (int i = 0; i < per; ++i) {
     const int r = tid * per + i;
     if (r >= P.n) break;
     const Request q = kept.read(P, r);
     bad |= q.bad;
+    falls |= q.falls;
     int u = 0;
     if (q.add > 0 && (int64_t)q.add * P.rep <= P.few_rows)
       u = P.hkv * (max(1, (q.hi + KS - 1) / KS - q.lo / KS) + PF_OVER);
     pre[r] = u;
     mine += u;
   }
-  int T;
-  int at = block_scan<PF_THREADS / 32>(mine, scan_tmp, &T);
-  for (int i = 0; i < per; ++i) {
-    const int r = tid * per + i;
-    if (r >= P.n) break;
-    const int u = pre[r];
-    pre[r] = at;
-    at += u;
-  }
-  if (tid == 0) pre[P.n] = T;
+  const int T = place_units<PF_THREADS / 32>(P, pre, per, mine, falls, scan_tmp);
   if (bad && blockIdx.x == 0) latch(P.status, MK_ERR_BOUNDS);
   __syncthreads();
 
