@@ -191,3 +191,33 @@ def test_a_long_saw_of_offsets(workspace):
     want, wlse, ok = attend(one, workspace, rows)
     assert status == mk.MK_ERR_BOUNDS and ok == 0
     assert np.array_equal(got, want) and np.array_equal(glse, wlse)
+
+
+@pytest.mark.parametrize("new", [2, 50])
+def test_lengths_past_the_table(new, workspace):
+    # rows stand at their positions, keys past the table's width are absent
+    s = paged.make_attention([100, 90, 100], [new] * 3, 8, 2, 64, 16, torch.bfloat16, seed=13, garbage=0.0)
+    room = s["table"].shape[1] * 16
+    s["table"][1] = np.arange(s["table"].shape[1]) % s["k"].shape[0]
+    for kv in (room + 1, room + new - 1, room + 40, 2 ** 31 - 1):
+        t = dict(s, kv=np.array([s["kv"][0], kv, s["kv"][2]]))
+        got, glse, status = attend(t, workspace, new)
+        assert status == mk.MK_ERR_BOUNDS
+        for r in range(3):
+            check_rows(t, got, glse, r, r * new, new, int(t["kv"][r]), room)
+
+
+@pytest.mark.parametrize("n", [500, 1500])
+def test_many_requests_with_chunks(n, workspace):
+    """Decode rows, drafted tokens and chunks of more than eight tiles among
+    several requests a thread, and more of them than are kept in shared memory."""
+    rng = np.random.default_rng(n)
+    ctx = rng.integers(0, 40, n)
+    new = rng.choice([0, 1, 1, 1, 2, 5], n)
+    for r in rng.permutation(n)[:6]:
+        new[r] = int(rng.integers(260, 420))      # 8 query heads on a kv head: tiles of 32 tokens
+    for r in rng.permutation(n)[:30]:
+        new[r] = int(rng.integers(3, 70))
+    s = paged.make_attention(ctx.tolist(), new.tolist(), 8, 1, 64, 16, torch.bfloat16, seed=n, pad=2)
+    paged.check_attention(s, workspace=workspace)
+    paged.check_attention(s, window=33, workspace=workspace)
