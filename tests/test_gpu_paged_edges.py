@@ -1,4 +1,6 @@
 """Edges of the paged-cache operators on the GPU."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -221,3 +223,31 @@ def test_many_requests_with_chunks(n, workspace):
     s = paged.make_attention(ctx.tolist(), new.tolist(), 8, 1, 64, 16, torch.bfloat16, seed=n, pad=2)
     paged.check_attention(s, workspace=workspace)
     paged.check_attention(s, window=33, workspace=workspace)
+
+
+# ---------------------------------------------------------------- threads
+
+def test_tables_of_many_requests_from_two_threads():
+    """Steps of different numbers of requests, all of them past 48 KB of shared memory."""
+    def step(n, errors):
+        b = mk.PagedBatch(ints(np.full((n, 1), -1)), ints([0] * (n + 1)), ints([0] * n), ints([0] * n), ints([0] * n), page_size=16, max_new=1)
+        free, count, left = ints(np.arange(n)), ints([n]), ints([0])
+        ctx, new = ints([0] * n), ints([1] * n)
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        try:
+            for _ in range(4000):
+                b.build(ctx, new, free, count, left, stream=stream)
+        except mk.MkError as e:
+            errors.append(e)
+        stream.synchronize()
+        if not torch.equal(b.slots.cpu(), 16 * torch.arange(n - 1, -1, -1, dtype=torch.int32)) or left.item() != 0:
+            errors.append(n)
+
+    errors = []
+    threads = [threading.Thread(target=step, args=(n, errors)) for n in (4096, 4088, 4080)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors

@@ -631,10 +631,13 @@ extern "C" int mk_paged_tables(const mk_paged_batch* b, const int32_t* ctx_lens,
   p.n = b->n; p.max_blocks = b->max_blocks; p.max_tokens = b->max_tokens;
   p.free_cap = free_capacity; p.page_shift = log2_page(b->page_size);
   const size_t smem = PtSmem::bytes(b->n);
-  if (smem > 49152 && cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return MK_ERR_CUDA;
+  if (smem > 49152) {  // the limit is the process's: set once, to the most a call takes
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+      e = paged_prepare((const void*)paged_tables_kernel, (int)PtSmem::bytes(MK_PAGED_MAX_REQUESTS), 0, dev, &ready);
+    if (e != cudaSuccess) return done(e);
   }
   const int grid = min(152, max(1, (b->max_tokens + 2 * PT_THREADS - 1) / (2 * PT_THREADS)));
   return done(paged_launch(paged_tables_kernel, grid, PT_THREADS, (int)smem, (cudaStream_t)stream, p));
