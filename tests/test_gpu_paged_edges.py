@@ -251,3 +251,38 @@ def test_tables_of_many_requests_from_two_threads():
     for th in threads:
         th.join()
     assert not errors
+
+
+def test_a_batch_that_calls_share():
+    """A call that comes between another's arguments and its launch (a second
+    thread's, where the first has given up the interpreter) leaves what that one
+    says of the batch as it was."""
+    s = paged.make_attention([40, 20, 30], [1, 2, 1], 4, 2, 64, 16, torch.bfloat16, seed=2, garbage=0.0)
+    n, rows = 3, 4
+    table = ints(s["table"])
+    batch = mk.PagedBatch(table, ints(s["cu"]), ints(s["kv"]), ints([0] * rows), ints([0] * rows), page_size=16, max_new=2)
+    cache, out = mk.PagedCache(s["k"], s["v"], n_q_heads=4), torch.zeros_like(s["q"])
+    cache.attention(s["q"], batch, out)
+    want = out.clone()
+
+    def between(name, owner, call, inner):
+        real = getattr(owner, name)
+
+        def spy(*args):
+            setattr(owner, name, real)
+            inner()
+            return real(*args)
+        setattr(owner, name, spy)
+        call()
+        assert getattr(owner, name) is real
+
+    status, left = ints([0]), ints([0])
+    between("_build", batch, lambda: batch.build(ints([40, 20, 30]), ints([1, 2, 1]), ints(np.arange(5)), ints([5]), left, status=status),
+            lambda: cache.attention(s["q"][:1], batch, out[:1]))
+    assert status.item() == 0 and batch.cu_new.tolist() == s["cu"].tolist() and batch.kv_lens.tolist() == s["kv"].tolist()
+    assert cache.status() == mk.MK_ERR_BOUNDS        # of the inner call: rows past the first
+    cache.reset()
+    out.zero_()
+    small = torch.zeros_like(out[:1])
+    between("_attention", cache, lambda: cache.attention(s["q"], batch, out), lambda: cache.attention(s["q"][:1], batch, small))
+    assert torch.equal(out, want) and torch.equal(small, want[:1])

@@ -453,6 +453,9 @@ class PagedBatch(_OnDevice):
     block_table [n, max_blocks], cu_new [n + 1], kv_lens [n], and for build()
     and append positions and slots [max_tokens].  Holds references to them."""
 
+    # Calls pass the structs by address without the interpreter's lock: one that a
+    # call has is never written again, so that threads may share a batch.
+
     def __init__(self, block_table, cu_new, kv_lens, positions=None, slots=None, *, page_size: int,
                  max_new: int):
         lib()
@@ -473,6 +476,15 @@ class PagedBatch(_OnDevice):
                                 None if slots is None else _ptr(slots), n, block_table.shape[1],
                                 self.max_tokens, self.max_new, page_size)
         self._p, self._build = ctypes.addressof(self.c), lib().mk_paged_tables
+        self._rows = (self.max_tokens, self.c, self._p)
+
+    def _of_rows(self, rows: int):
+        """(rows, struct with max_tokens = rows, its address) for attention; the
+        last one asked for is kept."""
+        c = mk_paged_batch.from_buffer_copy(self.c)
+        c.max_tokens = rows
+        self._rows = kept = (rows, c, ctypes.addressof(c))
+        return kept
 
     def build(self, ctx_lens, new_lens, free_pages, n_free, n_left, status=None, stream=None) -> None:
         """mk_paged_tables: fill the tables from device int32 lengths [n], taking
@@ -493,8 +505,6 @@ class PagedBatch(_OnDevice):
             _tensors(self.device, ctx_lens=(ctx_lens, i32, (n,)), new_lens=(new_lens, i32, (n,)),
                      free_pages=(free_pages, i32, None), n_free=(n_free, i32, (1,)),
                      n_left=(n_left, i32, (1,)), status=(status, i32, (1,)))
-        if self.c.max_tokens != self.max_tokens:
-            self.c.max_tokens = self.max_tokens
         args = (self._p, ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
                 free_pages.numel(), n_free.data_ptr(), n_left.data_ptr(),
                 None if status is None else status.data_ptr(),
@@ -623,8 +633,10 @@ class PagedCache(_OnDevice):
             _need(batch._dev == dev, "batch: on the cache's device")
         if n == 0:
             return
-        batch.c.max_tokens = n
-        args = (self._p, batch._p, q.data_ptr(), qs[0] if n > 1 else hq * d, out.data_ptr(),
+        rows = batch._rows  # held here until the call returns
+        if rows[0] != n:
+            rows = batch._of_rows(n)
+        args = (self._p, rows[2], q.data_ptr(), qs[0] if n > 1 else hq * d, out.data_ptr(),
                 os[0] if n > 1 else hq * d, None if lse is None else lse.data_ptr(), scale, window,
                 self._raw_stream(dev) if stream is None else int(stream.cuda_stream))
         if self._current is None or self._current() == dev:
