@@ -286,3 +286,27 @@ def test_a_batch_that_calls_share():
     small = torch.zeros_like(out[:1])
     between("_attention", cache, lambda: cache.attention(s["q"], batch, out), lambda: cache.attention(s["q"][:1], batch, small))
     assert torch.equal(out, want) and torch.equal(small, want[:1])
+
+
+def test_max_new_of_a_batch_can_be_set(workspace):
+    """A decode step on a batch that was made for chunks."""
+    s = paged.make_attention([300, 20, 900], [1, 1, 1], 8, 2, 128, 16, torch.bfloat16, seed=6)
+    want, _ = paged.check_attention(s, workspace=workspace, max_new=1)
+    batch = mk.PagedBatch(ints(s["table"]), ints(s["cu"]), ints(s["kv"]), page_size=16, max_new=512)
+    cache, out = mk.PagedCache(s["k"], s["v"], n_q_heads=8, workspace=workspace), torch.zeros_like(s["q"])
+    batch.max_new = 1
+    cache.attention(s["q"], batch, out)
+    assert batch.max_new == 1 and torch.equal(out, want) and cache.status() == 0
+    two = paged.make_attention([300], [2], 8, 2, 128, 16, torch.bfloat16, seed=6)
+    b2 = mk.PagedBatch(ints(two["table"]), ints(two["cu"]), ints(two["kv"]), page_size=16, max_new=2)
+    c2, o2 = mk.PagedCache(two["k"], two["v"], n_q_heads=8, workspace=workspace), torch.full_like(two["q"], 5.0)
+    b2.max_new = 1
+    c2.attention(two["q"], b2, o2)                   # more than the bound: left as they were, latched
+    assert c2.status() == mk.MK_ERR_BOUNDS and (o2 == 5).all()
+    c2.reset()
+    b2.max_new = 2
+    c2.attention(two["q"], b2, o2)
+    assert c2.status() == 0 and not (o2 == 5).any()
+    b2.max_new = 0
+    with pytest.raises(mk.MkError):
+        c2.attention(two["q"], b2, o2)

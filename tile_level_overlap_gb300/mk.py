@@ -451,7 +451,9 @@ class Rope:
 class PagedBatch(_OnDevice):
     """The tables of a step (mk_paged_batch) over torch int32 CUDA tensors:
     block_table [n, max_blocks], cu_new [n + 1], kv_lens [n], and for build()
-    and append positions and slots [max_tokens].  Holds references to them."""
+    and append positions and slots [max_tokens].  Holds references to them.
+    `max_new`, the most new tokens of a request that attention expects (it selects
+    the kernels: 1 for a decode step), may be set from step to step."""
 
     # Calls pass the structs by address without the interpreter's lock: one that a
     # call has is never written again, so that threads may share a batch.
@@ -469,20 +471,29 @@ class PagedBatch(_OnDevice):
                  slots=(slots, self._i32, rows), positions=(positions, self._i32, rows))
         self.block_table, self.cu_new, self.kv_lens = block_table, cu_new, kv_lens
         self.positions, self.slots = positions, slots
-        self.n, self.page_size, self.max_new = n, page_size, int(max_new)
+        self.n, self.page_size, self._max_new = n, page_size, int(max_new)
         self.max_tokens = 0 if slots is None else slots.numel()
         self.c = mk_paged_batch(_ptr(block_table), _ptr(cu_new), _ptr(kv_lens),
                                 None if slots is None else _ptr(positions),
                                 None if slots is None else _ptr(slots), n, block_table.shape[1],
-                                self.max_tokens, self.max_new, page_size)
+                                self.max_tokens, self._max_new, page_size)
         self._p, self._build = ctypes.addressof(self.c), lib().mk_paged_tables
         self._rows = (self.max_tokens, self.c, self._p)
+
+    @property
+    def max_new(self) -> int:
+        return self._max_new
+
+    @max_new.setter
+    def max_new(self, value: int) -> None:
+        self._max_new = int(value)
+        self._of_rows(self._rows[0])
 
     def _of_rows(self, rows: int):
         """(rows, struct with max_tokens = rows, its address) for attention; the
         last one asked for is kept."""
         c = mk_paged_batch.from_buffer_copy(self.c)
-        c.max_tokens = rows
+        c.max_tokens, c.max_new = rows, self._max_new
         self._rows = kept = (rows, c, ctypes.addressof(c))
         return kept
 
