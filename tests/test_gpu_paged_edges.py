@@ -310,3 +310,63 @@ def test_max_new_of_a_batch_can_be_set(workspace):
     b2.max_new = 0
     with pytest.raises(mk.MkError):
         c2.attention(two["q"], b2, o2)
+
+
+# ---------------------------------------------------------------- streams
+
+@pytest.mark.parametrize("given", ["stream", "current"])
+def test_a_cache_dropped_while_another_stream_runs(given):
+    """The workspace and the status word belong to the stream that the cache was
+    made and first called on; a call still waits on another when the cache goes.
+    Neither is handed out before it has run."""
+    s = paged.make_attention([40, 900], [1, 3], 4, 2, 64, 16, torch.bfloat16, seed=4, garbage=0.0)
+    batch = mk.PagedBatch(ints(s["table"]), ints(s["cu"]), ints(s["kv"]), page_size=16, max_new=3)
+    want, out = torch.empty_like(s["q"]), torch.zeros_like(s["q"])
+    k, v = s["k"].clone(), s["v"].clone()
+    g = torch.Generator().manual_seed(9)
+    kn, vn = (torch.randn(4, 2, 64, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    slots = ints([-1, -1, -1, int(s["table"][0, 0]) * 16])
+    cache = mk.PagedCache(k, v, 4)
+    cache.append(s["q"], kn, vn, slots)
+    cache.attention(s["q"], batch, want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    small, status = cache.workspace.data_ptr(), cache._status.data_ptr()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(600_000_000)                # a few tenths of a second
+        if given == "current":
+            cache.append(s["q"], kn, vn, slots)
+            cache.attention(s["q"], batch, out)
+    if given == "stream":
+        cache.append(s["q"], kn, vn, slots, stream=side)
+        cache.attention(s["q"], batch, out, stream=side)
+    del cache
+    took = [torch.empty(mk.MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    words = [torch.empty(1, dtype=torch.int32, device=DEV) for _ in range(64)]
+    assert not side.query()
+    assert small not in [t.data_ptr() for t in took] and status not in [t.data_ptr() for t in words]
+    side.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_a_workspace_made_after_other_streams_were_seen():
+    # append alone on one stream, then attention on a second, then on the first
+    s = paged.make_attention([40], [1], 4, 2, 64, 16, torch.bfloat16, seed=4, garbage=0.0)
+    batch = mk.PagedBatch(ints(s["table"]), ints(s["cu"]), ints(s["kv"]), page_size=16, max_new=1)
+    kn = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    first, second = torch.cuda.Stream(), torch.cuda.Stream()
+    out, slots = torch.zeros_like(s["q"]), ints([-1])
+    cache = mk.PagedCache(s["k"], s["v"], 4)
+    torch.cuda.synchronize()
+    cache.append(s["q"], kn, kn, slots, stream=first)
+    cache.attention(s["q"], batch, out, stream=second)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(first):
+        torch.cuda._sleep(600_000_000)
+    cache.attention(s["q"], batch, out, stream=first)
+    at = cache.workspace.data_ptr()
+    del cache
+    with torch.cuda.stream(second):
+        again = torch.empty(mk.MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=DEV)
+    assert not first.query() and again.data_ptr() != at
+    torch.cuda.synchronize()

@@ -536,7 +536,11 @@ class PagedCache(_OnDevice):
     overlap; without one the first attention call allocates it.  Holds
     references to the tensors.  The status word is cleared on the stream that is
     current when the cache is made (outside of a capture); calls on other streams
-    are ordered behind that by the caller, as behind one another."""
+    are ordered behind that by the caller, as behind one another.  A cache may be
+    dropped while its calls run on any stream (its own memory, the status word and
+    a workspace that it allocated, is then given back behind them); k, v and a given
+    workspace are the caller's, and a captured graph needs the cache as long as it
+    is replayed."""
 
     def __init__(self, k, v, n_q_heads: int, workspace=None):
         import torch
@@ -550,7 +554,7 @@ class PagedCache(_OnDevice):
         self.k, self.v, self.dtype = k, v, k.dtype
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size = n_q_heads, hkv, d, page
         self._status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self.workspace = None
+        self.workspace, self._given, self._seen = None, workspace is not None, set()
         s = k.stride()
         self.c = mk_paged_cache(_ptr(k), _ptr(v), None, _ptr(self._status), s[0], s[1], s[2],
                                 n_q_heads, hkv, d, page, n_pages,
@@ -562,6 +566,18 @@ class PagedCache(_OnDevice):
                   workspace.numel() * workspace.element_size() >= MK_PAGED_WORKSPACE_BYTES,
                   "workspace: MK_PAGED_WORKSPACE_BYTES on the cache's device")
             self._set_workspace(workspace)
+
+    def _first_on(self, stream, raw: int) -> None:
+        """The first call on a stream: the cache's own memory is used there."""
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(raw, self.device)
+        self._status.record_stream(stream)
+        if self.workspace is not None and not self._given:
+            self.workspace.record_stream(stream)
+        self._seen.add(raw)
 
     def _set_workspace(self, t) -> None:
         self.workspace = t
@@ -608,10 +624,12 @@ class PagedCache(_OnDevice):
             return
         if n == 1:  # the stride of a lone token joins nothing and may be any number
             qs, ks, vs, os = (hq * d,), (hkv * d,), (hkv * d,), (hq * d,)
+        raw = self._raw_stream(dev) if stream is None else int(stream.cuda_stream)
+        if raw not in self._seen:
+            self._first_on(stream, raw)
         args = (self._p, q.data_ptr(), qs[0], k.data_ptr(), ks[0], v.data_ptr(), vs[0], q_out.data_ptr(), os[0],
                 None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
-                eps, rp, pos, pos_stride, slots.data_ptr(), n,
-                self._raw_stream(dev) if stream is None else int(stream.cuda_stream))
+                eps, rp, pos, pos_stride, slots.data_ptr(), n, raw)
         if self._current is None or self._current() == dev:
             rc = self._append(*args)
         else:
@@ -631,6 +649,7 @@ class PagedCache(_OnDevice):
                 _need(not torch.cuda.is_current_stream_capturing(),
                       "workspace: give one, or call once before the capture (it would belong to the graph)")
                 self._set_workspace(torch.empty(MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device))
+            self._seen.clear()  # streams that have seen the status word alone
         hq, d, dev, typ = self.n_q_heads, self.head_dim, self._dev, self.dtype
         n = q.shape[0]
         wide, qs, os = (n, hq, d), q.stride(), out.stride()
@@ -647,9 +666,11 @@ class PagedCache(_OnDevice):
         rows = batch._rows  # held here until the call returns
         if rows[0] != n:
             rows = batch._of_rows(n)
+        raw = self._raw_stream(dev) if stream is None else int(stream.cuda_stream)
+        if raw not in self._seen:
+            self._first_on(stream, raw)
         args = (self._p, rows[2], q.data_ptr(), qs[0] if n > 1 else hq * d, out.data_ptr(),
-                os[0] if n > 1 else hq * d, None if lse is None else lse.data_ptr(), scale, window,
-                self._raw_stream(dev) if stream is None else int(stream.cuda_stream))
+                os[0] if n > 1 else hq * d, None if lse is None else lse.data_ptr(), scale, window, raw)
         if self._current is None or self._current() == dev:
             rc = self._attention(*args)
         else:
