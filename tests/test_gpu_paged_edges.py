@@ -370,3 +370,46 @@ def test_a_workspace_made_after_other_streams_were_seen():
         again = torch.empty(mk.MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=DEV)
     assert not first.query() and again.data_ptr() != at
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d,typ", [(128, "bf16"), (64, "fp16")])
+def test_steps_end_to_end_without_waiting(d, typ, workspace):
+    """Steps of tables, append and attention (decode rows and chunks, lengths that
+    change from step to step in the same arrays) launched behind one another, every
+    launch starting before its predecessor has ended: the same bits as with a wait
+    after every call."""
+    typ, hq, hkv, page, n, steps, width, pool = TYPES[typ], 8, 2, 16, 6, 24, 40, 240
+    rng = np.random.default_rng(d)
+    plan = [[int(x) for x in rng.choice([0, 1, 1, 1, 2, 9, 17], n)] for _ in range(steps)]
+    plan[0], plan[5][1], plan[11][4] = [70, 1, 33, 0, 150, 5], 120, 64
+    rows = max(sum(p) for p in plan) + 2
+    g = torch.Generator().manual_seed(d)
+    qkv = torch.randn(steps, rows, hq + 2 * hkv, d, generator=g).to(typ).to(DEV)
+    lens = [ints(np.sum(plan[:i], 0) if i else [0] * n) for i in range(steps)]
+    adds = [ints(p) for p in plan]
+    rope, order = mk.Rope(d), rng.permutation(pool)
+
+    def run(wait):
+        kc, vc = (torch.zeros(pool, hkv, page, d, dtype=typ, device=DEV) for _ in range(2))
+        cache = mk.PagedCache(kc, vc, n_q_heads=hq, workspace=workspace)
+        batch = mk.PagedBatch(ints(np.full((n, width), -1)), ints([0] * (n + 1)), ints([0] * n), ints([0] * rows), ints([0] * rows), page_size=page, max_new=150)
+        free, counts = ints(order), [ints([pool])] + [ints([0]) for _ in range(steps)]
+        q = qkv[:, :, :hq].clone()
+        outs = torch.zeros(steps, rows, hq, d, dtype=typ, device=DEV)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            batch.build(lens[i], adds[i], free, counts[i], counts[i + 1], status=cache._status)
+            if wait:
+                torch.cuda.synchronize()
+            cache.append(q[i], qkv[i, :, hq:hq + hkv], qkv[i, :, hq + hkv:], batch.slots, batch.positions, rope)
+            if wait:
+                torch.cuda.synchronize()
+            cache.attention(q[i], batch, outs[i])
+            if wait:
+                torch.cuda.synchronize()
+        assert cache.status() == 0
+        return outs, kc, vc, counts[-1]
+
+    want = run(True)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))

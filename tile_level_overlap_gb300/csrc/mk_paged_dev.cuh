@@ -63,10 +63,11 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 // ---------------------------------------------------------------- dependent launches
 // Every kernel here is launched as a programmatic dependent of what precedes it
-// in the stream: it may be set up while that one's last blocks run, and touches
-// global memory only after grid_wait_prior() has seen it complete.  (The tile
-// kernel waits only at its end where the few-row kernel comes before it: that one
-// lets it go after its own wait.)
+// in the stream: it may be set up while that one's last blocks run, and uses
+// global memory only after grid_wait_prior() has seen it complete.  (The join reads
+// the workspace once before, to fetch its own code, and drops what it read.)  A
+// kernel that starts early has what earlier kernels wrote from its own wait alone,
+// so every one waits before its first read, also where its predecessor has.
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -199,44 +200,48 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, bool flag, int* tmp, 
   return before + x - v;
 }
 
+// Where cu falls: requests that begin below an earlier offset have no units
+// (each thread's `per` consecutive requests; returns what is left of them).  Out
+// of line, so that the kernels' code is as without it.
+template <int W>
+__device__ __noinline__ uint32_t refuse_below(const int32_t* cu, int n, int* pre, int per, int* tmp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r0 = min(tid * per, n), r1 = min(r0 + per, n);
+  int before = -0x7fffffff - 1;  // the largest offset of the requests before
+  for (int r = r0; r < r1; ++r) before = max(before, max(cu[r], cu[r + 1]));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before = max(before, u);
+  }
+  __syncthreads();  // tmp has been read
+  if (lane == 31) tmp[warp] = before;
+  before = __shfl_up_sync(0xffffffffu, before, 1);
+  if (lane == 0) before = -0x7fffffff - 1;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before = max(before, tmp[w]);
+  __syncthreads();
+  uint32_t left = 0;
+  for (int r = r0; r < r1; ++r) {
+    if (cu[r] < before) pre[r] = 0;
+    left += (uint32_t)pre[r];
+    before = max(before, max(cu[r], cu[r + 1]));
+  }
+  return left;
+}
+
 // The units of the requests, pre[r] (each thread's `per` consecutive ones, `mine`
 // of them together), to a request's first unit; returns their number.  `falls`:
-// cu falls at one of the thread's requests.  Where it falls anywhere, requests
-// that begin below an earlier offset are refused first: their rows may be another's,
-// and the units of overlapping requests have no bound (the launch's check counts
-// every row of the step once).
+// cu falls at one of the thread's requests.  Rows below an earlier offset may be
+// another request's, and the units of overlapping requests have no bound (the
+// launch's check counts every row of the step once).
 template <int W>
 __device__ __forceinline__ int place_units(const PagedAttnParams& P, int* pre, int per, uint32_t mine, bool falls, int* tmp) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r0 = min(tid * per, P.n), r1 = min(r0 + per, P.n);
+  const int tid = threadIdx.x, r0 = min(tid * per, P.n), r1 = min(r0 + per, P.n);
   int T;
   bool any;
   uint32_t at = block_scan<W>(mine, falls, tmp, &T, &any);
-  if (any) {
-    int top = -0x7fffffff - 1;  // the largest offset up to this thread's last request
-    for (int r = r0; r < r1; ++r) top = max(top, max(P.cu[r], P.cu[r + 1]));
-    int before = top;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before = max(before, u);
-    }
-    __syncthreads();
-    if (lane == 31) tmp[warp] = before;
-    before = __shfl_up_sync(0xffffffffu, before, 1);
-    if (lane == 0) before = -0x7fffffff - 1;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) before = max(before, tmp[w]);
-    __syncthreads();
-    mine = 0;
-    for (int r = r0; r < r1; ++r) {
-      const int c0 = P.cu[r];
-      if (c0 < before) pre[r] = 0;
-      mine += (uint32_t)pre[r];
-      before = max(before, max(c0, P.cu[r + 1]));
-    }
-    at = block_scan<W>(mine, false, tmp, &T, &any);
-  }
+  if (any) at = block_scan<W>(refuse_below<W>(P.cu, P.n, pre, per, tmp), false, tmp, &T, &any);
   for (int r = r0; r < r1; ++r) {
     const int u = pre[r];
     pre[r] = (int)at;
