@@ -225,6 +225,20 @@ def test_many_requests_with_chunks(n, workspace):
     paged.check_attention(s, window=33, workspace=workspace)
 
 
+def test_bounds_past_32_bits(workspace):
+    # a window past every position is none; its low 32 bits would be a window of 5
+    s = paged.make_attention([300, 20], [2, 40], 8, 2, 64, 16, torch.bfloat16, seed=8, garbage=0.0)
+    want, wlse = paged.check_attention(s, workspace=workspace)
+    for max_new in (2 ** 32 + 1, 2 ** 31, 40):
+        batch = mk.PagedBatch(ints(s["table"]), ints(s["cu"]), ints(s["kv"]), page_size=16, max_new=max_new)
+        cache, out = mk.PagedCache(s["k"], s["v"], n_q_heads=8, workspace=workspace), torch.zeros_like(want)
+        for window in (2 ** 32 + 5, 2 ** 31, 10 ** 12, 2 ** 31 - 1, 0):
+            cache.attention(s["q"], batch, out.zero_(), window=window)
+            assert torch.equal(out, want) and cache.status() == 0
+        batch.max_new = 2 ** 32 + 1
+        assert batch.max_new == 2 ** 31 - 1
+
+
 # ---------------------------------------------------------------- threads
 
 def test_tables_of_many_requests_from_two_threads():

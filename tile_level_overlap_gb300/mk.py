@@ -381,6 +381,11 @@ def _heads(device, dtype, **wanted):
         _need(s[2] == 1 and (shape[1] == 1 or s[1] == shape[2]), f"{name}: heads that lie end to end")
 
 
+def _int32(x) -> int:
+    """A bound as the C calls take it (ctypes would keep its low 32 bits)."""
+    return min(int(x), 0x7fffffff)
+
+
 _torch_parts = None
 
 
@@ -471,7 +476,7 @@ class PagedBatch(_OnDevice):
                  slots=(slots, self._i32, rows), positions=(positions, self._i32, rows))
         self.block_table, self.cu_new, self.kv_lens = block_table, cu_new, kv_lens
         self.positions, self.slots = positions, slots
-        self.n, self.page_size, self._max_new = n, page_size, int(max_new)
+        self.n, self.page_size, self._max_new = n, page_size, _int32(max_new)
         self.max_tokens = 0 if slots is None else slots.numel()
         self.c = mk_paged_batch(_ptr(block_table), _ptr(cu_new), _ptr(kv_lens),
                                 None if slots is None else _ptr(positions),
@@ -486,7 +491,7 @@ class PagedBatch(_OnDevice):
 
     @max_new.setter
     def max_new(self, value: int) -> None:
-        self._max_new = int(value)
+        self._max_new = _int32(value)
         self._of_rows(self._rows[0])
 
     def _of_rows(self, rows: int):
@@ -663,6 +668,8 @@ class PagedCache(_OnDevice):
             _need(batch._dev == dev, "batch: on the cache's device")
         if n == 0:
             return
+        if window > 0x7fffffff:  # past every position; ctypes would keep its low 32 bits
+            window = 0
         rows = batch._rows  # held here until the call returns
         if rows[0] != n:
             rows = batch._of_rows(n)
