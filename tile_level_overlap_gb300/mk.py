@@ -559,7 +559,9 @@ class PagedCache(_OnDevice):
         self.k, self.v, self.dtype = k, v, k.dtype
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size = n_q_heads, hkv, d, page
         self._status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self.workspace, self._given, self._seen = None, workspace is not None, set()
+        # streams on which the status word and an own workspace need no record (any more)
+        self._home = self._raw_stream(self._dev)
+        self.workspace, self._given, self._seen = None, workspace is not None, {self._home}
         s = k.stride()
         self.c = mk_paged_cache(_ptr(k), _ptr(v), None, _ptr(self._status), s[0], s[1], s[2],
                                 n_q_heads, hkv, d, page, n_pages,
@@ -573,7 +575,7 @@ class PagedCache(_OnDevice):
             self._set_workspace(workspace)
 
     def _first_on(self, stream, raw: int) -> None:
-        """The first call on a stream: the cache's own memory is used there."""
+        """The first call on a stream that the cache's own memory is not of."""
         import torch
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
@@ -654,7 +656,9 @@ class PagedCache(_OnDevice):
                 _need(not torch.cuda.is_current_stream_capturing(),
                       "workspace: give one, or call once before the capture (it would belong to the graph)")
                 self._set_workspace(torch.empty(MK_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device))
-            self._seen.clear()  # streams that have seen the status word alone
+            # (streams that have seen the status word alone have to see both)
+            raw = self._raw_stream(self._dev) if stream is None else int(stream.cuda_stream)
+            self._seen = {raw} if raw == self._home else set()
         hq, d, dev, typ = self.n_q_heads, self.head_dim, self._dev, self.dtype
         n = q.shape[0]
         wide, qs, os = (n, hq, d), q.stride(), out.stride()
