@@ -531,8 +531,11 @@ int mk_paged_append(const mk_paged_cache *cache, const void *q, int64_t q_stride
  * taken as absent), a page is not one of the cache's (its keys and values count
  * as zeros), or a request's rows are more than max_new, past max_tokens or out of
  * order (cu_new falls there, or they begin below an earlier offset): such rows are
- * left as they were.  The result of a row depends on the batch only through the
- * order in which partial sums of its keys are joined; equal calls give equal bits. */
+ * left as they were.  Equal calls give equal bits.  In another batch a row's result
+ * may differ by the rounding of its weights (half a step of the cache's type times
+ * the softmax-weighted mean of |v|): max_new selects the kernel and the other
+ * requests where a row's keys are divided among SMs, and both change the maximum
+ * that the weights are rounded against. */
 int mk_paged_attention(const mk_paged_cache *cache, const mk_paged_batch *batch, const void *q,
                        int64_t q_stride, void *out, int64_t out_stride, float *lse, float scale,
                        int window, void *stream);

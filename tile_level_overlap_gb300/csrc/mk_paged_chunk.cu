@@ -7,9 +7,10 @@
 // to end, after the causal bound and the window; each persistent CTA (one per
 // SM) takes an equal run of it, and rows whose keys lie in several runs are
 // joined as in the few-row kernel.  Measured with 32 query heads on 8 kv heads of
-// 128: a prompt of 8192 tokens 363 us (1514 TFLOP/s), of 16384 1403 us (1567), 2 x
-// 512 tokens over 4-12K cached keys 102 us; a block of keys takes 3050 cycles, 2048
-// of them products.
+// 128: a prompt of 8192 tokens 363 us (1514 TFLOP/s; 385 us, 1428, without a pause,
+// when the power limit holds the clock at 1.94 GHz), of 16384 1390 us (1580), 2 x 512
+// tokens over 4-12K cached keys 104 us; a block of keys takes 3050 cycles, 2048 of
+// them products.
 //
 // Warps of a CTA: two load (TMA: queries, K and V blocks page by page, 128-byte
 // swizzle), one for each half issues tcgen05.mma, two groups of four own
@@ -637,8 +638,8 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
   const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF>,
                                       ChunkCfg<HD>::most, PC_REGS, p.device, &ready);
   if (e != cudaSuccess) return e;
-  // without the few-row kernel before it, which waits for what is before both, it
-  // is launched behind that as a whole
+  // behind the few-row kernel it is set up while that one ends; alone it is launched
+  // behind the whole of what precedes (8192-token prompt 363 against 368 us)
   return paged_launch_if(p.few_rows > 0, paged_chunk_kernel<HD, BF>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
                          tq, tk, tv, p, w);
 }

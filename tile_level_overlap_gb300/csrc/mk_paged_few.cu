@@ -10,7 +10,7 @@
 // joins the parts of each pair in the order of their keys.  Measured with 32 query
 // heads on 8 kv heads of 128: 64 rows over 4096 keys in pages of 16 169 us (6.4
 // TB/s), over 16384 627 us (6.9 TB/s); 2 x 4 drafted tokens over 128K keys in pages
-// of 64 165 us (6.45 TB/s); one row over 4096 keys 9.4 us, join included.
+// of 64 165 us (6.45 TB/s); one row over 4096 keys 9.5 us, join included.
 //
 // A warp walks the run: it posts each pair's description and query rows (bulk
 // copies) to a small ring and loads the key blocks (32 KB of keys and values: 64
@@ -23,6 +23,9 @@
 // products, keys and dimensions on the 16-row side and the query rows on the
 // 8-column side, so that 8 rows fill a product that would be half empty the other
 // way round, and the softmax of a row stays in the lanes that rescale its output.
+// The weights are rounded once to the cache's type for the product with V, as in
+// the tile kernel (half a step of the softmax-weighted mean of |v|, about the
+// output's own rounding; their sum keeps 32 bits).
 // The legacy tensor path is ample here (a block costs its four warps 16 products
 // each).  At the end of a pair the eight states are joined in shared memory.
 #include "mk_paged_dev.cuh"
