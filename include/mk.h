@@ -540,6 +540,159 @@ int mk_paged_attention(const mk_paged_cache *cache, const mk_paged_batch *batch,
                        int64_t q_stride, void *out, int64_t out_stride, float *lse, float scale,
                        int window, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens over a paged cache.  A request's new tokens can be a
+ * tree: its token 0 is the root (the last one that stands, whose keys and values
+ * the cache does not hold yet), token i's parent is a token before it.  One step is
+ * mk_paged_tables (the tree's tokens take the slots ctx, ctx + 1, .. in the order
+ * of the rows), mk_paged_tree (masks, positions), per layer mk_paged_append and
+ * mk_paged_tree_attention, then mk_tree_verify (which tokens stand, and the one
+ * that follows), mk_paged_keep (their keys and values move together, all layers in
+ * one launch) and mk_paged_fork in its trimming form (pages behind them go back to
+ * the free list). */
+
+/* New tokens of a request that is a tree, at most. */
+#define MK_TREE_MAX_NODES 1024
+/* Layers of one mk_paged_keep or mk_paged_copy call. */
+#define MK_PAGED_MAX_LAYERS 128
+
+/* Masks and positions of a step's trees.  Row c = cu_new[r] + i of request r:
+ *   bit j % 32 of masks[c][j / 32]: token j is token i or one of its ancestors;
+ *   positions[c] = kv_lens[r] - new tokens + number of its ancestors.
+ * A request of more than 32 mask_words new tokens is a chunk of a prompt: its masks
+ * are left alone, its token i stands at ctx + i.  Rows of no request: positions
+ * 0, masks left alone; rows of a request whose kv_lens is less than its new tokens
+ * (one that mk_paged_tables refused): positions 0, masks as described.
+ *   parents    device int32 [max_tokens]: the parent's index among the request's
+ *              new tokens, -1: a root; not read for chunks
+ *   masks      device uint32 [max_tokens][mask_words], 1 <= mask_words <=
+ *              MK_TREE_MAX_NODES / 32
+ *   positions  device int32 [max_tokens], batch->positions or another
+ * A parent that is not before its child makes the child a root, and MK_ERR_BOUNDS is
+ * latched in *status; so it is for a request whose rows are out of order (cu_new
+ * falls there, or they begin below an earlier offset) or pass max_tokens: they are
+ * left alone.  What is written may overlap nothing else of the call. */
+int mk_paged_tree(const mk_paged_batch *batch, const int32_t *parents, uint32_t *masks, int mask_words,
+                  int32_t *positions, int32_t *status, void *stream);
+
+/* mk_paged_attention for rows that see the cached tokens and the new tokens that
+ * their masks name: row i of a request with ctx = kv_lens - new cached tokens sees
+ * the keys j < ctx and the keys ctx + j, j <= i, with bit j of its mask.  With n set
+ * bits (up to bit i) it stands at p = ctx + max(n, 1) - 1; window > 0: it sees the
+ * cached keys j > p - window and the last `window` of its set bits.  Masks of
+ * chains give what mk_paged_attention gives, up to the rounding of the weights.
+ * Requests of more than 32 mask_words new tokens are causal (chunks of prompts in
+ * the same step); their masks are not read.  Keys count as read by a request from
+ * ctx - window + 1 on.  All else as there. */
+int mk_paged_tree_attention(const mk_paged_cache *cache, const mk_paged_batch *batch,
+                            const uint32_t *masks, int mask_words, const void *q, int64_t q_stride,
+                            void *out, int64_t out_stride, float *lse, float scale, int window,
+                            void *stream);
+
+/* Which drafted tokens stand, so that the emitted ones are distributed as if drawn
+ * one by one from the target's probabilities.  Row c of a request belongs to its
+ * token; target_probs[c] are the target's probabilities of the token after it,
+ * draft_probs[c] those that its children were drawn from, independently of one
+ * another.  From the root on, at the token that stands last, with R = its target row
+ * and Z = 1: its children are asked in the order of their rows; child x with
+ * u = uniforms[x's row] stands when u * draft(x) * Z < R(x); else R becomes
+ * max(R - Z draft, 0) and Z its sum.  Where no child is left the last token is
+ * the least t with R(0) + .. + R(t) > last_uniforms[r] * sum R (with R = the target
+ * row again if that sum is 0).  draft_probs NULL: tokens that were not drawn but
+ * found (looked up, or a draft's best ones): child x stands when u * Z < R(x), else
+ * Z loses R(x) (not below 0) and R(x) becomes 0.  A row of probabilities with a single 1 is greedy.
+ *   target_probs, draft_probs  device float [max_tokens][vocab], *_stride elements
+ *               from row to row (>= vocab); rows sum to 1 up to rounding; values
+ *               that are not positive (and NaN) count as 0, above 1 as 1.  Draft rows
+ *               of tokens without children are not read.
+ *   tokens      device int32 [max_tokens]; the root's is not read
+ *   uniforms    device float [max_tokens], last_uniforms [n], in [0, 1) (values
+ *               outside are taken as 0 or the largest below 1)
+ *   path        int32 [max_tokens]: path[c] = 0 and the indices of the tokens that
+ *               stand, in order, then -1 (mk_paged_keep takes it)
+ *   emitted     int32 [max_tokens]: their tokens without the root's, then the last one,
+ *               then -1
+ *   kept        int32 [n]: tokens that stand, the root included = tokens emitted
+ *   lens        int32 [n]: kv_lens[r] - new tokens + kept[r], the cached tokens of the
+ *               next step
+ * A request without new tokens: kept 0, lens = kv_lens.  One with more than
+ * MK_TREE_MAX_NODES (or whose rows are out of order or past max_tokens) likewise,
+ * its path and emitted left alone and MK_ERR_BOUNDS latched in *status.  Where
+ * kv_lens is less than the new tokens (refused by mk_paged_tables) kept is 0 and
+ * lens kv_lens, path and emitted -1.  A token outside the vocabulary never stands,
+ * a parent that is not before its child has no such child; both are latched.  A
+ * target row without mass where the last token is drawn: the token 0, latched.
+ * Sums are exact to 2^-62 (whole numbers), so that equal calls, and equal requests
+ * in any batch, give equal tokens.  vocab 1 .. 2^24.  What is written may overlap
+ * nothing else of the call; *status may be the cache's. */
+int mk_tree_verify(const mk_paged_batch *batch, const int32_t *parents, const int32_t *tokens,
+                   const float *target_probs, int64_t target_stride, const float *draft_probs,
+                   int64_t draft_stride, int vocab, const float *uniforms, const float *last_uniforms,
+                   int32_t *path, int32_t *emitted, int32_t *kept, int32_t *lens, int32_t *status,
+                   void *stream);
+
+/* ------------------------------------------------------------------------
+ * Sharing and giving back pages.  shared[p] is how many holders page p has beside
+ * the first: 0 for pages that mk_paged_tables hands out and for free ones, so that
+ * it needs no part of this.  A page that more than one request holds is never
+ * written: the page that a request's next token goes to is its own. */
+
+/* Requests as continuations of others, with the pages' holders and the free list
+ * kept up to date.  Old request s holds ceil(lens[s] / page_size) pages by its row
+ * of `table`; it is cut to keep[s] tokens (NULL: lens[s]) and continued by every
+ * new request i with parents[i] == s (none: it ends; parents[i] == -1: request i
+ * begins empty).  Request i holds the whole pages of what it continues together with
+ * the others; a page that is filled in part goes over to the first child, if
+ * nobody else held it, and every other child takes a page from the end of the free
+ * list, in the order of the requests, that the caller has to fill (mk_paged_copy of
+ * `copies`).  Pages that nobody holds any more are added behind the free pages that
+ * are left, in the order of the requests and blocks that let them go (at the first
+ * place of several).
+ *   parents == NULL: in place: m == n, next_table == table, every request continues
+ *     itself.  This trims requests, keep[s] = 0 frees them.  A cut that ends inside a
+ *     page that others hold takes a page of its own as above.
+ *   table        device int32 [n][max_blocks], next_table [m][max_blocks] (entries
+ *                behind the held ones are left alone)
+ *   lens, keep   device int32 [n], next_lens [m]: the tokens that request i holds
+ *   copies       device int32 [3][m]: page to copy from (-1: none), page to copy to,
+ *                tokens; NULL: none are taken (as if there were no free pages)
+ *   shared       device int32 [n_pages]
+ *   free_pages   device int32 [free_capacity], *n_free in use; *n_left receives the
+ *                new number and may be *n_free itself
+ * A request that needs a free page when none is left keeps its whole pages only
+ * (next_lens says so).  It, lengths outside 0 .. max_blocks * page_size, keep outside
+ * 0 .. lens, parents outside -1 .. n - 1 (taken as -1), held pages that are not
+ * 0 .. n_pages - 1 where holders change (they are passed on, nothing is counted), pages let go more often
+ * than they were held and a free list that overflows (what does not fit is dropped)
+ * latch MK_ERR_BOUNDS in *status.  n, m <= MK_PAGED_MAX_REQUESTS.  Other arrays may
+ * not overlap, but that lens, keep and parents may be the same ones. */
+int mk_paged_fork(const int32_t *table, int n, const int32_t *lens, const int32_t *keep,
+                  const int32_t *parents, int32_t *next_table, int32_t *next_lens, int m, int max_blocks,
+                  int page_size, int32_t *copies, int32_t *shared, int n_pages, int32_t *free_pages,
+                  int free_capacity, const int32_t *n_free, int32_t *n_left, int32_t *status,
+                  void *stream);
+
+/* Copy the first copies[2][i] tokens of page copies[0][i] to page copies[1][i], keys
+ * and values of all kv heads, in n_layers caches of the same shape: `cache` with k
+ * and v replaced by ks[l], vs[l] (host arrays, read during the call).  A pair with a
+ * source of -1 is none.  Pages that are not the cache's and more tokens than a page
+ * has are latched in cache->status (the pair is left out, the tokens clamped).  No
+ * page may be the target of two pairs or the target of one and the source of
+ * another.  n_copies >= 0 (MK_PAGED_MAX_REQUESTS at most). */
+int mk_paged_copy(const mk_paged_cache *cache, void *const *ks, void *const *vs, int n_layers,
+                  const int32_t *copies, int n_copies, void *stream);
+
+/* The accepted paths' keys and values move together: for every request r, with
+ * c = cu_new[r], the token in slots[c + path[c + j]] moves to slots[c + j], j = 0, 1,
+ * .. until path is -1 or the request's rows end; keys and values of all kv heads of
+ * n_layers caches as above.  Paths are increasing (a request's stops at the first
+ * entry that is not, or is no index of its tokens, and MK_ERR_BOUNDS is latched in
+ * cache->status; so it is for a slot past the last page, whose token is left out, as
+ * is one of slot -1; a request whose rows are out of order or pass max_tokens is left
+ * alone).  batch->slots is read, batch->max_tokens = rows of path. */
+int mk_paged_keep(const mk_paged_cache *cache, void *const *ks, void *const *vs, int n_layers,
+                  const mk_paged_batch *batch, const int32_t *path, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,3 +17,4 @@ from .model import (  # noqa: F401
     causal_gqa_attention,
 )
 from .paged import paged_tables, rope_rows, paged_attention  # noqa: F401
+from .tree import ancestors, paged_fork, paged_tree, tree_attention, tree_seen, tree_verify  # noqa: F401

@@ -536,17 +536,16 @@ cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool 
   return e;
 }
 
-// ---------------------------------------------------------------- argument checks
-bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+}  // namespace
 
-int log2_page(int page) {
+// ---------------------------------------------------------------- argument checks
+int paged_log2(int page) {
   for (int s = 4; s <= 8; ++s)
     if (page == 1 << s) return s;
   return -1;
 }
 
-int check_cache(const mk_paged_cache* c) {
+int paged_check_cache(const mk_paged_cache* c) {
   if (!c || !c->k || !c->v || !al16(c->k) || !al16(c->v) || !al4(c->status)) return MK_ERR_INVALID_ARG;
   if (c->n_q_heads < 1 || c->n_kv_heads < 1 || c->n_pages < 1) return MK_ERR_INVALID_ARG;
   if (c->dtype != MK_BF16 && c->dtype != MK_FP16) return MK_ERR_INVALID_ARG;
@@ -559,30 +558,37 @@ int check_cache(const mk_paged_cache* c) {
   if (c->head_dim != 64 && c->head_dim != 128) return MK_ERR_UNSUPPORTED;
   // a token's heads are counted in bytes in 32 bits
   if (c->n_q_heads > MK_PAGED_MAX_HEADS || c->n_kv_heads > MK_PAGED_MAX_HEADS) return MK_ERR_UNSUPPORTED;
-  if (log2_page(c->page_size) < 0) return MK_ERR_UNSUPPORTED;
+  if (paged_log2(c->page_size) < 0) return MK_ERR_UNSUPPORTED;
   if ((int64_t)c->n_pages * c->page_size > 0x7fffffffll) return MK_ERR_UNSUPPORTED;
   return MK_OK;
 }
 
 // The code of a call whose launches said `e` (a failed one leaves nothing behind
 // for the next CUDA call to report).
-int done(cudaError_t e) {
+int paged_done(cudaError_t e) {
   if (e == cudaSuccess) return MK_OK;
   cudaGetLastError();
   return MK_ERR_CUDA;
 }
 
-int check_batch(const mk_paged_batch* b) {
+int paged_check_batch(const mk_paged_batch* b) {
   if (!b || !b->block_table || !b->cu_new || !b->kv_lens) return MK_ERR_INVALID_ARG;
   if (!al4(b->block_table) || !al4(b->cu_new) || !al4(b->kv_lens)) return MK_ERR_INVALID_ARG;
   if (b->n < 1 || b->max_blocks < 1 || b->max_tokens < 0) return MK_ERR_INVALID_ARG;
-  if (b->n > MK_PAGED_MAX_REQUESTS || log2_page(b->page_size) < 0) return MK_ERR_UNSUPPORTED;
+  if (b->n > MK_PAGED_MAX_REQUESTS || paged_log2(b->page_size) < 0) return MK_ERR_UNSUPPORTED;
   if ((int64_t)b->n * b->max_blocks > 0x7fffffffll || (int64_t)b->max_blocks * b->page_size > (1ll << 30))
     return MK_ERR_UNSUPPORTED;
   return MK_OK;
 }
 
-}  // namespace
+bool paged_overlap(const PagedWords* a, int n, int written) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (a[i].words > 0 && a[j].words > 0 && (uintptr_t)a[i].at < (uintptr_t)a[j].at + 4 * a[j].words &&
+          (uintptr_t)a[j].at < (uintptr_t)a[i].at + 4 * a[i].words)
+        return true;
+  return false;
+}
 
 cudaError_t paged_prepare(const void* kernel, int smem, int regs, int device, std::atomic<uint64_t>* done) {
   const uint64_t bit = 1ull << (device & 63);
@@ -603,7 +609,7 @@ extern "C" int mk_paged_tables(const mk_paged_batch* b, const int32_t* ctx_lens,
                                const int32_t* new_lens, const int32_t* free_pages,
                                int free_capacity, const int32_t* n_free, int32_t* n_left,
                                int32_t* status, void* stream) {
-  const int rc = check_batch(b);
+  const int rc = paged_check_batch(b);
   if (rc != MK_OK) return rc;
   if (!ctx_lens || !new_lens || !n_free || !n_left || free_capacity < 0 ||
       (free_capacity > 0 && !free_pages) || (b->max_tokens > 0 && (!b->positions || !b->slots)))
@@ -613,23 +619,17 @@ extern "C" int mk_paged_tables(const mk_paged_batch* b, const int32_t* ctx_lens,
     if (!al4(p)) return MK_ERR_INVALID_ARG;
   // A block may still read the lengths when another has written its part: what
   // is written shares no word with anything else of the call.
-  const struct { const int32_t* at; int64_t words; } arrays[] = {
+  const PagedWords arrays[] = {
       {b->block_table, (int64_t)b->n * b->max_blocks}, {b->cu_new, b->n + 1}, {b->kv_lens, b->n},
       {b->positions, b->max_tokens}, {b->slots, b->max_tokens}, {n_left, 1}, {status, status ? 1 : 0},
       {ctx_lens, b->n}, {new_lens, b->n}, {free_pages, free_capacity}, {n_free, 1}};
-  constexpr int n_arrays = sizeof(arrays) / sizeof(arrays[0]), n_written = 7;
-  for (int i = 0; i < n_written; ++i)
-    for (int j = i + 1; j < n_arrays; ++j)
-      if (arrays[i].words > 0 && arrays[j].words > 0 &&
-          (uintptr_t)arrays[i].at < (uintptr_t)arrays[j].at + 4 * arrays[j].words &&
-          (uintptr_t)arrays[j].at < (uintptr_t)arrays[i].at + 4 * arrays[i].words)
-        return MK_ERR_INVALID_ARG;
+  if (paged_overlap(arrays, 11, 7)) return MK_ERR_INVALID_ARG;
   PagedTablesParams p{};
   p.ctx = ctx_lens; p.add = new_lens; p.free_pages = free_pages; p.n_free = n_free;
   p.table = b->block_table; p.cu = b->cu_new; p.kv = b->kv_lens; p.pos = b->positions;
   p.slot = b->slots; p.n_left = n_left; p.status = status;
   p.n = b->n; p.max_blocks = b->max_blocks; p.max_tokens = b->max_tokens;
-  p.free_cap = free_capacity; p.page_shift = log2_page(b->page_size);
+  p.free_cap = free_capacity; p.page_shift = paged_log2(b->page_size);
   const size_t smem = PtSmem::bytes(b->n);
   if (smem > 49152) {  // the limit is the process's: set once, to the most a call takes
     static std::atomic<uint64_t> ready{0};
@@ -637,10 +637,10 @@ extern "C" int mk_paged_tables(const mk_paged_batch* b, const int32_t* ctx_lens,
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
       e = paged_prepare((const void*)paged_tables_kernel, (int)PtSmem::bytes(MK_PAGED_MAX_REQUESTS), 0, dev, &ready);
-    if (e != cudaSuccess) return done(e);
+    if (e != cudaSuccess) return paged_done(e);
   }
   const int grid = min(152, max(1, (b->max_tokens + 2 * PT_THREADS - 1) / (2 * PT_THREADS)));
-  return done(paged_launch(paged_tables_kernel, grid, PT_THREADS, (int)smem, (cudaStream_t)stream, p));
+  return paged_done(paged_launch(paged_tables_kernel, grid, PT_THREADS, (int)smem, (cudaStream_t)stream, p));
 }
 
 extern "C" int mk_rope_init(mk_rope* rope, int rotary_dim, double theta, const double* inv_freq,
@@ -669,7 +669,7 @@ extern "C" int mk_paged_append(const mk_paged_cache* c, const void* q, int64_t q
                                int64_t q_out_stride, const void* q_norm, const void* k_norm, float eps,
                                const mk_rope* rope, const int32_t* positions, int64_t pos_stride,
                                const int32_t* slots, int n_tokens, void* stream) {
-  const int rc = check_cache(c);
+  const int rc = paged_check_cache(c);
   if (rc != MK_OK) return rc;
   if (n_tokens < 0 || !q || !k || !v || !q_out || !slots || !al4(slots)) return MK_ERR_INVALID_ARG;
   const void* ptrs[] = {q, k, v, q_out, q_norm, k_norm};
@@ -697,7 +697,7 @@ extern "C" int mk_paged_append(const mk_paged_cache* c, const void* q, int64_t q
   p.pos_stride = pos_stride; p.page_stride = c->page_stride; p.head_stride = c->head_stride;
   p.token_stride = c->token_stride;
   p.hq = c->n_q_heads; p.hkv = c->n_kv_heads; p.n_tokens = n_tokens;
-  p.n_slots = c->n_pages * c->page_size; p.page_shift = log2_page(c->page_size);
+  p.n_slots = c->n_pages * c->page_size; p.page_shift = paged_log2(c->page_size);
   p.eps = eps;
   if (rope) p.rope = *rope;
   cudaStream_t st = (cudaStream_t)stream;
@@ -709,15 +709,15 @@ extern "C" int mk_paged_append(const mk_paged_cache* c, const void* q, int64_t q
     else
       e = c->head_dim == 128 ? append_launch<128, false>(p, dev, sms, st) : append_launch<64, false>(p, dev, sms, st);
   }
-  return done(e);
+  return paged_done(e);
 }
 
-extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch* b, const void* q,
-                                  int64_t q_stride, void* out, int64_t out_stride, float* lse,
-                                  float scale, int window, void* stream) {
-  int rc = check_cache(c);
+static int attend(const mk_paged_cache* c, const mk_paged_batch* b, const uint32_t* masks, int mask_words,
+                  const void* q, int64_t q_stride, void* out, int64_t out_stride, float* lse, float scale,
+                  int window, void* stream) {
+  int rc = paged_check_cache(c);
   if (rc != MK_OK) return rc;
-  rc = check_batch(b);
+  rc = paged_check_batch(b);
   if (rc != MK_OK) return rc;
   if (!q || !out || q == out || !al16(q) || !al16(out) || !al4(lse) || !c->workspace ||
       !al16(c->workspace))
@@ -734,9 +734,11 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch*
   p.table = b->block_table; p.cu = b->cu_new; p.kv = b->kv_lens; p.status = c->status;
   p.q_stride = q_stride; p.o_stride = out_stride;
   p.n = b->n; p.max_blocks = b->max_blocks; p.rows = b->max_tokens; p.max_new = b->max_new;
-  p.n_pages = c->n_pages; p.page_shift = log2_page(c->page_size);
+  p.n_pages = c->n_pages; p.page_shift = paged_log2(c->page_size);
   p.hkv = c->n_kv_heads; p.rep = c->n_q_heads / c->n_kv_heads;
   p.window = window ? window : 0x7fffffff;
+  p.masks = masks;
+  p.mask_words = mask_words;
   p.scale = scale != 0.f ? scale : 1.0f / sqrtf((float)c->head_dim);
   // units of work (key blocks and overheads of tiles or requests) are counted in 32
   // bits; their bound itself may pass 64
@@ -746,5 +748,19 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch*
   const PagedKv kv = {c->k, c->v, c->page_stride, c->head_stride, c->token_stride,
                       c->n_pages, c->n_kv_heads, c->page_size};
   const cudaError_t e = attention_launch(p, kv, c->head_dim, c->dtype == MK_BF16, c->workspace, (cudaStream_t)stream);
-  return done(e);
+  return paged_done(e);
+}
+
+extern "C" int mk_paged_attention(const mk_paged_cache* c, const mk_paged_batch* b, const void* q,
+                                  int64_t q_stride, void* out, int64_t out_stride, float* lse,
+                                  float scale, int window, void* stream) {
+  return attend(c, b, nullptr, 0, q, q_stride, out, out_stride, lse, scale, window, stream);
+}
+
+extern "C" int mk_paged_tree_attention(const mk_paged_cache* c, const mk_paged_batch* b, const uint32_t* masks,
+                                       int mask_words, const void* q, int64_t q_stride, void* out,
+                                       int64_t out_stride, float* lse, float scale, int window, void* stream) {
+  if (!masks || !al4(masks) || mask_words < 1) return MK_ERR_INVALID_ARG;
+  if (mask_words > MK_TREE_MAX_NODES / 32) return MK_ERR_UNSUPPORTED;
+  return attend(c, b, masks, mask_words, q, q_stride, out, out_stride, lse, scale, window, stream);
 }

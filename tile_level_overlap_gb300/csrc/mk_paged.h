@@ -42,6 +42,10 @@ struct PagedAttnParams {
   int rep_inv;  // ceil(2^16 / rep)
   int join_shares;  // log2 of the warps that join one row of the few-row kernel
   float scale;
+  // trees: bit j of a row's mask: it sees the request's new token j; requests of more than
+  // 32 mask_words new tokens are causal.  NULL: all are.
+  const uint32_t* masks;
+  int mask_words;
 #ifdef __CUDACC__
   // token of a tile's row (row < 256, rep <= 64: the error, row / 2^16, stays
   // below 1 / rep)
@@ -71,6 +75,23 @@ struct PagedParts {
   int rt, ctas;
 };
 
+// Argument checks of the entry points (MK_OK or the code to return); the code of a
+// call whose launches said `e`; log2 of a page size, -1 where it is none.
+int paged_check_cache(const mk_paged_cache* c);
+int paged_check_batch(const mk_paged_batch* b);
+int paged_done(cudaError_t e);
+int paged_log2(int page);
+inline bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+inline bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Words [at, at + words) of a call's arrays.
+struct PagedWords {
+  const void* at;
+  int64_t words;
+};
+// Whether one of the first `written` arrays shares a word with another.
+bool paged_overlap(const PagedWords* a, int n, int written);
+
 // Opt a kernel into `smem` bytes of shared memory, once per device (the limit
 // is set to the largest a call can ask for).  `regs`: what the kernel has to be
 // compiled to, 0: any.  `done` is the kernel's own word, a bit per device.
@@ -95,6 +116,26 @@ inline cudaError_t paged_launch_if(bool dependent, void (*kernel)(P...), int gri
 template <class... P, class... A>
 inline cudaError_t paged_launch(void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t st, A&&... args) {
   return paged_launch_if(true, kernel, grid, threads, smem, st, std::forward<A>(args)...);
+}
+
+// Launch in clusters of `cluster` CTAs, as a programmatic dependent.
+template <class... P, class... A>
+inline cudaError_t paged_launch_clusters(void (*kernel)(P...), int grid, int cluster, int threads, int smem,
+                                         cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
 cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,

@@ -67,13 +67,22 @@ struct Tile {
   int lo, hi;              // keys the request's rows may see
   int part;                // workspace part, -1: all of the tile's blocks
   int req;                 // its request
-  int pad[6];
+  int ctx;                 // of a tree: its cached tokens; else -2^31
+  int pad[5];
 };
 static_assert(sizeof(Tile) == 64, "meta slot");
 
-// First block and number of blocks of tile t of a request (TT tokens a tile).
+// Whether a request's rows have masks.
+template <bool TREE>
+__device__ __forceinline__ bool is_tree(const PagedAttnParams& P, const Request& q) {
+  return TREE && q.add <= 32 * P.mask_words;
+}
+
+// First block and number of blocks of tile t of a request (TT tokens a tile).  Any
+// row of a tree may stand where its root does.
+template <bool TREE>
 __device__ __forceinline__ int tile_blocks(const PagedAttnParams& P, const Request& q, int t, int TT, int* first) {
-  const int p0 = q.pos0 + t * TT, p1 = q.pos0 + min(q.add, (t + 1) * TT);
+  const int p0 = q.pos0 + (is_tree<TREE>(P, q) ? 0 : t * TT), p1 = q.pos0 + min(q.add, (t + 1) * TT);
   const int hi = min(max(p1, 0), q.hi);
   const int lo = p0 >= P.window ? min(p0 - P.window + 1, hi) : 0;
   *first = lo / 128;
@@ -98,7 +107,9 @@ __device__ __forceinline__ void quad_swap(uint32_t (&a)[4], uint32_t (&b)[4], in
   }
 }
 
-template <int HD, bool BF>
+// TREE: rows of requests with masks see the cached keys and the new ones that their
+// masks name.
+template <int HD, bool BF, bool TREE>
 __global__ void __launch_bounds__(PC_THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedAttnParams P,
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       if ((int64_t)q.add * P.rep > P.few_rows) ntile = (q.add + TT - 1) / TT;
     }
     if (ntile <= 8)
-      for (int t = 0; t < ntile; ++t) u += tile_blocks(P, q, t, TT, &b0);
+      for (int t = 0; t < ntile; ++t) u += tile_blocks<TREE>(P, q, t, TT, &b0);
     for (uint32_t many = __ballot_sync(0xffffffffu, ntile > 8); many; many &= many - 1) {
       const int from = __ffs(many) - 1;
       Request x{};
@@ -180,7 +191,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       x.hi = __shfl_sync(0xffffffffu, q.hi, from);
       const int nt = __shfl_sync(0xffffffffu, ntile, from);
       int v = 0;
-      for (int t = lane; t < nt; t += 32) v += tile_blocks(P, x, t, TT, &b0);
+      for (int t = lane; t < nt; t += 32) v += tile_blocks<TREE>(P, x, t, TT, &b0);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == from) u = v;
@@ -282,7 +293,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           int rem = local - head * per_head;
           for (int base = 0;; base += 32) {
             int f, k = 0;
-            if (base + lane < ntile) k = tile_blocks(P, q, base + lane, TT, &f) + PC_OVER;
+            if (base + lane < ntile) k = tile_blocks<TREE>(P, q, base + lane, TT, &f) + PC_OVER;
             int x = k;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -300,7 +311,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           }
         }
         // units [x0, x1) of the tile: blocks [blk, blk + nblk)
-        const int nb = tile_blocks(P, q, t, TT, &b0), x1 = min(nb + PC_OVER, x0 + u1 - u);
+        const int nb = tile_blocks<TREE>(P, q, t, TT, &b0), x1 = min(nb + PC_OVER, x0 + u1 - u);
         const int blk = max(0, x0 - PC_OVER), nblk = max(0, x1 - PC_OVER) - blk;
         const int ntok = min(TT, q.add - t * TT), end = u - x0 + nb + PC_OVER;
         if (nblk == 0) break;  // the run ends with the tile's overhead: the next CTA has it all
@@ -319,6 +330,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           m.pos0 = q.pos0 + t * TT; m.lo = q.lo; m.hi = q.hi;
           m.part = whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
           m.req = r;
+          m.ctx = is_tree<TREE>(P, q) ? q.pos0 : -0x7fffffff - 1;
           meta[slot] = m;
           mbar_arrive(&mfull[slot]);
         }
@@ -476,12 +488,60 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       }
       const int ntok = min(TS, m.ntok - tok0);
       const int pos0 = m.pos0 + tok0, pos = pos0 + min(tok_in, ntok - 1), end = pos0 + ntok - 1;
-      const int last = min(pos, m.hi - 1), first = pos >= P.window ? pos - P.window + 1 : 0;
+      int last = min(pos, m.hi - 1), first = pos >= P.window ? pos - P.window + 1 : 0;
       // every row of the half sees the keys [all_lo, all_hi)
-      const int all_lo = end >= P.window ? end - P.window + 1 : 0, all_hi = min(pos0 + 1, m.hi);
+      const int all_lo = end >= P.window ? end - P.window + 1 : 0;
+      int all_hi = min(pos0 + 1, m.hi);
+      // a tree's row: the cached keys [first, last], and of the new ones those of its
+      // mask from bit `least` to itself
+      const bool tree = TREE && m.ctx != -0x7fffffff - 1;
+      const uint32_t* mask = nullptr;
+      int node = 0, least = 0;
+      if constexpr (TREE) {
+        if (tree) {
+          node = pos - m.ctx;
+          mask = P.masks + (int64_t)(m.row0 + tok0 + min(tok_in, ntok - 1)) * P.mask_words;
+          last = min(m.ctx, m.hi) - 1;
+          all_hi = min(m.ctx, m.hi);
+          if (P.window != 0x7fffffff) {
+            int have = 0;  // set bits so far, from the row itself down
+            bool some = false;
+            for (int w = node >> 5; w >= 0; --w) {
+              uint32_t x = mask[w];
+              if (w == node >> 5) x &= (2u << (node & 31)) - 1;
+              const int n = __popc(x);
+              if (!some && have + n >= P.window) {  // the window's last bit is in this word
+                for (int k = have + n; k > P.window; --k) x &= x - 1;
+                least = 32 * w + __ffs(x) - 1;
+                some = true;
+              }
+              have += n;
+            }
+            const int p = m.ctx + max(have, 1) - 1;
+            first = p >= P.window ? p - P.window + 1 : 0;
+          }
+        }
+      }
       float mx = -INFINITY, l = 0.f;
       for (int j = 0; j < m.nblk; ++j, ++blkn) {
         const int key0 = m.key0 + 128 * j;
+        uint32_t named[4] = {0, 0, 0, 0};  // columns of the block that the row's mask names
+        if constexpr (TREE) {
+          if (tree && key0 + 128 > all_hi) {
+            const int d = key0 - m.ctx;  // new token of column 0
+            const int top = min(node, m.hi - 1 - m.ctx);
+            uint32_t w[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+              const int at = (d >> 5) + i, b = 32 * at;  // bits of new tokens b .. b + 31
+              w[i] = at >= 0 && b <= top ? mask[at] : 0u;
+              if (b + 31 > top && b <= top) w[i] &= (2u << (top - b)) - 1;
+              if (least > b) w[i] = least > b + 31 ? 0u : w[i] & (0xffffffffu << (least - b));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) named[i] = __funnelshift_r(w[i], w[i + 1], d & 31);
+          }
+        }
         wait_phase(&sfull[half], sn & 1, dead, P.status);
         ++sn;
         tc_fence_after();
@@ -496,7 +556,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           const uint32_t w = width > 0 ? (uint32_t)width : 0u;
 #pragma unroll
           for (int i = 0; i < 128; ++i)
-            if ((uint32_t)(i - c0) >= w) s[i] = -INFINITY;
+            if ((uint32_t)(i - c0) >= w && !(TREE && (named[i >> 5] >> (i & 31) & 1u))) s[i] = -INFINITY;
         }
         float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
 #pragma unroll
@@ -627,7 +687,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   }
 }
 
-template <int HD, bool BF>
+template <int HD, bool BF, bool TREE>
 cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
   CUtensorMap tq, tk, tv;
   if (!make_page_tmap(&tk, kv.k, kv, HD, 128, 1, BF) || !make_page_tmap(&tv, kv.v, kv, HD, 128, 1, BF) ||
@@ -635,12 +695,12 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
     return cudaErrorInvalidValue;
   // the register split needs the block to be launched with what it counts on
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF>,
+  const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF, TREE>,
                                       ChunkCfg<HD>::most, PC_REGS, p.device, &ready);
   if (e != cudaSuccess) return e;
   // behind the few-row kernel it is set up while that one ends; alone it is launched
   // behind the whole of what precedes (8192-token prompt 363 against 368 us)
-  return paged_launch_if(p.few_rows > 0, paged_chunk_kernel<HD, BF>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
+  return paged_launch_if(p.few_rows > 0, paged_chunk_kernel<HD, BF, TREE>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
                          tq, tk, tv, p, w);
 }
 
@@ -648,8 +708,12 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
 
 cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
                                bool bf, cudaStream_t st) {
-  if (d == 128) return bf ? launch<128, true>(p, kv, w, st) : launch<128, false>(p, kv, w, st);
-  return bf ? launch<64, true>(p, kv, w, st) : launch<64, false>(p, kv, w, st);
+  if (p.masks) {
+    if (d == 128) return bf ? launch<128, true, true>(p, kv, w, st) : launch<128, false, true>(p, kv, w, st);
+    return bf ? launch<64, true, true>(p, kv, w, st) : launch<64, false, true>(p, kv, w, st);
+  }
+  if (d == 128) return bf ? launch<128, true, false>(p, kv, w, st) : launch<128, false, false>(p, kv, w, st);
+  return bf ? launch<64, true, false>(p, kv, w, st) : launch<64, false, false>(p, kv, w, st);
 }
 
 }  // namespace mk

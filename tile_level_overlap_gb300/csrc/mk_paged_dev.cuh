@@ -75,6 +75,42 @@ __device__ __forceinline__ void grid_wait_prior() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- clusters
+// (A barrier of the cluster waits for the threads that have not exited, and every
+// kernel here passes its barriers whatever its inputs hold.)
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of the same shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ u64 ld_cluster64(uint32_t a) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 // ---------------------------------------------------------------- bounded waits
 // Wait for the phase.  After WAIT_TRIES tries (each suspends the thread for a
 // while; tens of milliseconds at the very least, and no wait here depends on
@@ -141,6 +177,14 @@ __device__ __forceinline__ Request make_request(const PagedAttnParams& P, int c0
   // the first row's window begins at pos0 - window + 1
   q.lo = q.pos0 >= P.window ? min(q.pos0 - P.window + 1, q.hi) : 0;
   return q;
+}
+
+// Whether a request that begins at cu[r] does so below an earlier offset (its rows may
+// be another's); the block's threads together.
+__device__ __forceinline__ bool begins_below(const int32_t* cu, int r, int c0) {
+  bool low = false;
+  for (int i = threadIdx.x; i < r; i += blockDim.x) low |= cu[i] > c0;
+  return __syncthreads_or(low);
 }
 
 // The scan's results in shared memory: pre [n + 1], a request's first unit, and

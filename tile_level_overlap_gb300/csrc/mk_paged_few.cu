@@ -55,7 +55,8 @@ struct FewCfg {
   static constexpr int o_merge = o_q + QSLOTS * RT * QROW;
   static constexpr int o_ml = o_merge + PF_WARPS * 8 * OROW * 4;
   static constexpr int o_meta = o_ml + PF_WARPS * RT * 8;
-  static constexpr int o_bar = o_meta + QSLOTS * 48;
+  static constexpr int o_mask = o_meta + QSLOTS * 48;  // of trees
+  static constexpr int o_bar = o_mask + QSLOTS * RT * 4;
   static constexpr int o_pre = o_bar + 8 * (2 * STAGES + 3 * QSLOTS) + 64;
   static constexpr int total(int n) { return o_pre + Kept::bytes(n); }
   static constexpr int most = o_pre + KEPT_MOST;
@@ -72,6 +73,8 @@ struct Segment {
   int pad[2];
 };
 static_assert(sizeof(Segment) == 48, "meta slot");
+// A slot's rows have their masks behind the descriptions (the rows of a tree that
+// comes here are at most 16 tokens: the first word).
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -125,7 +128,8 @@ __device__ __noinline__ void let_copies_land() {
 
 // (The bound for few rows keeps the kernel to 128 registers, so that the blocks
 // of the join fit beside it and are set up before it ends.)
-template <int HD, bool BF, int NT>
+// TREE: rows see the cached keys and the new ones that their masks name.
+template <int HD, bool BF, int NT, bool TREE>
 __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                      const __grid_constant__ PagedAttnParams P, const __grid_constant__ PagedParts W) {
@@ -142,6 +146,7 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
   const Kept kept(smem + C::o_pre, P.n);
   int* pre = kept.pre;
   Segment* meta = reinterpret_cast<Segment*>(smem + C::o_meta);
+  uint32_t* mask_of = reinterpret_cast<uint32_t*>(smem + C::o_mask);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -252,6 +257,9 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
       const int b0 = q.lo / KS + blk, rows = q.add * P.rep;
       const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
       const int page = page_of(tab, b0, q.lo, q.hi);
+      uint32_t seen = 0;  // this lane's row, up to itself
+      if constexpr (TREE)
+        if (lane < rows) seen = P.masks[(int64_t)(q.row0 + my_tok) * P.mask_words] & ((2u << my_tok) - 1);
       const bool whole = blk == 0 && nblk == nb;
       if (blk == 0 && !whole) {  // joined by this CTA's block of the second launch
         const int last = runs.of(u - x0 + units - 1);  // CTA of the pair's last unit
@@ -263,6 +271,10 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
       }
       wait_phase(&qempty[slot], qphase, dead, P.status);
       if (*dead) return let_copies_land();
+      if constexpr (TREE) {
+        if (lane < RT) mask_of[slot * RT + lane] = seen;
+        __syncwarp();  // before lane 0's arrival
+      }
       if (lane == 0) {
         Segment s;
         s.key0 = b0 * KS; s.nblk = nblk; s.row0 = q.row0; s.rows = rows; s.head = head;
@@ -333,19 +345,31 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
         qf[nt][2 * k2][0] = r4[0]; qf[nt][2 * k2][1] = r4[1];
         qf[nt][2 * k2 + 1][0] = r4[2]; qf[nt][2 * k2 + 1][1] = r4[3];
       }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&qempty[slot]);
-    if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
-    // keys [first, last] are what this lane's rows see
+    // keys [first, last] are what this lane's rows see (in a tree, of the cached ones;
+    // of the new ones those in `named`)
     int first[NT][2], last[NT][2];
+    uint32_t named[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = nt * 8 + 2 * t + e, pos = s.pos0 + (row < s.rows ? P.token_of(row) : 0);
-        last[nt][e] = min(pos, s.hi - 1);
+        const int row = nt * 8 + 2 * t + e;
+        int pos = s.pos0 + (row < s.rows ? P.token_of(row) : 0);
+        if constexpr (TREE) {
+          uint32_t m = mask_of[slot * RT + row];
+          const int have = __popc(m);
+          pos = s.pos0 + max(have, 1) - 1;
+          for (int x = have; x > P.window; --x) m &= m - 1;
+          named[nt][e] = m;
+          last[nt][e] = min(s.pos0, s.hi) - 1;
+        } else {
+          last[nt][e] = min(pos, s.hi - 1);
+        }
         first[nt][e] = pos >= P.window ? pos - P.window + 1 : 0;
       }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&qempty[slot]);
+    if (++slot == C::QSLOTS) { slot = 0; qphase ^= 1; }
     float m[NT][2], l[NT][2], o[HD / 16][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -358,7 +382,7 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
     }
     // every row sees the keys [all_lo, all_hi)
     const int end = s.pos0 + P.token_of(s.rows - 1);
-    const int all_lo = end >= P.window ? end - P.window + 1 : 0, all_hi = min(s.pos0 + 1, s.hi);
+    const int all_lo = end >= P.window ? end - P.window + 1 : 0, all_hi = min(s.pos0 + (TREE ? 0 : 1), s.hi);
     for (int i = 0; i < s.nblk; ++i) {
       // both groups see every block's phase, also of those they leave to the
       // other one (a warp that skipped one could take the next for it)
@@ -401,7 +425,12 @@ __global__ void __launch_bounds__(NT == 1 ? 512 : PF_THREADS, 1)
                 float x = sc[mt][nt][2 * h + e] * cs;
                 if (partial) {
                   const int key = key0 + (kw * MT + mt) * 16 + g + 8 * h;
-                  if (key > last[nt][e] || key < first[nt][e]) x = -INFINITY;
+                  bool out = key > last[nt][e] || key < first[nt][e];
+                  if constexpr (TREE) {
+                    const uint32_t j = (uint32_t)(key - s.pos0);  // (a cached key's is past 31)
+                    if (j < 32u && (named[nt][e] >> j & 1u)) out = key >= s.hi;
+                  }
+                  if (out) x = -INFINITY;
                 }
                 sc[mt][nt][2 * h + e] = x;
                 mx = fmaxf(mx, x);
@@ -683,22 +712,23 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) paged_join_kernel(const __gri
   }
 }
 
-template <int HD, bool BF, int NT>
+template <int HD, bool BF, int NT, bool TREE>
 cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
   CUtensorMap tk, tv;
   if (!make_page_tmap(&tk, kv.k, kv, HD, FewCfg<HD, NT>::KS, HD / 64, BF) ||
       !make_page_tmap(&tv, kv.v, kv, HD, FewCfg<HD, NT>::KS, HD / 64, BF))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = paged_prepare((const void*)paged_few_kernel<HD, BF, NT>,
+  const cudaError_t e = paged_prepare((const void*)paged_few_kernel<HD, BF, NT, TREE>,
                                       FewCfg<HD, NT>::most, 0, p.device, &ready);
   if (e != cudaSuccess) return e;
-  return paged_launch(paged_few_kernel<HD, BF, NT>, w.ctas, PF_THREADS, FewCfg<HD, NT>::total(p.n), st, tk, tv, p, w);
+  return paged_launch(paged_few_kernel<HD, BF, NT, TREE>, w.ctas, PF_THREADS, FewCfg<HD, NT>::total(p.n), st, tk, tv, p, w);
 }
 
 template <int HD, bool BF>
 cudaError_t launch_rows(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
-  return p.few_rows <= 8 ? launch<HD, BF, 1>(p, kv, w, st) : launch<HD, BF, 2>(p, kv, w, st);
+  if (p.masks) return p.few_rows <= 8 ? launch<HD, BF, 1, true>(p, kv, w, st) : launch<HD, BF, 2, true>(p, kv, w, st);
+  return p.few_rows <= 8 ? launch<HD, BF, 1, false>(p, kv, w, st) : launch<HD, BF, 2, false>(p, kv, w, st);
 }
 
 }  // namespace

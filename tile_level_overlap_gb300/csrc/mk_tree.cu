@@ -1,0 +1,445 @@
+// Trees of drafted tokens: masks and positions of their rows, and which of them
+// stand against the target's probabilities (include/mk.h).
+#include "mk_paged_dev.cuh"
+
+namespace mk {
+namespace {
+
+// ---------------------------------------------------------------- masks, positions
+// A CTA per request (and some for the rows behind the last one): its parents go to
+// shared memory, a thread takes a row and a word of its mask and walks up.  Parents
+// precede their children, so a walk ends below its word.  Latency bound.
+constexpr int TT_THREADS = 128;
+
+struct TreeParams {
+  const int32_t *cu, *kv, *parents;
+  uint32_t* masks;
+  int32_t *pos, *status;
+  int n, rows, words;
+};
+
+__global__ void __launch_bounds__(TT_THREADS) paged_tree_kernel(const TreeParams P) {
+  __shared__ int up[MK_TREE_MAX_NODES];
+  const int tid = threadIdx.x, r = blockIdx.x;
+  grid_launch_dependents();
+  grid_wait_prior();
+  if (r >= P.n) {  // rows of no request: behind every offset
+    __shared__ int behind;
+    if (tid == 0) behind = 0;
+    __syncthreads();
+    int most = 0;
+    for (int i = tid; i <= P.n; i += TT_THREADS) most = max(most, P.cu[i]);
+    atomicMax(&behind, most);
+    __syncthreads();
+    const int end = min(behind, P.rows);
+    for (int t = end + (r - P.n) * TT_THREADS + tid; t < P.rows; t += (gridDim.x - P.n) * TT_THREADS) P.pos[t] = 0;
+    return;
+  }
+  const int c0 = P.cu[r], c1 = P.cu[r + 1], kv = P.kv[r], k = c1 - c0;
+  const bool below = begins_below(P.cu, r, c0);
+  if (below || c0 < 0 || c1 < c0 || c1 > P.rows) {
+    if (tid == 0) latch(P.status, MK_ERR_BOUNDS);
+    return;
+  }
+  const bool here = kv >= k;
+  const int ctx = kv - k;
+  if (k > 32 * P.words) {
+    for (int i = tid; i < k; i += TT_THREADS) P.pos[c0 + i] = here ? ctx + i : 0;
+    return;
+  }
+  for (int i = tid; i < k; i += TT_THREADS) {
+    const int u = P.parents[c0 + i];
+    const bool ok = u >= -1 && u < i;
+    if (!ok) latch(P.status, MK_ERR_BOUNDS);
+    up[i] = ok ? u : -1;
+  }
+  __syncthreads();
+  for (int x = tid; x < k * P.words; x += TT_THREADS) {
+    const int i = x / P.words, w = x - i * P.words;
+    uint32_t bits = 0;
+    int depth = 0;
+    for (int a = i; a >= 32 * w; a = up[a]) {
+      if (a < 32 * w + 32) bits |= 1u << (a & 31);
+      ++depth;
+    }
+    P.masks[(int64_t)c0 * P.words + x] = bits;
+    if (w == 0) P.pos[c0 + i] = here ? ctx + depth - 1 : 0;
+  }
+}
+
+// ---------------------------------------------------------------- verification
+// A cluster of CTAs per request.  Its first CTA reads the probabilities of all
+// drafted tokens (two of each, at once), walks the tree and says which row's rest
+// is to be summed; all of them sum their share of the vocabulary.  A chain needs one
+// such pass, to draw its last token; a tree one more for every refused child that has
+// siblings behind it.  For q >= 0 the rest after several refusals is
+// max(p - S q, 0) with S the sum of the Z so far (max(max(a, 0) - b, 0) =
+// max(a - b, 0)), so that a pass reads the two rows and keeps nothing.
+//
+// Probabilities are summed as whole numbers in units of 2^-62: the order of a sum
+// does not matter, the place where the sum passes u Z is the same whatever the
+// cluster, and 100000 values lose nothing that 64-bit floats would keep.  Bound by
+// latency for few requests, by HBM (the rows that are drawn from) for many.
+constexpr int TV_THREADS = 512, TV_WARPS = TV_THREADS / 32, TV_CLUSTER = 8;
+
+struct VerifyParams {
+  const int32_t *cu, *kv, *parents, *tokens;
+  const float *p, *q, *u, *u_last;
+  int32_t *path, *emitted, *kept, *lens, *status;
+  int64_t p_stride, q_stride;
+  int n, rows, vocab;
+};
+
+__device__ __forceinline__ float probability(float x) { return fminf(fmaxf(x, 0.f), 1.f); }  // NaN: 0
+
+// x in [0, 1] in units of 2^-62, rounded down.
+__device__ __forceinline__ u64 units(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const int sh = (int)(b >> 23) - 88;
+  const u64 m = (b & 0x7fffffu) | 0x800000u;
+  return sh >= 0 ? m << sh : sh > -24 ? m >> -sh : 0;
+}
+
+// S (units of 2^-53) times q, in units of 2^-62; what passes 2 becomes 2.
+constexpr u64 ONE_S = 1ull << 53;
+__device__ __forceinline__ u64 times(u64 S, u64 q) {
+  if (S == ONE_S) return q;
+  const u64 hi = __umul64hi(S, q), lo = S * q;
+  return hi >= (1ull << 52) ? 1ull << 63 : (hi << 11) | (lo >> 53);
+}
+__device__ __forceinline__ u64 rest(float p, float q, u64 S) {
+  const u64 a = units(probability(p));
+  if (S == 0) return a;
+  const u64 b = times(S, units(probability(q)));
+  return a > b ? a - b : 0;
+}
+
+struct VerifyCtl {  // what the first CTA asks of the others
+  int cur, depth, last, refused;  // last: the pass that draws the last token
+  u64 S;
+};
+
+struct VerifySmem {
+  int up[MK_TREE_MAX_NODES], tok[MK_TREE_MAX_NODES], path[MK_TREE_MAX_NODES];
+  float p[MK_TREE_MAX_NODES], q[MK_TREE_MAX_NODES], u[MK_TREE_MAX_NODES];
+  int gone[MK_TREE_MAX_NODES];      // tokens found that were refused at this node, and their units
+  u64 gone_units[MK_TREE_MAX_NODES];
+  u64 warp_sum[TV_WARPS], total, scan[TV_WARPS];
+  VerifyCtl ctl;
+};
+
+// Next child of `cur` from row `from` on; k where there is none (a warp together).
+__device__ __forceinline__ int next_child(const int* up, int k, int cur, int from, int lane) {
+  for (int b = from & ~31; b < k; b += 32) {
+    const int i = b + lane;
+    const uint32_t m = __ballot_sync(0xffffffffu, i >= from && i < k && up[i] == cur);
+    if (m) return b + __ffs(m) - 1;
+  }
+  return k;
+}
+
+// Elements 4 v .. 4 v + 3 of a row, zeros past its end.  `wide`: the row is 16-byte
+// aligned.
+__device__ __forceinline__ float4 load4(const float* row, int v, int vocab, bool wide) {
+  const int e = 4 * v;
+  if (wide && e + 4 <= vocab) return __ldcs(reinterpret_cast<const float4*>(row + e));
+  float4 x;
+  x.x = e < vocab ? row[e] : 0.f;
+  x.y = e + 1 < vocab ? row[e + 1] : 0.f;
+  x.z = e + 2 < vocab ? row[e + 2] : 0.f;
+  x.w = e + 3 < vocab ? row[e + 3] : 0.f;
+  return x;
+}
+
+__global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const VerifyParams P) {
+  __shared__ VerifySmem S;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = cluster_rank(), ctas = cluster_size(), r = blockIdx.x / ctas;
+  grid_launch_dependents();
+  grid_wait_prior();
+  // state of the walk, in the first CTA's first warp
+  int k = 0, c0 = 0, cur = 0, depth = 0, at = 0, n_gone = 0;
+  u64 sum_z = 0;
+  double z = 1.0;
+  bool none = false;  // nothing to draw from: this request gets no token
+  if (rank == 0) {
+    c0 = P.cu[r];
+    const int c1 = P.cu[r + 1], kv = P.kv[r];
+    k = c1 - c0;
+    const bool below = begins_below(P.cu, r, c0), bad = below || c0 < 0 || c1 < c0 || c1 > P.rows || k > MK_TREE_MAX_NODES;
+    none = bad || k == 0 || kv < k;
+    if (none) {
+      if (!bad)
+        for (int i = tid; i < k; i += TV_THREADS) P.path[c0 + i] = P.emitted[c0 + i] = -1;
+      if (tid == 0) {
+        if (bad) latch(P.status, MK_ERR_BOUNDS);
+        P.kept[r] = 0;
+        P.lens[r] = kv;
+      }
+      k = 0;
+    }
+    for (int i = tid; i < k; i += TV_THREADS) {
+      int up = -1, x = -1;
+      float p = 0.f, q = 0.f, u = 0.f;
+      if (i > 0) {
+        up = P.parents[c0 + i];
+        x = P.tokens[c0 + i];
+        u = P.u[c0 + i];
+        if (up < -1 || up >= i || x < 0 || x >= P.vocab) latch(P.status, MK_ERR_BOUNDS);
+        if (up < 0 || up >= i) up = -1;
+        if (x < 0 || x >= P.vocab) x = -1;
+        if (up >= 0 && x >= 0) {
+          p = probability(P.p[(c0 + up) * P.p_stride + x]);
+          if (P.q) q = probability(P.q[(c0 + up) * P.q_stride + x]);
+        }
+      }
+      S.up[i] = up; S.tok[i] = x; S.p[i] = p; S.q[i] = q;
+      S.u[i] = u >= 1.f ? 0x1.fffffep-1f : fmaxf(u, 0.f);
+    }
+    __syncthreads();
+    if (warp == 0 && k > 0) at = next_child(S.up, k, 0, 1, lane);
+  }
+
+  const int vecs = (P.vocab + 3) / 4, per_cta = (vecs + ctas - 1) / ctas, per_warp = (per_cta + TV_WARPS - 1) / TV_WARPS;
+  const int v_end = min(vecs, (rank + 1) * per_cta);
+  auto warp_first = [&](int w) { return min(v_end, rank * per_cta + w * per_warp); };
+  const uint32_t ctl0 = cluster_addr(&S.ctl, 0);
+  for (;;) {
+    if (rank == 0 && warp == 0) {
+      while (at < k) {
+        const int i = at, x = S.tok[i];
+        bool again = false;
+        u64 left = 0;
+        bool stands;
+        if (P.q) {
+          left = rest(S.p[i], S.q[i], sum_z);
+          // the first child's comparison is of the probabilities themselves
+          const double mine = sum_z == 0 ? (double)S.p[i] : (double)left * 0x1p-62;
+          stands = (double)S.u[i] * (double)S.q[i] * z < mine;
+        } else {
+          for (int b = 0; b < n_gone; b += 32)
+            again |= __any_sync(0xffffffffu, b + lane < n_gone && S.gone[min(b + lane, n_gone - 1)] == x);
+          stands = (double)S.u[i] * z < (again ? 0.0 : (double)S.p[i]);
+        }
+        if (stands) {
+          cur = i;
+          ++depth;
+          if (lane == 0) S.path[depth] = i;
+          at = next_child(S.up, k, cur, i + 1, lane);
+          sum_z = 0;
+          z = 1.0;
+          n_gone = 0;
+          continue;
+        }
+        at = next_child(S.up, k, cur, i + 1, lane);
+        if (P.q) {
+          sum_z += sum_z == 0 ? ONE_S : (u64)(z * 0x1p53);
+          if (at < k) break;  // its siblings are asked against the rest's sum
+        } else if (!again && x >= 0) {
+          if (lane == 0) {
+            S.gone[n_gone] = x;
+            S.gone_units[n_gone] = units(S.p[i]);
+          }
+          ++n_gone;
+          z = fmax(z - (double)S.p[i], 0.0);
+          __syncwarp();
+        }
+      }
+      if (lane == 0) S.ctl = {cur, depth, none ? 2 : at >= k, n_gone, sum_z};
+    }
+    cluster_sync();
+    VerifyCtl c;
+    c.cur = ld_cluster32(ctl0);
+    c.depth = ld_cluster32(ctl0 + 4);
+    c.last = ld_cluster32(ctl0 + 8);
+    c.refused = ld_cluster32(ctl0 + 12);
+    c.S = ld_cluster64(ctl0 + 16);
+    if (c.last == 2) break;
+    if (rank != 0) c0 = P.cu[r];
+    const float* rp = P.p + (c0 + c.cur) * P.p_stride;
+    const float* rq = P.q ? P.q + (c0 + c.cur) * P.q_stride : rp;
+    const bool wide = ((uintptr_t)rp & 15) == 0 && ((uintptr_t)rq & 15) == 0;
+
+    // sum of the rest over this CTA's share (a second time without refusals where
+    // nothing of it is left)
+    u64 total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      u64 sum = 0;
+      const int v1 = warp_first(warp + 1);
+      if (c.S != 0) {
+#pragma unroll 4
+        for (int v = warp_first(warp) + lane; v < v1; v += 32) {
+          const float4 a = load4(rp, v, P.vocab, wide), b = load4(rq, v, P.vocab, wide);
+          sum += rest(a.x, b.x, c.S) + rest(a.y, b.y, c.S) + rest(a.z, b.z, c.S) + rest(a.w, b.w, c.S);
+        }
+      } else {
+#pragma unroll 4
+        for (int v = warp_first(warp) + lane; v < v1; v += 32) {
+          const float4 a = load4(rp, v, P.vocab, wide);
+          sum += units(probability(a.x)) + units(probability(a.y)) + units(probability(a.z)) + units(probability(a.w));
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) S.warp_sum[warp] = sum;
+      __syncthreads();
+      // without what was refused
+      for (int g = tid; g < c.refused; g += TV_THREADS) {
+        const int v = (int)ld_cluster32(cluster_addr(&S.gone[g], 0)) / 4;
+        if (v / per_cta == rank)
+          atomicAdd(&S.warp_sum[(v - rank * per_cta) / per_warp], 0ull - ld_cluster64(cluster_addr(&S.gone_units[g], 0)));
+      }
+      __syncthreads();
+      if (tid == 0) {
+        u64 t = 0;
+        for (int w = 0; w < TV_WARPS; ++w) t += S.warp_sum[w];
+        S.total = t;
+      }
+      cluster_sync();
+      total = 0;
+      for (int x = 0; x < ctas; ++x) total += ld_cluster64(cluster_addr(&S.total, x));
+      if (!c.last || total != 0 || pass == 1) break;
+      c.S = 0;
+      c.refused = 0;
+      cluster_sync();  // the totals have been read
+    }
+    if (!c.last) {
+      z = (double)total * 0x1p-62;
+      continue;
+    }
+    // the last token: the element where the running sum passes u total
+    float ul = P.u_last[r];
+    ul = ul >= 1.f ? 0x1.fffffep-1f : fmaxf(ul, 0.f);
+    u64 want = __umul64hi(total, units(ul) << 2);
+    int owner = 0;
+    for (; owner < ctas - 1; ++owner) {
+      const u64 t = ld_cluster64(cluster_addr(&S.total, owner));
+      if (want < t) break;
+      want -= t;
+    }
+    int32_t* last = P.emitted + c0 + c.depth;
+    if (total == 0) {
+      if (rank == 0 && tid == 0) {
+        latch(P.status, MK_ERR_BOUNDS);
+        *last = 0;
+      }
+    } else if (owner == rank) {
+      int w = 0;
+      for (; w < TV_WARPS - 1; ++w) {
+        const u64 t = S.warp_sum[w];
+        if (want < t) break;
+        want -= t;
+      }
+      const int v0 = warp_first(w), v1 = warp_first(w + 1);
+      bool found = false;
+      for (int b = v0; b < v1 && !found; b += TV_THREADS) {
+        const int v = b + tid;
+        u64 x[4] = {0, 0, 0, 0};
+        if (v < v1) {
+          const float4 a = load4(rp, v, P.vocab, wide), q = c.S ? load4(rq, v, P.vocab, wide) : a;
+          x[0] = rest(a.x, q.x, c.S); x[1] = rest(a.y, q.y, c.S); x[2] = rest(a.z, q.z, c.S); x[3] = rest(a.w, q.w, c.S);
+          for (int g = 0; g < c.refused; ++g) {
+            const int t = (int)ld_cluster32(cluster_addr(&S.gone[g], 0));
+            if (t / 4 == v) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((t & 3) == e) x[e] = 0;
+            }
+          }
+        }
+        const u64 mine = x[0] + x[1] + x[2] + x[3];
+        u64 upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        if (lane == 31) S.scan[warp] = upto;
+        __syncthreads();
+        u64 all = 0;
+        for (int y = 0; y < TV_WARPS; ++y) {
+          if (y < warp) upto += S.scan[y];
+          all += S.scan[y];
+        }
+        u64 before = upto - mine;
+        const bool here = before <= want && want < upto;
+        if (here) {
+          int e = 0;
+          while (e < 3 && want >= before + x[e]) before += x[e++];
+          *last = 4 * v + e;
+        }
+        found = __syncthreads_or(here);
+        want -= all;
+      }
+      // (sums that pass 2^64, of rows that are no probabilities, may miss it)
+      if (!found && tid == 0) *last = min(max(4 * v1 - 1, 0), P.vocab - 1);
+    }
+    if (rank == 0) {
+      for (int j = tid; j < k; j += TV_THREADS) {
+        P.path[c0 + j] = j == 0 ? 0 : j <= c.depth ? S.path[j] : -1;
+        if (j != c.depth) P.emitted[c0 + j] = j < c.depth ? S.tok[S.path[j + 1]] : -1;
+      }
+      if (tid == 0) {
+        P.kept[r] = c.depth + 1;
+        P.lens[r] = P.kv[r] - k + c.depth + 1;
+      }
+    }
+    break;
+  }
+  cluster_sync();  // no CTA's shared memory is read any more
+}
+
+}  // namespace
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" int mk_paged_tree(const mk_paged_batch* b, const int32_t* parents, uint32_t* masks, int mask_words,
+                             int32_t* positions, int32_t* status, void* stream) {
+  const int rc = paged_check_batch(b);
+  if (rc != MK_OK) return rc;
+  if (!parents || !masks || !positions || mask_words < 1) return MK_ERR_INVALID_ARG;
+  if (mask_words > MK_TREE_MAX_NODES / 32) return MK_ERR_UNSUPPORTED;
+  const void* ptrs[] = {parents, masks, positions, status};
+  for (const void* p : ptrs)
+    if (!al4(p)) return MK_ERR_INVALID_ARG;
+  const PagedWords arrays[] = {{masks, (int64_t)b->max_tokens * mask_words}, {positions, b->max_tokens},
+                               {status, status ? 1 : 0}, {parents, b->max_tokens}, {b->cu_new, b->n + 1}, {b->kv_lens, b->n}};
+  if (paged_overlap(arrays, 6, 3)) return MK_ERR_INVALID_ARG;
+  if (b->max_tokens == 0) return MK_OK;
+  TreeParams p{};
+  p.cu = b->cu_new; p.kv = b->kv_lens; p.parents = parents; p.masks = masks; p.pos = positions; p.status = status;
+  p.n = b->n; p.rows = b->max_tokens; p.words = mask_words;
+  const int behind = min(64, (p.rows + 4 * TT_THREADS - 1) / (4 * TT_THREADS));
+  return paged_done(paged_launch(paged_tree_kernel, p.n + behind, TT_THREADS, 0, (cudaStream_t)stream, p));
+}
+
+extern "C" int mk_tree_verify(const mk_paged_batch* b, const int32_t* parents, const int32_t* tokens,
+                              const float* target_probs, int64_t target_stride, const float* draft_probs,
+                              int64_t draft_stride, int vocab, const float* uniforms, const float* last_uniforms,
+                              int32_t* path, int32_t* emitted, int32_t* kept, int32_t* lens, int32_t* status,
+                              void* stream) {
+  const int rc = paged_check_batch(b);
+  if (rc != MK_OK) return rc;
+  if (!parents || !tokens || !target_probs || !uniforms || !last_uniforms || !path || !emitted || !kept || !lens || vocab < 1 ||
+      target_stride < vocab || (draft_probs && draft_stride < vocab))
+    return MK_ERR_INVALID_ARG;
+  if (vocab > 1 << 24 || target_stride >= (1ll << 38) || (draft_probs && draft_stride >= (1ll << 38))) return MK_ERR_UNSUPPORTED;
+  const void* ptrs[] = {parents, tokens, target_probs, draft_probs, uniforms, last_uniforms, path, emitted, kept, lens, status};
+  for (const void* p : ptrs)
+    if (!al4(p)) return MK_ERR_INVALID_ARG;
+  const int64_t rows = b->max_tokens;
+  const PagedWords arrays[] = {{path, rows}, {emitted, rows}, {kept, b->n}, {lens, b->n}, {status, status ? 1 : 0},
+                               {parents, rows}, {tokens, rows}, {uniforms, rows}, {last_uniforms, b->n},
+                               {target_probs, rows ? (rows - 1) * target_stride + vocab : 0},
+                               {draft_probs, rows && draft_probs ? (rows - 1) * draft_stride + vocab : 0},
+                               {b->cu_new, b->n + 1}, {b->kv_lens, b->n}};
+  if (paged_overlap(arrays, 13, 5)) return MK_ERR_INVALID_ARG;
+  VerifyParams p{};
+  p.cu = b->cu_new; p.kv = b->kv_lens; p.parents = parents; p.tokens = tokens;
+  p.p = target_probs; p.q = draft_probs; p.u = uniforms; p.u_last = last_uniforms;
+  p.path = path; p.emitted = emitted; p.kept = kept; p.lens = lens; p.status = status;
+  p.p_stride = target_stride; p.q_stride = draft_stride;
+  p.n = b->n; p.rows = b->max_tokens; p.vocab = vocab;
+  return paged_done(paged_launch_clusters(tree_verify_kernel, p.n * TV_CLUSTER, TV_CLUSTER, TV_THREADS, 0, (cudaStream_t)stream, p));
+}

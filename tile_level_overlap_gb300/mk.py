@@ -28,6 +28,8 @@ MK_BF16, MK_FP16 = 0, 1
 MK_PAGED_MAX_REQUESTS = 4096
 MK_PAGED_MAX_HEADS = 65536
 MK_PAGED_WORKSPACE_BYTES = 64 << 20  # scratch of mk_paged_attention
+MK_PAGED_MAX_LAYERS = 128
+MK_TREE_MAX_NODES = 1024
 TRACE_WORDS = 16  # u64 words per trace record (mk_trace_copy)
 MK_NOALLOC_SCRATCH_BYTES = 16 << 20  # static device scratch of mk_decode_step_noalloc
 
@@ -39,6 +41,8 @@ EXPORTED = [
     "mk_plan_set_lm_mode", "mk_decode_steps", "mk_prefill_logits", "mk_prefill_batch",
     "mk_decode_step_slots", "mk_plan_create_for_sms", "mk_prefill_chunks",
     "mk_paged_tables", "mk_rope_init", "mk_paged_append", "mk_paged_attention",
+    "mk_paged_tree", "mk_paged_tree_attention", "mk_tree_verify", "mk_paged_fork", "mk_paged_copy",
+    "mk_paged_keep",
 ]
 
 
@@ -137,6 +141,13 @@ def lib() -> ctypes.CDLL:
     L.mk_paged_append.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, vp,
                                   vp, i64, vp, ctypes.c_int, vp]
     L.mk_paged_attention.argtypes = [vp, vp, vp, i64, vp, i64, vp, ctypes.c_float, ctypes.c_int, vp]
+    i32, f32 = ctypes.c_int, ctypes.c_float
+    L.mk_paged_tree.argtypes = [vp, vp, vp, i32, vp, vp, vp]
+    L.mk_paged_tree_attention.argtypes = [vp, vp, vp, i32, vp, i64, vp, i64, vp, f32, i32, vp]
+    L.mk_tree_verify.argtypes = [vp, vp, vp, vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.mk_paged_fork.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, vp, vp]
+    L.mk_paged_copy.argtypes = [vp, vp, vp, i32, vp, i32, vp]
+    L.mk_paged_keep.argtypes = [vp, vp, vp, i32, vp, vp, vp]
     _lib = L
     return L
 
@@ -417,6 +428,23 @@ class _OnDevice:
         with self._guard(self._dev):
             return fn(*args)
 
+    def _call(self, fn, what: str, *args) -> None:
+        """fn(*args) on the tensors' device; what it refuses is raised."""
+        if self._current is None or self._current() == self._dev:
+            rc = fn(*args)
+        else:
+            rc = self._elsewhere(fn, *args)
+        if rc:
+            raise MkError(rc, what)
+
+    def _are(self, dtype, *tensors) -> bool:
+        """Whether all of (tensor or None, elements) are contiguous ones of that kind."""
+        for t, n in tensors:
+            if t is not None and not (t.dtype is dtype and t.get_device() == self._dev and t.numel() == n
+                                      and t.is_contiguous()):
+                return False
+        return True
+
 
 class Rope:
     """Rotary positions (mk_rope).  One axis, or several: `sections` gives the
@@ -482,7 +510,7 @@ class PagedBatch(_OnDevice):
                                 None if slots is None else _ptr(positions),
                                 None if slots is None else _ptr(slots), n, block_table.shape[1],
                                 self.max_tokens, self._max_new, page_size)
-        self._p, self._build = ctypes.addressof(self.c), lib().mk_paged_tables
+        self._p, self._build, self._fork = ctypes.addressof(self.c), lib().mk_paged_tables, lib().mk_paged_fork
         self._rows = (self.max_tokens, self.c, self._p)
 
     @property
@@ -532,6 +560,48 @@ class PagedBatch(_OnDevice):
         if rc:
             raise MkError(rc, "mk_paged_tables")
 
+    def trim(self, lens, keep, next_lens, shared, free_pages, n_free, n_left, copies=None, status=None,
+             stream=None) -> None:
+        """mk_paged_fork in place: request r holds lens[r] tokens and keeps the first
+        keep[r] (0: it ends); pages that nobody holds any more go behind the free
+        ones.  `copies` (int32 [3, n], for PagedLayers.copy) is needed where a cut may
+        end inside a page that others hold.  All int32; shared [n_pages], n_left[0]
+        may be n_free[0]."""
+        n = self.n
+        self._hold(self, None, n, lens, next_lens, copies, shared, free_pages, n_free, n_left, keep, status, stream)
+
+    def fork(self, old: "PagedBatch", parents, lens, next_lens, copies, shared, free_pages, n_free, n_left,
+             keep=None, status=None, stream=None) -> None:
+        """mk_paged_fork: this batch's request i continues request parents[i] of `old`
+        (-1: none; what no request continues ends), which holds lens tokens (cut to
+        keep); fills this batch's block_table and next_lens [n].  Pages filled in part
+        that several continue are copied by PagedLayers.copy(copies), copies int32
+        [3, n].  Other arguments as in trim."""
+        _need(old is not self and old._dev == self._dev and old.page_size == self.page_size
+              and old.block_table.shape[1] == self.block_table.shape[1],
+              "old: another batch on the same device, of the same page size and max_blocks")
+        _need(parents is not None and copies is not None, "fork needs parents and copies")
+        self._hold(old, parents, self.n, lens, next_lens, copies, shared, free_pages, n_free, n_left, keep, status,
+                   stream)
+
+    def _hold(self, old, parents, m, lens, next_lens, copies, shared, free_pages, n_free, n_left, keep, status,
+              stream) -> None:
+        i32, n = self._i32, old.n
+        if not (self._are(i32, (lens, n), (keep, n), (parents, m), (next_lens, m), (shared, shared.numel()),
+                          (free_pages, free_pages.numel()), (n_free, 1), (n_left, 1), (copies, 3 * m), (status, 1))
+                and (copies is None or copies.shape == (3, m))):
+            _tensors(self.device, lens=(lens, i32, (n,)), keep=(keep, i32, (n,)), parents=(parents, i32, (m,)),
+                     next_lens=(next_lens, i32, (m,)), copies=(copies, i32, (3, m)), shared=(shared, i32, None),
+                     free_pages=(free_pages, i32, None), n_free=(n_free, i32, (1,)), n_left=(n_left, i32, (1,)),
+                     status=(status, i32, (1,)))
+        self._call(self._fork, "mk_paged_fork", old.c.block_table, n, lens.data_ptr(),
+                   None if keep is None else keep.data_ptr(), None if parents is None else parents.data_ptr(),
+                   self.c.block_table, next_lens.data_ptr(), m, self.block_table.shape[1], self.page_size,
+                   None if copies is None else copies.data_ptr(), shared.data_ptr(), shared.numel(),
+                   free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(), n_left.data_ptr(),
+                   None if status is None else status.data_ptr(),
+                   self._raw_stream(self._dev) if stream is None else int(stream.cuda_stream))
+
 
 class PagedCache(_OnDevice):
     """One layer's paged cache (mk_paged_cache) over torch tensors k and v
@@ -568,6 +638,7 @@ class PagedCache(_OnDevice):
                                 MK_BF16 if k.dtype == torch.bfloat16 else MK_FP16)
         self._p = ctypes.addressof(self.c)
         self._append, self._attention = lib().mk_paged_append, lib().mk_paged_attention
+        self._tree_attention = lib().mk_paged_tree_attention
         if workspace is not None:
             _need(workspace.device == k.device and workspace.is_contiguous() and
                   workspace.numel() * workspace.element_size() >= MK_PAGED_WORKSPACE_BYTES,
@@ -645,9 +716,10 @@ class PagedCache(_OnDevice):
             raise MkError(rc, "mk_paged_append")
 
     def attention(self, q, batch: PagedBatch, out, lse=None, scale: float = 0.0, window: int = 0,
-                  stream=None) -> None:
+                  stream=None, tree: Optional["DraftTree"] = None) -> None:
         """mk_paged_attention: q, out [rows, n_q_heads, head_dim], lse float32
-        [rows, n_q_heads] or None."""
+        [rows, n_q_heads] or None.  With a `tree` (its masks) mk_paged_tree_attention:
+        new tokens see the cached ones and their ancestors."""
         if self.workspace is None:
             import torch
             # on the call's stream: memory that another one has given back may
@@ -680,12 +752,18 @@ class PagedCache(_OnDevice):
         raw = self._raw_stream(dev) if stream is None else int(stream.cuda_stream)
         if raw not in self._seen:
             self._first_on(stream, raw)
-        args = (self._p, rows[2], q.data_ptr(), qs[0] if n > 1 else hq * d, out.data_ptr(),
+        args = (q.data_ptr(), qs[0] if n > 1 else hq * d, out.data_ptr(),
                 os[0] if n > 1 else hq * d, None if lse is None else lse.data_ptr(), scale, window, raw)
+        if tree is not None:
+            masks = tree.masks
+            _need(masks is not None and masks.shape[0] >= n and tree._dev == dev,
+                  "tree: masks of every row, on the cache's device")
+            self._call(self._tree_attention, "mk_paged_tree_attention", self._p, rows[2], tree._masks, tree._words, *args)
+            return
         if self._current is None or self._current() == dev:
-            rc = self._attention(*args)
+            rc = self._attention(self._p, rows[2], *args)
         else:
-            rc = self._elsewhere(self._attention, *args)
+            rc = self._elsewhere(self._attention, self._p, rows[2], *args)
         if rc:
             raise MkError(rc, "mk_paged_attention")
 
@@ -696,3 +774,130 @@ class PagedCache(_OnDevice):
 
     def reset(self) -> None:
         self._status.zero_()
+
+
+class DraftTree(_OnDevice):
+    """Trees of drafted tokens over a batch's rows (request r's new tokens are the
+    rows cu_new[r] .. cu_new[r + 1), its row 0 the root): parents int32 [rows] (index
+    among the request's new tokens, -1: a root), masks int32 [rows, words] (bit j % 32
+    of word j / 32: the row sees the request's new token j), positions int32 [rows]
+    (the batch's own if not given).  build() makes masks and positions from the
+    parents; masks alone suffice for PagedCache.attention(tree=...), parents alone for
+    verify().  Holds references to them and to the batch."""
+
+    def __init__(self, batch: PagedBatch, parents=None, masks=None, positions=None):
+        _need(parents is not None or masks is not None, "a tree of parents, masks or both is wanted")
+        self._place(batch.device)
+        rows = (masks if parents is None else parents).shape[0]
+        if positions is None:
+            positions = batch.positions
+        _need(masks is None or masks.dim() == 2, "masks: [rows, words]")
+        _tensors(self.device, parents=(parents, self._i32, (rows,)),
+                 masks=(masks, self._i32, None if masks is None else (rows, masks.shape[1])))
+        self.batch, self.parents, self.masks, self.positions, self.rows = batch, parents, masks, positions, rows
+        self._words = 0 if masks is None else masks.shape[1]
+        self._masks = None if masks is None else _ptr(masks)
+        self._parents = None if parents is None else _ptr(parents)
+        self.c = mk_paged_batch.from_buffer_copy(batch.c)
+        self.c.max_tokens = rows
+        self._p = ctypes.addressof(self.c)
+        self._build, self._verify = lib().mk_paged_tree, lib().mk_tree_verify
+
+    def build(self, status=None, stream=None) -> None:
+        """mk_paged_tree: masks and positions from the parents, behind the batch's own
+        build (its offsets and lengths are read).  `status` (int32 [1]) receives
+        MK_ERR_BOUNDS where a parent does not precede its child."""
+        pos = self.positions
+        _need(self.parents is not None and self.masks is not None and pos is not None,
+              "build needs parents, masks and positions")
+        if not self._are(self._i32, (pos, self.rows), (status, 1)):
+            _tensors(self.device, positions=(pos, self._i32, (self.rows,)), status=(status, self._i32, (1,)))
+        self._call(self._build, "mk_paged_tree", self._p, self._parents, self._masks, self._words, pos.data_ptr(),
+                   None if status is None else status.data_ptr(),
+                   self._raw_stream(self._dev) if stream is None else int(stream.cuda_stream))
+
+    def verify(self, tokens, target_probs, uniforms, last_uniforms, path, emitted, kept, lens, draft_probs=None,
+               status=None, stream=None) -> None:
+        """mk_tree_verify: tokens int32 [rows], target_probs and draft_probs float32
+        [rows, vocab] (rows contiguous; draft_probs None: tokens that were found, not
+        drawn), uniforms float32 [rows], last_uniforms [n]; writes path, emitted int32
+        [rows], kept, lens [n]."""
+        i32, f32, rows, n, dev = self._i32, self._f32, self.rows, self.batch.n, self._dev
+        _need(self.parents is not None, "verify needs parents")
+        vocab = target_probs.shape[-1]
+        for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+            if t is not None and not (t.dtype is f32 and t.get_device() == dev and t.shape == (rows, vocab)
+                                      and (vocab < 2 or t.stride(1) == 1)):
+                raise ValueError(f"{name}: float32 [{rows}, vocab] on {self.device}, rows contiguous")
+        if not (self._are(i32, (tokens, rows), (path, rows), (emitted, rows), (kept, n), (lens, n), (status, 1))
+                and self._are(f32, (uniforms, rows), (last_uniforms, n))):
+            _tensors(self.device, tokens=(tokens, i32, (rows,)), path=(path, i32, (rows,)), emitted=(emitted, i32, (rows,)),
+                     kept=(kept, i32, (n,)), lens=(lens, i32, (n,)), status=(status, i32, (1,)),
+                     uniforms=(uniforms, f32, (rows,)), last_uniforms=(last_uniforms, f32, (n,)))
+        if rows == 0:  # empty tensors have no address: every request rests
+            import torch
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                kept.zero_()
+                lens.copy_(self.batch.kv_lens)
+            return
+        one = rows == 1  # the stride of a lone row joins nothing
+        self._call(self._verify, "mk_tree_verify", self._p, self._parents, tokens.data_ptr(), target_probs.data_ptr(),
+                   vocab if one else target_probs.stride(0), None if draft_probs is None else draft_probs.data_ptr(),
+                   0 if draft_probs is None else vocab if one else draft_probs.stride(0), vocab, uniforms.data_ptr(),
+                   last_uniforms.data_ptr(), path.data_ptr(), emitted.data_ptr(), kept.data_ptr(), lens.data_ptr(),
+                   None if status is None else status.data_ptr(),
+                   self._raw_stream(dev) if stream is None else int(stream.cuda_stream))
+
+
+class PagedLayers(_OnDevice):
+    """The caches of a model's layers, of one shape, for what moves tokens in all of
+    them with one launch.  What is out of range is latched in the first one's status
+    word.  Holds references to the caches."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        _need(1 <= len(caches) <= MK_PAGED_MAX_LAYERS, "1 to MK_PAGED_MAX_LAYERS caches")
+        first = caches[0]
+        self._place(first.device)
+        for c in caches:
+            _need(c.device == first.device and c.dtype == first.dtype and c.k.shape == first.k.shape
+                  and c.k.stride() == first.k.stride(), "caches of one shape, type and device")
+        self.caches, self.n = caches, len(caches)
+        row = ctypes.c_void_p * self.n
+        self._ks, self._vs = row(*[_ptr(c.k) for c in caches]), row(*[_ptr(c.v) for c in caches])
+        self._copy, self._keep = lib().mk_paged_copy, lib().mk_paged_keep
+
+    def _stream(self, stream) -> int:
+        first = self.caches[0]
+        raw = self._raw_stream(self._dev) if stream is None else int(stream.cuda_stream)
+        if raw not in first._seen:
+            first._first_on(stream, raw)
+        return raw
+
+    def copy(self, copies, stream=None) -> None:
+        """mk_paged_copy: for every i the first copies[2, i] tokens of page copies[0, i]
+        to page copies[1, i] (source -1: none); copies int32 [3, n]."""
+        n = copies.shape[1] if copies.dim() == 2 else 0
+        if not (copies.shape == (3, n) and self._are(self._i32, (copies, 3 * n))):
+            _need(copies.dim() == 2, "copies: [3, n]")
+            _tensors(self.device, copies=(copies, self._i32, (3, n)))
+        if n == 0:
+            return
+        self._call(self._copy, "mk_paged_copy", self.caches[0]._p, self._ks, self._vs, self.n, copies.data_ptr(), n,
+                   self._stream(stream))
+
+    def keep(self, batch: PagedBatch, path, stream=None) -> None:
+        """mk_paged_keep: the tokens that DraftTree.verify's path names move to the front
+        of their request's rows (batch.slots says where they lie)."""
+        n = path.numel()
+        _need(batch.slots is not None and batch._dev == self._dev, "batch: with slots, on the caches' device")
+        _need(n <= batch.max_tokens, "path: no more rows than the batch has slots")
+        if not self._are(self._i32, (path, n)):
+            _tensors(self.device, path=(path, self._i32, (n,)))
+        if n == 0:
+            return
+        rows = batch._rows  # held here until the call returns
+        if rows[0] != n:
+            rows = batch._of_rows(n)
+        self._call(self._keep, "mk_paged_keep", self.caches[0]._p, self._ks, self._vs, self.n, rows[2], path.data_ptr(),
+                   self._stream(stream))
