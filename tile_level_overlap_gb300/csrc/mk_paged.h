@@ -142,6 +142,7 @@ cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const 
                              bool bf, cudaStream_t st);
 cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
                                bool bf, cudaStream_t st);
+cudaError_t paged_join_tiles_launch(const PagedAttnParams& p, const PagedParts& b, int d, bool bf, cudaStream_t st);
 cudaError_t paged_join_launch(const PagedAttnParams& p, const PagedParts& a, const PagedParts& b, int d,
                               bool bf, cudaStream_t st);
 

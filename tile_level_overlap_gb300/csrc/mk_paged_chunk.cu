@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   const bool split_v = P.page_shift < PC_SPLIT_V;
 
   grid_launch_dependents();
+  if (TREE && tid >= 32 && tid < 35)  // (their first use would wait for them)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tid == 32 ? &tk : tid == 33 ? &tv : &tq) : "memory");
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
@@ -554,9 +556,23 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (key0 < all_lo || key0 + 128 > all_hi) {
           const int c0 = first - key0, width = last + 1 - first;  // visible columns [c0, c0 + width)
           const uint32_t w = width > 0 ? (uint32_t)width : 0u;
+          if constexpr (TREE) {
+            const int c1 = width > 0 ? c0 + width : c0;
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if ((uint32_t)(i - c0) >= w && !(TREE && (named[i >> 5] >> (i & 31) & 1u))) s[i] = -INFINITY;
+            for (int q = 0; q < 4; ++q) {
+              // bits [c0 - 32 q, c1 - 32 q) of a word, and the named ones
+              const int b0 = min(max(c0 - 32 * q, 0), 32), b1 = min(max(c1 - 32 * q, 0), 32);
+              const uint32_t keep = ((uint32_t)((1ull << b1) - 1) & ~(uint32_t)((1ull << b0) - 1)) | named[q];
+              if (__any_sync(0xffffffffu, keep != 0xffffffffu)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[32 * q + i] = keep >> i & 1u ? s[32 * q + i] : -INFINITY;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if ((uint32_t)(i - c0) >= w) s[i] = -INFINITY;
+          }
         }
         float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
 #pragma unroll
@@ -608,14 +624,29 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (key0 < m.lo || key0 + 128 > m.hi) {
           const uint32_t vst = (2 * blkn) % ST + 1;
           wait_phase(&full[vst], ((2 * blkn) / ST) & 1, dead, P.status);
-          const int key = key0 + row;  // rows of 128 threads
-          if (key < m.lo || key >= m.hi) {
-            uint8_t* v = smem + C::o_kv + vst * C::TILE + row * 128;
+          uint8_t* v = smem + C::o_kv + vst * C::TILE;
+          if constexpr (TREE) {
+            // (pages that no row sees have arrived as zeros: what is hidden of those
+            // that a row sees, 16 bytes after 16)
+            const int boxt = min(128, 1 << P.page_shift);
+            const int h0 = max(0, (m.lo & ~(boxt - 1)) - key0), h1 = m.lo - key0;              // before the first seen key
+            const int t0 = m.hi - key0, t1 = min(128, ((m.hi + boxt - 1) & ~(boxt - 1)) - key0);  // behind the last
+            auto clear = [&](int a, int b) {
+              for (int i = a * 8 + row; i < b * 8; i += 128)
 #pragma unroll
-            for (int x = 0; x < HD / 64; ++x)
+                for (int x = 0; x < HD / 64; ++x) *reinterpret_cast<uint4*>(v + x * 16384 + 16 * i) = make_uint4(0, 0, 0, 0);
+            };
+            clear(h0, min(h1, 128));
+            clear(max(t0, 0), t1);
+          } else {
+            const int key = key0 + row;  // rows of 128 threads
+            if (key < m.lo || key >= m.hi) {
+              uint8_t* r = v + row * 128;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(v + x * 16384 + 16 * i) = make_uint4(0, 0, 0, 0);
+              for (int x = 0; x < HD / 64; ++x)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(r + x * 16384 + 16 * i) = make_uint4(0, 0, 0, 0);
+            }
           }
           fence_proxy_async_smem();
         }
@@ -687,6 +718,139 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   }
 }
 
+// ---------------------------------------------------------------- join
+// The tile kernel's parts of trees, where no few-row kernel precedes it: 32 rows of
+// a tile at a time, lanes on the rows, warps on the dimensions; the items of all
+// tiles end to end.  Latency bound: what counts is that all loads of an item are in
+// flight at once and that the items go round few times.  With few of them (a lone
+// request: 8 tiles of 19 parts) an item is 32 dimensions of which the block's two
+// teams take every other part; with many (two parts each, mostly) a team takes all
+// dimensions of an item of its own.  32 requests of 40 to 64 rows over 0.5-2K keys
+// TIMES.
+constexpr int JT_THREADS = 512, JT_TEAM = JT_THREADS / 2;
+
+// A team's warp `quad` joins parts first, first + step, .. of 32 rows (one a lane), Q
+// groups of four dimensions, AHEAD parts in flight.
+template <int HD, int Q, int AHEAD>
+__device__ __forceinline__ void join_parts(const PagedParts& B, int c, int parts, int row, int quad, int first, int step,
+                                           float* m_out, float* l_out, float4 (&o)[Q]) {
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = first; k0 < parts; k0 += step * AHEAD) {
+    float2 ml[AHEAD];
+    float4 v[AHEAD][Q];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int k = k0 + step * i;
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (k < parts) {
+        const int64_t part = k == 0 ? 2 * c + 1 : 2 * (c + k);
+        ml[i] = __ldcg(B.ml + part * B.rt + row);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          v[i][q] = __ldcg(reinterpret_cast<const float4*>(B.o + part * B.rt * HD + ((int64_t)(quad + q) * B.rt + row) * 4));
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) mn = fmaxf(mn, ml[i].x);
+    const float ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref);
+    l *= a;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) { o[q].x *= a; o[q].y *= a; o[q].z *= a; o[q].w *= a; }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (k0 + step * i < parts) {
+        const float f = ex2(ml[i].x - ref);
+        l += ml[i].y * f;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          o[q].x += v[i][q].x * f; o[q].y += v[i][q].y * f; o[q].z += v[i][q].z * f; o[q].w += v[i][q].w * f;
+        }
+      }
+    }
+    m = mn;
+  }
+  *m_out = m;
+  *l_out = l;
+}
+
+template <int HD, bool BF>
+__global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const __grid_constant__ PagedAttnParams P, const __grid_constant__ PagedParts B) {
+  constexpr int DG = HD / 32, Q = DG;
+  __shared__ int upto[225], tmp[JT_THREADS / 32];
+  __shared__ float other[8][4][33];
+  __shared__ float2 other_ml[32];
+  __shared__ uint2 rows_out[2][32][HD / 4 + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = warp >> 3, quad = warp & 7;
+  grid_launch_dependents();
+  grid_wait_prior();
+  PartDesc d{};
+  if (tid < B.ctas) d = B.desc[tid];
+  int total;  // items of all dimensions
+  bool any;
+  const uint32_t at = block_scan<JT_THREADS / 32>(d.parts ? (uint32_t)(d.rows + 31) / 32 : 0u, false, tmp, &total, &any);
+  if (tid <= B.ctas) upto[tid] = (int)at;
+  __syncthreads();
+  auto put_lse = [&](const PartDesc& t, int row, float m, float l) {
+    if (!P.lse || row >= t.rows) return;
+    const int tk = P.token_of(row);
+    P.lse[(int64_t)(t.row0 + tk) * (P.hkv * P.rep) + t.head * P.rep + row - tk * P.rep] = lse_of(m, l);
+  };
+  // a team's rows to memory, `pieces` of 8 bytes each
+  auto put_rows = [&](const PartDesc& t, int row0, int d0, int pieces) {
+    for (int i = tid & (JT_TEAM - 1); i < 32 * pieces; i += JT_TEAM) {
+      const int rw = row0 + i / pieces, q = i % pieces;
+      if (rw >= t.rows) break;
+      const int tk = P.token_of(rw);
+      *reinterpret_cast<uint2*>(P.out + (int64_t)(t.row0 + tk) * P.o_stride + (int64_t)(t.head * P.rep + rw - tk * P.rep) * HD + d0 + q * 4) =
+          rows_out[team][i / pieces][q];
+    }
+  };
+  if (total * DG > 2 * (int)gridDim.x) {
+    for (int item = 2 * blockIdx.x + team; item < total; item += 2 * gridDim.x) {
+      const int c = find_le(upto, B.ctas, item), row0 = (item - upto[c]) * 32;
+      const PartDesc t = B.desc[c];
+      float m, l;
+      float4 o[Q];
+      join_parts<HD, Q, 2>(B, c, t.parts, row0 + lane, quad * Q, 0, 1, &m, &l, o);
+      const float inv = inv_of(l);
+      named_bar(1 + team, JT_TEAM);  // the previous rows have been written
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        rows_out[team][lane][quad * Q + q] = make_uint2(down2<BF>(o[q].x * inv, o[q].y * inv), down2<BF>(o[q].z * inv, o[q].w * inv));
+      if (quad == 0) put_lse(t, row0 + lane, m, l);
+      named_bar(1 + team, JT_TEAM);
+      put_rows(t, row0, 0, HD / 4);
+    }
+    return;
+  }
+  for (int item = blockIdx.x; item < total * DG; item += gridDim.x) {
+    const int c = find_le(upto, B.ctas, item / DG), row0 = (item / DG - upto[c]) * 32, d0 = item % DG * 32;
+    const PartDesc t = B.desc[c];
+    float m, l;
+    float4 o[1];
+    join_parts<HD, 1, 5>(B, c, t.parts, row0 + lane, d0 / 4 + quad, team, 2, &m, &l, o);
+    if (team) {
+      other[quad][0][lane] = o[0].x; other[quad][1][lane] = o[0].y; other[quad][2][lane] = o[0].z; other[quad][3][lane] = o[0].w;
+      if (quad == 0) other_ml[lane] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (!team) {
+      const float2 y = other_ml[lane];
+      const float mn = fmaxf(m, y.x), ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref), f = ex2(y.x - ref);
+      l = l * a + y.y * f;
+      const float inv = inv_of(l);
+      rows_out[0][lane][quad] = make_uint2(down2<BF>((o[0].x * a + other[quad][0][lane] * f) * inv, (o[0].y * a + other[quad][1][lane] * f) * inv),
+                                           down2<BF>((o[0].z * a + other[quad][2][lane] * f) * inv, (o[0].w * a + other[quad][3][lane] * f) * inv));
+      if (quad == 0 && d0 == 0) put_lse(t, row0 + lane, mn, l);
+    }
+    __syncthreads();
+    if (!team) put_rows(t, row0, d0, 8);
+  }
+}
+
 template <int HD, bool BF, bool TREE>
 cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
   CUtensorMap tq, tk, tv;
@@ -700,7 +864,7 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
   if (e != cudaSuccess) return e;
   // behind the few-row kernel it is set up while that one ends; alone it is launched
   // behind the whole of what precedes (8192-token prompt 363 against 368 us)
-  return paged_launch_if(p.few_rows > 0, paged_chunk_kernel<HD, BF, TREE>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
+  return paged_launch_if(TREE || p.few_rows > 0, paged_chunk_kernel<HD, BF, TREE>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
                          tq, tk, tv, p, w);
 }
 
@@ -714,6 +878,15 @@ cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, cons
   }
   if (d == 128) return bf ? launch<128, true, false>(p, kv, w, st) : launch<128, false, false>(p, kv, w, st);
   return bf ? launch<64, true, false>(p, kv, w, st) : launch<64, false, false>(p, kv, w, st);
+}
+
+cudaError_t paged_join_tiles_launch(const PagedAttnParams& p, const PagedParts& b, int d, bool bf, cudaStream_t st) {
+  const int grid = 2 * b.ctas;
+  if (d == 128)
+    return bf ? paged_launch(paged_join_tiles_kernel<128, true>, grid, JT_THREADS, 0, st, p, b)
+              : paged_launch(paged_join_tiles_kernel<128, false>, grid, JT_THREADS, 0, st, p, b);
+  return bf ? paged_launch(paged_join_tiles_kernel<64, true>, grid, JT_THREADS, 0, st, p, b)
+            : paged_launch(paged_join_tiles_kernel<64, false>, grid, JT_THREADS, 0, st, p, b);
 }
 
 }  // namespace mk
