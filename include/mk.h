@@ -622,8 +622,8 @@ int mk_paged_tree_attention(const mk_paged_cache *cache, const mk_paged_batch *b
  * lens kv_lens, path and emitted -1.  A token outside the vocabulary never stands,
  * a parent that is not before its child has no such child; both are latched.  A
  * target row without mass where the last token is drawn: the token 0, latched.
- * Sums are exact to 2^-62 (whole numbers), so that equal calls, and equal requests
- * in any batch, give equal tokens.  vocab 1 .. 2^24.  What is written may overlap
+ * Sums are of whole numbers (each value rounded to 2^-43), so that equal calls, and
+ * equal requests in any batch, give equal tokens.  vocab 1 .. 2^24.  What is written may overlap
  * nothing else of the call; *status may be the cache's. */
 int mk_tree_verify(const mk_paged_batch *batch, const int32_t *parents, const int32_t *tokens,
                    const float *target_probs, int64_t target_stride, const float *draft_probs,

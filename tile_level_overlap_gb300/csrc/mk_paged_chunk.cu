@@ -725,8 +725,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
 // flight at once and that the items go round few times.  With few of them (a lone
 // request: 8 tiles of 19 parts) an item is 32 dimensions of which the block's two
 // teams take every other part; with many (two parts each, mostly) a team takes all
-// dimensions of an item of its own.  32 requests of 40 to 64 rows over 0.5-2K keys
-// TIMES.
+// dimensions of an item of its own.  (a lone request of 32 tokens over 4096 keys
+// 30.7 -> 17.3 us by this and the spared launch).
 constexpr int JT_THREADS = 512, JT_TEAM = JT_THREADS / 2;
 
 // A team's warp `quad` joins parts first, first + step, .. of 32 rows (one a lane), Q

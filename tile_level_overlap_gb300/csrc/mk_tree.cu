@@ -76,11 +76,15 @@ __global__ void __launch_bounds__(TT_THREADS) paged_tree_kernel(const TreeParams
 // max(p - S q, 0) with S the sum of the Z so far (max(max(a, 0) - b, 0) =
 // max(a - b, 0)), so that a pass reads the two rows and keeps nothing.
 //
-// Probabilities are summed as whole numbers in units of 2^-62: the order of a sum
-// does not matter, the place where the sum passes u Z is the same whatever the
-// cluster, and 100000 values lose nothing that 64-bit floats would keep.  Bound by
-// latency for few requests, by HBM (the rows that are drawn from) for many.
-constexpr int TV_THREADS = 512, TV_WARPS = TV_THREADS / 32, TV_CLUSTER = 8;
+// Probabilities are summed as whole numbers in units of 2^-43, each rounded once: the
+// order of a sum does not matter, so the token is the same whatever the cluster, and a
+// sum of 150000 is off by 2^-36 (32-bit floats would be off by 2^-24 at each of the
+// places between two tokens).  x = hi 2^-22 + lo comes from adding 3: the bits of x + 3
+// are hi, the rest is exact and gets its bits in the same way; six instructions, of
+// which none is 64 bits wide.  p - S q has its parts subtracted, with the product's
+// rounding error from a second multiply-add.  Bound by latency for few requests, by
+// HBM (the rows that are drawn from) and these instructions for many.
+constexpr int TV_THREADS = 512, TV_WARPS = TV_THREADS / 32;
 
 struct VerifyParams {
   const int32_t *cu, *kv, *parents, *tokens;
@@ -92,31 +96,64 @@ struct VerifyParams {
 
 __device__ __forceinline__ float probability(float x) { return fminf(fmaxf(x, 0.f), 1.f); }  // NaN: 0
 
-// x in [0, 1] in units of 2^-62, rounded down.
-__device__ __forceinline__ u64 units(float x) {
+// x in [0, 1) as a fraction of 2^64, rounded down.
+__device__ __forceinline__ u64 fraction(float x) {
   const uint32_t b = __float_as_uint(x);
-  const int sh = (int)(b >> 23) - 88;
+  const int sh = (int)(b >> 23) - 86;
   const u64 m = (b & 0x7fffffu) | 0x800000u;
   return sh >= 0 ? m << sh : sh > -24 ? m >> -sh : 0;
 }
 
-// S (units of 2^-53) times q, in units of 2^-62; what passes 2 becomes 2.
-constexpr u64 ONE_S = 1ull << 53;
-__device__ __forceinline__ u64 times(u64 S, u64 q) {
-  if (S == ONE_S) return q;
-  const u64 hi = __umul64hi(S, q), lo = S * q;
-  return hi >= (1ull << 52) ? 1ull << 63 : (hi << 11) | (lo >> 53);
+// S, what the draft's row is multiplied by: none (0), 1, or hi + lo.
+struct Refusals {
+  float hi, lo;
+  __device__ __forceinline__ Refusals(double s) : hi((float)s), lo((float)(s - (double)(float)s)) {}
+};
+// Sum of whole numbers: hi in units of 2^-22, lo of 2^-43 (some 250 values of up to
+// 1 before it has to be taken out).
+constexpr float HI_AT = 3.f, LO_AT = 0x1.8p-20f;
+struct Units {
+  int hi = 0, lo = 0;
+  __device__ __forceinline__ void add(float x) {  // x in [0, 1]
+    const float t = x + HI_AT, y = (x - (t - HI_AT)) + LO_AT;
+    hi += __float_as_int(t) - __float_as_int(HI_AT);
+    lo += __float_as_int(y) - __float_as_int(LO_AT);
+  }
+  // max(p - S q, 0)
+  template <bool ONE>
+  __device__ __forceinline__ void add(float p, float q, const Refusals& S) {
+    float x = q, err = 0.f;
+    if constexpr (!ONE) {
+      x = S.hi * q;
+      err = fmaf(S.lo, q, fmaf(S.hi, q, -x));
+      x = fminf(x, 2.f);  // over any p all the same
+    }
+    const float tp = p + HI_AT, tx = x + HI_AT;
+    const float lo_part = (p - (tp - HI_AT)) - (x - (tx - HI_AT)) - err;
+    if ((tp - tx) + lo_part > 0.f) {
+      hi += __float_as_int(tp) - __float_as_int(tx);
+      lo += __float_as_int(lo_part + LO_AT) - __float_as_int(LO_AT);
+    }
+  }
+  __device__ __forceinline__ u64 value() const { return (u64)(((int64_t)hi << 21) + lo); }
+};
+__device__ __forceinline__ u64 units(float x) {
+  Units a;
+  a.add(x);
+  return a.value();
 }
-__device__ __forceinline__ u64 rest(float p, float q, u64 S) {
-  const u64 a = units(probability(p));
-  if (S == 0) return a;
-  const u64 b = times(S, units(probability(q)));
-  return a > b ? a - b : 0;
+__device__ __forceinline__ u64 rest_units(float p, float q, double S) {
+  Units a;
+  if (S == 0.0) a.add(probability(p));
+  else if (S == 1.0) a.add<true>(probability(p), probability(q), Refusals(S));
+  else a.add<false>(probability(p), probability(q), Refusals(S));
+  return a.value();
 }
 
 struct VerifyCtl {  // what the first CTA asks of the others
-  int cur, depth, last, refused;  // last: the pass that draws the last token
-  u64 S;
+  int row, last, refused;  // last: 1 the pass that draws the last token, 2 nothing to draw
+  int emitted;             // row that receives it
+  double S;
 };
 
 struct VerifySmem {
@@ -151,20 +188,74 @@ __device__ __forceinline__ float4 load4(const float* row, int v, int vocab, bool
   return x;
 }
 
-__global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const VerifyParams P) {
+// A warp's sum of the rest over the vectors [v, v1), lanes side by side, U vectors of
+// each row in flight a lane.
+enum { REST_P, REST_ONE, REST_S };
+template <int U, int KIND>
+__device__ __forceinline__ u64 sum_rest(const float* rp, const float* rq, double s, int v, int v1, int vocab, bool wide) {
+  const Refusals S(s);
+  u64 sum = 0;
+  for (v += threadIdx.x & 31; v < v1; v += 32 * U) {
+    float4 a[U], b[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (v + 32 * i < v1) {
+        a[i] = load4(rp, v + 32 * i, vocab, wide);
+        if (KIND != REST_P) b[i] = load4(rq, v + 32 * i, vocab, wide);
+      }
+    }
+    Units x;
+    auto one = [&](float p, float q) {
+      if constexpr (KIND == REST_P) x.add(probability(p));
+      else x.template add<KIND == REST_ONE>(probability(p), probability(q), S);
+    };
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      one(a[i].x, b[i].x);
+      one(a[i].y, b[i].y);
+      one(a[i].z, b[i].z);
+      one(a[i].w, b[i].w);
+    }
+    sum += x.value();
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// Of n <= 32 sums in the lanes, the first whose running sum passes *want; *want becomes
+// what is left of it there, *all their sum.
+__device__ __forceinline__ int find_sum(u64 mine, int n, int lane, u64* want) {
+  u64 upto = lane < n ? mine : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const uint32_t m = __ballot_sync(0xffffffffu, lane < n && upto > *want);
+  const int at = m ? __ffs(m) - 1 : n - 1;
+  const u64 before = __shfl_sync(0xffffffffu, upto - mine, at);
+  *want -= before;
+  return at;
+}
+
+__global__ void __launch_bounds__(TV_THREADS, 1) tree_verify_kernel(const VerifyParams P) {
   __shared__ VerifySmem S;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = cluster_rank(), ctas = cluster_size(), r = blockIdx.x / ctas;
   grid_launch_dependents();
   grid_wait_prior();
+  float ul = P.u_last[r];
+  ul = ul >= 1.f ? 0x1.fffffep-1f : fmaxf(ul, 0.f);
   // state of the walk, in the first CTA's first warp
-  int k = 0, c0 = 0, cur = 0, depth = 0, at = 0, n_gone = 0;
-  u64 sum_z = 0;
-  double z = 1.0;
+  int k = 0, c0 = 0, kv = 0, cur = 0, depth = 0, at = 0, n_gone = 0;
+  double sum_z = 0.0, z = 1.0;
   bool none = false;  // nothing to draw from: this request gets no token
   if (rank == 0) {
     c0 = P.cu[r];
-    const int c1 = P.cu[r + 1], kv = P.kv[r];
+    const int c1 = P.cu[r + 1];
+    kv = P.kv[r];
     k = c1 - c0;
     const bool below = begins_below(P.cu, r, c0), bad = below || c0 < 0 || c1 < c0 || c1 > P.rows || k > MK_TREE_MAX_NODES;
     none = bad || k == 0 || kv < k;
@@ -208,14 +299,10 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const VerifyPar
     if (rank == 0 && warp == 0) {
       while (at < k) {
         const int i = at, x = S.tok[i];
-        bool again = false;
-        u64 left = 0;
-        bool stands;
+        bool again = false, stands;
         if (P.q) {
-          left = rest(S.p[i], S.q[i], sum_z);
-          // the first child's comparison is of the probabilities themselves
-          const double mine = sum_z == 0 ? (double)S.p[i] : (double)left * 0x1p-62;
-          stands = (double)S.u[i] * (double)S.q[i] * z < mine;
+          const double left = fmax((double)S.p[i] - sum_z * (double)S.q[i], 0.0);
+          stands = (double)S.u[i] * (double)S.q[i] * z < left;
         } else {
           for (int b = 0; b < n_gone; b += 32)
             again |= __any_sync(0xffffffffu, b + lane < n_gone && S.gone[min(b + lane, n_gone - 1)] == x);
@@ -226,14 +313,14 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const VerifyPar
           ++depth;
           if (lane == 0) S.path[depth] = i;
           at = next_child(S.up, k, cur, i + 1, lane);
-          sum_z = 0;
+          sum_z = 0.0;
           z = 1.0;
           n_gone = 0;
           continue;
         }
         at = next_child(S.up, k, cur, i + 1, lane);
         if (P.q) {
-          sum_z += sum_z == 0 ? ONE_S : (u64)(z * 0x1p53);
+          sum_z += z;
           if (at < k) break;  // its siblings are asked against the rest's sum
         } else if (!again && x >= 0) {
           if (lane == 0) {
@@ -245,99 +332,88 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const VerifyPar
           __syncwarp();
         }
       }
-      if (lane == 0) S.ctl = {cur, depth, none ? 2 : at >= k, n_gone, sum_z};
+      if (lane == 0) S.ctl = {c0 + cur, none ? 2 : at >= k, n_gone, c0 + depth, sum_z};
     }
     cluster_sync();
     VerifyCtl c;
-    c.cur = ld_cluster32(ctl0);
-    c.depth = ld_cluster32(ctl0 + 4);
-    c.last = ld_cluster32(ctl0 + 8);
-    c.refused = ld_cluster32(ctl0 + 12);
-    c.S = ld_cluster64(ctl0 + 16);
+    c.row = ld_cluster32(ctl0);
+    c.last = ld_cluster32(ctl0 + 4);
+    c.refused = ld_cluster32(ctl0 + 8);
+    c.emitted = ld_cluster32(ctl0 + 12);
+    c.S = __longlong_as_double((long long)ld_cluster64(ctl0 + 16));
     if (c.last == 2) break;
-    if (rank != 0) c0 = P.cu[r];
-    const float* rp = P.p + (c0 + c.cur) * P.p_stride;
-    const float* rq = P.q ? P.q + (c0 + c.cur) * P.q_stride : rp;
+    const float* rp = P.p + c.row * P.p_stride;
+    const float* rq = P.q ? P.q + c.row * P.q_stride : rp;
     const bool wide = ((uintptr_t)rp & 15) == 0 && ((uintptr_t)rq & 15) == 0;
 
     // sum of the rest over this CTA's share (a second time without refusals where
     // nothing of it is left)
-    u64 total = 0;
+    u64 total = 0, cta_total = 0;
     for (int pass = 0; pass < 2; ++pass) {
-      u64 sum = 0;
-      const int v1 = warp_first(warp + 1);
-      if (c.S != 0) {
-#pragma unroll 4
-        for (int v = warp_first(warp) + lane; v < v1; v += 32) {
-          const float4 a = load4(rp, v, P.vocab, wide), b = load4(rq, v, P.vocab, wide);
-          sum += rest(a.x, b.x, c.S) + rest(a.y, b.y, c.S) + rest(a.z, b.z, c.S) + rest(a.w, b.w, c.S);
-        }
-      } else {
-#pragma unroll 4
-        for (int v = warp_first(warp) + lane; v < v1; v += 32) {
-          const float4 a = load4(rp, v, P.vocab, wide);
-          sum += units(probability(a.x)) + units(probability(a.y)) + units(probability(a.z)) + units(probability(a.w));
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const int v0 = warp_first(warp), v1 = warp_first(warp + 1);
+      const u64 sum = c.S == 0.0   ? sum_rest<8, REST_P>(rp, rq, 0.0, v0, v1, P.vocab, wide)
+                      : c.S == 1.0 ? sum_rest<4, REST_ONE>(rp, rq, 1.0, v0, v1, P.vocab, wide)
+                                   : sum_rest<4, REST_S>(rp, rq, c.S, v0, v1, P.vocab, wide);
       if (lane == 0) S.warp_sum[warp] = sum;
       __syncthreads();
-      // without what was refused
-      for (int g = tid; g < c.refused; g += TV_THREADS) {
-        const int v = (int)ld_cluster32(cluster_addr(&S.gone[g], 0)) / 4;
-        if (v / per_cta == rank)
-          atomicAdd(&S.warp_sum[(v - rank * per_cta) / per_warp], 0ull - ld_cluster64(cluster_addr(&S.gone_units[g], 0)));
+      if (c.refused > 0) {  // without what was refused
+        for (int g = tid; g < c.refused; g += TV_THREADS) {
+          const int v = (int)ld_cluster32(cluster_addr(&S.gone[g], 0)) / 4;
+          if (v / per_cta == rank)
+            atomicAdd(&S.warp_sum[(v - rank * per_cta) / per_warp], 0ull - ld_cluster64(cluster_addr(&S.gone_units[g], 0)));
+        }
+        __syncthreads();
       }
-      __syncthreads();
-      if (tid == 0) {
-        u64 t = 0;
-        for (int w = 0; w < TV_WARPS; ++w) t += S.warp_sum[w];
-        S.total = t;
+      if (warp == 0) {
+        u64 t = lane < TV_WARPS ? S.warp_sum[lane] : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (lane == 0) S.total = t;
+      }
+      if (pass == 0 && c.last && rank == 0) {  // meanwhile, what the walk has found
+        for (int j = tid; j < k; j += TV_THREADS) {
+          const int d = c.emitted - c0;
+          P.path[c0 + j] = j == 0 ? 0 : j <= d ? S.path[j] : -1;
+          if (j != d) P.emitted[c0 + j] = j < d ? S.tok[S.path[j + 1]] : -1;
+        }
+        if (tid == 0) {
+          P.kept[r] = c.emitted - c0 + 1;
+          P.lens[r] = kv - k + c.emitted - c0 + 1;
+        }
       }
       cluster_sync();
-      total = 0;
-      for (int x = 0; x < ctas; ++x) total += ld_cluster64(cluster_addr(&S.total, x));
+      cta_total = lane < ctas ? ld_cluster64(cluster_addr(&S.total, lane)) : 0;
+      total = cta_total;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
       if (!c.last || total != 0 || pass == 1) break;
-      c.S = 0;
+      c.S = 0.0;
       c.refused = 0;
       cluster_sync();  // the totals have been read
     }
     if (!c.last) {
-      z = (double)total * 0x1p-62;
+      z = (double)total * 0x1p-43;
       continue;
     }
     // the last token: the element where the running sum passes u total
-    float ul = P.u_last[r];
-    ul = ul >= 1.f ? 0x1.fffffep-1f : fmaxf(ul, 0.f);
-    u64 want = __umul64hi(total, units(ul) << 2);
-    int owner = 0;
-    for (; owner < ctas - 1; ++owner) {
-      const u64 t = ld_cluster64(cluster_addr(&S.total, owner));
-      if (want < t) break;
-      want -= t;
-    }
-    int32_t* last = P.emitted + c0 + c.depth;
+    u64 want = __umul64hi(total, fraction(ul));
+    const int owner = find_sum(cta_total, ctas, lane, &want);
+    int32_t* last = P.emitted + c.emitted;
     if (total == 0) {
       if (rank == 0 && tid == 0) {
         latch(P.status, MK_ERR_BOUNDS);
         *last = 0;
       }
     } else if (owner == rank) {
-      int w = 0;
-      for (; w < TV_WARPS - 1; ++w) {
-        const u64 t = S.warp_sum[w];
-        if (want < t) break;
-        want -= t;
-      }
+      const int w = find_sum(lane < TV_WARPS ? S.warp_sum[lane] : 0, TV_WARPS, lane, &want);
       const int v0 = warp_first(w), v1 = warp_first(w + 1);
       bool found = false;
       for (int b = v0; b < v1 && !found; b += TV_THREADS) {
         const int v = b + tid;
         u64 x[4] = {0, 0, 0, 0};
         if (v < v1) {
-          const float4 a = load4(rp, v, P.vocab, wide), q = c.S ? load4(rq, v, P.vocab, wide) : a;
-          x[0] = rest(a.x, q.x, c.S); x[1] = rest(a.y, q.y, c.S); x[2] = rest(a.z, q.z, c.S); x[3] = rest(a.w, q.w, c.S);
+          const float4 a = load4(rp, v, P.vocab, wide), q = c.S != 0.0 ? load4(rq, v, P.vocab, wide) : a;
+          x[0] = rest_units(a.x, q.x, c.S); x[1] = rest_units(a.y, q.y, c.S); x[2] = rest_units(a.z, q.z, c.S); x[3] = rest_units(a.w, q.w, c.S);
           for (int g = 0; g < c.refused; ++g) {
             const int t = (int)ld_cluster32(cluster_addr(&S.gone[g], 0));
             if (t / 4 == v) {
@@ -374,19 +450,21 @@ __global__ void __launch_bounds__(TV_THREADS) tree_verify_kernel(const VerifyPar
       // (sums that pass 2^64, of rows that are no probabilities, may miss it)
       if (!found && tid == 0) *last = min(max(4 * v1 - 1, 0), P.vocab - 1);
     }
-    if (rank == 0) {
-      for (int j = tid; j < k; j += TV_THREADS) {
-        P.path[c0 + j] = j == 0 ? 0 : j <= c.depth ? S.path[j] : -1;
-        if (j != c.depth) P.emitted[c0 + j] = j < c.depth ? S.tok[S.path[j + 1]] : -1;
-      }
-      if (tid == 0) {
-        P.kept[r] = c.depth + 1;
-        P.lens[r] = P.kv[r] - k + c.depth + 1;
-      }
-    }
     break;
   }
   cluster_sync();  // no CTA's shared memory is read any more
+}
+
+// CTAs of a request: as many as fill the GPU once, 16 at most.
+// (A cluster of 16 is more than every GPU has to take: the device is asked once.)
+cudaError_t verify_launch(const VerifyParams& p, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  int cluster = 8;
+  while (cluster > 1 && p.n * cluster > sms) cluster /= 2;
+  return paged_launch_clusters(tree_verify_kernel, p.n * cluster, cluster, TV_THREADS, 0, st, p);
 }
 
 }  // namespace
@@ -441,5 +519,5 @@ extern "C" int mk_tree_verify(const mk_paged_batch* b, const int32_t* parents, c
   p.path = path; p.emitted = emitted; p.kept = kept; p.lens = lens; p.status = status;
   p.p_stride = target_stride; p.q_stride = draft_stride;
   p.n = b->n; p.rows = b->max_tokens; p.vocab = vocab;
-  return paged_done(paged_launch_clusters(tree_verify_kernel, p.n * TV_CLUSTER, TV_CLUSTER, TV_THREADS, 0, (cudaStream_t)stream, p));
+  return paged_done(verify_launch(p, (cudaStream_t)stream));
 }
