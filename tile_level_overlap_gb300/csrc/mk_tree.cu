@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(TT_THREADS) paged_tree_kernel(const TreeParams
 // which none is 64 bits wide.  p - S q has its parts subtracted, with the product's
 // rounding error from a second multiply-add.  Bound by latency for few requests, by
 // HBM (the rows that are drawn from) and these instructions for many.
-constexpr int TV_THREADS = 512, TV_WARPS = TV_THREADS / 32;
+constexpr int TV_THREADS = 256, TV_WARPS = TV_THREADS / 32;
+constexpr int TV_U = 4, TV_BATCH = 64 * TV_U;  // vectors in flight a lane and row (of one row twice as many)
 
 struct VerifyParams {
   const int32_t *cu, *kv, *parents, *tokens;
@@ -94,7 +95,7 @@ struct VerifyParams {
   int n, rows, vocab;
 };
 
-__device__ __forceinline__ float probability(float x) { return fminf(fmaxf(x, 0.f), 1.f); }  // NaN: 0
+__device__ __forceinline__ float probability(float x) { return __saturatef(x); }  // NaN: 0
 
 // x in [0, 1) as a fraction of 2^64, rounded down.
 __device__ __forceinline__ u64 fraction(float x) {
@@ -162,6 +163,7 @@ struct VerifySmem {
   int gone[MK_TREE_MAX_NODES];      // tokens found that were refused at this node, and their units
   u64 gone_units[MK_TREE_MAX_NODES];
   u64 warp_sum[TV_WARPS], total, scan[TV_WARPS];
+  u64 piece[TV_WARPS][32];          // of a warp's share, 32 consecutive pieces' sums
   VerifyCtl ctl;
 };
 
@@ -179,7 +181,7 @@ __device__ __forceinline__ int next_child(const int* up, int k, int cur, int fro
 // aligned.
 __device__ __forceinline__ float4 load4(const float* row, int v, int vocab, bool wide) {
   const int e = 4 * v;
-  if (wide && e + 4 <= vocab) return __ldcs(reinterpret_cast<const float4*>(row + e));
+  if (wide && e + 4 <= vocab) return __ldcg(reinterpret_cast<const float4*>(row + e));
   float4 x;
   x.x = e < vocab ? row[e] : 0.f;
   x.y = e + 1 < vocab ? row[e + 1] : 0.f;
@@ -188,21 +190,33 @@ __device__ __forceinline__ float4 load4(const float* row, int v, int vocab, bool
   return x;
 }
 
-// A warp's sum of the rest over the vectors [v, v1), lanes side by side, U vectors of
-// each row in flight a lane.
+// A warp's sums of the rest over the vectors [v, v1): lane i gets the sum of the i-th
+// piece of `piece` vectors (a multiple of 32 U; 32 of them cover all).  Lanes side by
+// side, U vectors of each row in flight a lane.
 enum { REST_P, REST_ONE, REST_S };
 template <int U, int KIND>
-__device__ __forceinline__ u64 sum_rest(const float* rp, const float* rq, double s, int v, int v1, int vocab, bool wide) {
+__device__ __forceinline__ u64 sum_rest(const float* rp, const float* rq, double s, int v, int v1, int piece, int vocab, bool wide) {
   const Refusals S(s);
-  u64 sum = 0;
-  for (v += threadIdx.x & 31; v < v1; v += 32 * U) {
+  const int lane = threadIdx.x & 31;
+  u64 sum = 0, mine = 0;
+  int left = piece, at = 0;
+  for (v += lane; v - lane < v1; v += 32 * U) {
     float4 a[U], b[U];
+    if (wide && v - lane + 32 * U <= min(v1, vocab / 4)) {
+      // (without a branch between the loads)
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (v + 32 * i < v1) {
-        a[i] = load4(rp, v + 32 * i, vocab, wide);
-        if (KIND != REST_P) b[i] = load4(rq, v + 32 * i, vocab, wide);
+      for (int i = 0; i < U; ++i) {
+        a[i] = __ldcg(reinterpret_cast<const float4*>(rp) + v + 32 * i);
+        b[i] = KIND != REST_P ? __ldcg(reinterpret_cast<const float4*>(rq) + v + 32 * i) : a[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (v + 32 * i < v1) {
+          a[i] = load4(rp, v + 32 * i, vocab, wide);
+          if (KIND != REST_P) b[i] = load4(rq, v + 32 * i, vocab, wide);
+        }
       }
     }
     Units x;
@@ -218,10 +232,17 @@ __device__ __forceinline__ u64 sum_rest(const float* rp, const float* rq, double
       one(a[i].w, b[i].w);
     }
     sum += x.value();
-  }
+    left -= 32 * U;
+    if (left == 0 || v - lane + 32 * U >= v1) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == at) mine = sum;
+      sum = 0;
+      left = piece;
+      ++at;
+    }
+  }
+  return mine;
 }
 
 // Of n <= 32 sums in the lanes, the first whose running sum passes *want; *want becomes
@@ -240,7 +261,7 @@ __device__ __forceinline__ int find_sum(u64 mine, int n, int lane, u64* want) {
   return at;
 }
 
-__global__ void __launch_bounds__(TV_THREADS, 1) tree_verify_kernel(const VerifyParams P) {
+__global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const VerifyParams P) {
   __shared__ VerifySmem S;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = cluster_rank(), ctas = cluster_size(), r = blockIdx.x / ctas;
@@ -292,6 +313,7 @@ __global__ void __launch_bounds__(TV_THREADS, 1) tree_verify_kernel(const Verify
   }
 
   const int vecs = (P.vocab + 3) / 4, per_cta = (vecs + ctas - 1) / ctas, per_warp = (per_cta + TV_WARPS - 1) / TV_WARPS;
+  const int piece = ((per_warp + TV_BATCH - 1) / TV_BATCH + 31) / 32 * TV_BATCH;  // a multiple of what is in flight
   const int v_end = min(vecs, (rank + 1) * per_cta);
   auto warp_first = [&](int w) { return min(v_end, rank * per_cta + w * per_warp); };
   const uint32_t ctl0 = cluster_addr(&S.ctl, 0);
@@ -351,16 +373,23 @@ __global__ void __launch_bounds__(TV_THREADS, 1) tree_verify_kernel(const Verify
     u64 total = 0, cta_total = 0;
     for (int pass = 0; pass < 2; ++pass) {
       const int v0 = warp_first(warp), v1 = warp_first(warp + 1);
-      const u64 sum = c.S == 0.0   ? sum_rest<8, REST_P>(rp, rq, 0.0, v0, v1, P.vocab, wide)
-                      : c.S == 1.0 ? sum_rest<4, REST_ONE>(rp, rq, 1.0, v0, v1, P.vocab, wide)
-                                   : sum_rest<4, REST_S>(rp, rq, c.S, v0, v1, P.vocab, wide);
+      u64 sum = c.S == 0.0   ? sum_rest<2 * TV_U, REST_P>(rp, rq, 0.0, v0, v1, piece, P.vocab, wide)
+                : c.S == 1.0 ? sum_rest<TV_U, REST_ONE>(rp, rq, 1.0, v0, v1, piece, P.vocab, wide)
+                             : sum_rest<TV_U, REST_S>(rp, rq, c.S, v0, v1, piece, P.vocab, wide);
+      if (c.last) S.piece[warp][lane] = sum;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) S.warp_sum[warp] = sum;
       __syncthreads();
       if (c.refused > 0) {  // without what was refused
         for (int g = tid; g < c.refused; g += TV_THREADS) {
           const int v = (int)ld_cluster32(cluster_addr(&S.gone[g], 0)) / 4;
-          if (v / per_cta == rank)
-            atomicAdd(&S.warp_sum[(v - rank * per_cta) / per_warp], 0ull - ld_cluster64(cluster_addr(&S.gone_units[g], 0)));
+          if (v / per_cta == rank) {
+            const int w = (v - rank * per_cta) / per_warp;
+            const u64 less = 0ull - ld_cluster64(cluster_addr(&S.gone_units[g], 0));
+            atomicAdd(&S.warp_sum[w], less);
+            if (c.last) atomicAdd(&S.piece[w][(v - warp_first(w)) / piece], less);
+          }
         }
         __syncthreads();
       }
@@ -406,7 +435,8 @@ __global__ void __launch_bounds__(TV_THREADS, 1) tree_verify_kernel(const Verify
       }
     } else if (owner == rank) {
       const int w = find_sum(lane < TV_WARPS ? S.warp_sum[lane] : 0, TV_WARPS, lane, &want);
-      const int v0 = warp_first(w), v1 = warp_first(w + 1);
+      const int part = find_sum(S.piece[w][lane], 32, lane, &want);
+      const int v0 = min(warp_first(w) + part * piece, warp_first(w + 1)), v1 = min(v0 + piece, warp_first(w + 1));
       bool found = false;
       for (int b = v0; b < v1 && !found; b += TV_THREADS) {
         const int v = b + tid;
@@ -455,15 +485,39 @@ __global__ void __launch_bounds__(TV_THREADS, 1) tree_verify_kernel(const Verify
   cluster_sync();  // no CTA's shared memory is read any more
 }
 
-// CTAs of a request: as many as fill the GPU once, 16 at most.
-// (A cluster of 16 is more than every GPU has to take: the device is asked once.)
+// CTAs of a request: as many as all requests' fit the GPU at once (two an SM).  16 are
+// more than a device has to take in a cluster; it is asked once.
+int verify_cluster_most(int device) {
+  static std::atomic<uint64_t> known{0}, wide{0};
+  const uint64_t bit = 1ull << (device & 63);
+  if (!(known.load(std::memory_order_acquire) & bit) || device >= 64) {
+    int n = 0;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 16;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(TV_THREADS);
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const bool ok = cudaFuncSetAttribute(tree_verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, tree_verify_kernel, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();
+    if (device >= 64) return ok ? 16 : 8;
+    if (ok) wide.fetch_or(bit, std::memory_order_relaxed);
+    known.fetch_or(bit, std::memory_order_release);
+  }
+  return wide.load(std::memory_order_relaxed) & bit ? 16 : 8;
+}
+
 cudaError_t verify_launch(const VerifyParams& p, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  int cluster = 8;
-  while (cluster > 1 && p.n * cluster > sms) cluster /= 2;
+  int cluster = verify_cluster_most(dev);
+  while (cluster > 1 && p.n * cluster > 2 * sms) cluster /= 2;
   return paged_launch_clusters(tree_verify_kernel, p.n * cluster, cluster, TV_THREADS, 0, st, p);
 }
 
