@@ -515,7 +515,10 @@ cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool 
   p.few_rows = want <= 8 ? 8 : want <= 16 ? 16 : 0;
   // Among trees a request of a single token is an exception that the tile kernel
   // takes too: a launch for it would be paid by every call.
-  if (p.masks && !all_few) p.few_rows = 0;
+  if (p.masks && !all_few) {
+    p.few_rows = 0;
+    paged_chunk_clusters(&p, d, bf);
+  }
   // rows a pair has at most: a warp each in the join, or several for one
   p.join_shares = !all_few || want > 4 ? 0 : want > 2 ? 1 : want > 1 ? 2 : 3;
   // workspace: descriptions, maxima and sums, outputs of the two kernels' parts
@@ -535,7 +538,7 @@ cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool 
   static_assert(224 * (2 * 16 + 2 * (16 + 256) * (8 + 128 * 4)) <= MK_PAGED_WORKSPACE_BYTES, "workspace");
   if (few.ctas) e = paged_few_launch(p, kv, few, d, bf, st);
   if (e == cudaSuccess && !all_few) e = paged_chunk_launch(p, kv, chunk, d, bf, st);
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && !p.cluster)
     e = p.masks && !all_few ? paged_join_tiles_launch(p, chunk, d, bf, st) : paged_join_launch(p, few, chunk, d, bf, st);
   return e;
 }

@@ -46,6 +46,7 @@ struct PagedAttnParams {
   // 32 mask_words new tokens are causal.  NULL: all are.
   const uint32_t* masks;
   int mask_words;
+  int cluster, cluster_tiles;  // CTAs of a tile's cluster (0: no clusters), tiles
 #ifdef __CUDACC__
   // token of a tile's row (row < 256, rep <= 64: the error, row / 2^16, stays
   // below 1 / rep)
@@ -142,6 +143,7 @@ cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const 
                              bool bf, cudaStream_t st);
 cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
                                bool bf, cudaStream_t st);
+void paged_chunk_clusters(PagedAttnParams* p, int d, bool bf);
 cudaError_t paged_join_tiles_launch(const PagedAttnParams& p, const PagedParts& b, int d, bool bf, cudaStream_t st);
 cudaError_t paged_join_launch(const PagedAttnParams& p, const PagedParts& a, const PagedParts& b, int d,
                               bool bf, cudaStream_t st);

@@ -89,6 +89,10 @@ __device__ __forceinline__ int tile_blocks(const PagedAttnParams& P, const Reque
   return max(1, (hi + 127) / 128 - lo / 128);
 }
 
+// First of n blocks that CTA k of a cluster takes (the first ones have one more: the
+// last blocks, with masks, take longer).
+__device__ __forceinline__ int share_of(int n, int k, int ctas) { return (n * k + ctas - 1) / ctas; }
+
 __device__ __forceinline__ void let_land() {
   const uint64_t t0 = globaltimer();
   while (globaltimer() - t0 < 1000000ull) {
@@ -108,8 +112,8 @@ __device__ __forceinline__ void quad_swap(uint32_t (&a)[4], uint32_t (&b)[4], in
 }
 
 // TREE: rows of requests with masks see the cached keys and the new ones that their
-// masks name.
-template <int HD, bool BF, bool TREE>
+// masks name.  CLUSTERS: a cluster for each tile instead of runs of all tiles' blocks.
+template <int HD, bool BF, bool TREE, bool CLUSTERS>
 __global__ void __launch_bounds__(PC_THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedAttnParams P,
@@ -128,6 +132,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   uint64_t* ofull = pfull + 2;           // O of half h complete
   volatile int* dead = reinterpret_cast<volatile int*>(ofull + 2);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(const_cast<int*>(dead) + 1);
+  int* joined = reinterpret_cast<int*>(tslot + 1);  // [4] a cluster's tile: rows, first token, blocks, head
   Tile* meta = reinterpret_cast<Tile*>(smem + C::o_meta);
   const Kept kept(smem + C::o_pre, P.n);
   int* pre = kept.pre;
@@ -166,11 +171,37 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   // written before that one's own wait, but a grid is promised to see it only by
   // waiting itself: mixed step of 27 requests 46.8 us, with the wait at the end 44.5.)
   grid_wait_prior();
-  if (tid == 0) W.desc[blockIdx.x].parts = 0;
+  constexpr bool clustered = CLUSTERS;
+  if (tid == 0 && !clustered) W.desc[blockIdx.x].parts = 0;
+
+  // In clusters: this one's tile, of which the CTA takes blocks [cb0, cb1).
+  Request cq{};
+  int cr = 0, ch = 0, ct = 0, cnb = 0, cb0 = 0, cb1 = 0, rank = 0;
+  if constexpr (clustered) {
+    const int tiles = (P.max_new + TT - 1) / TT, id = blockIdx.x / P.cluster;
+    rank = (int)cluster_rank();
+    cr = id / (P.hkv * tiles);
+    ch = id / tiles - cr * P.hkv;
+    ct = id % tiles;
+    const int first = P.cu[cr];
+    cq = make_request(P, first, P.cu[cr + 1], P.kv[cr]);
+    if (begins_below(P.cu, cr, first)) cq.add = 0;
+    int f;
+    if ((int64_t)ct * TT < cq.add) cnb = tile_blocks<TREE>(P, cq, ct, TT, &f);
+    cb0 = share_of(cnb, rank, P.cluster);
+    cb1 = share_of(cnb, rank + 1, P.cluster);
+    if (cq.bad && tid == 0) latch(P.status, MK_ERR_BOUNDS);
+    if (tid == 0) {  // for the join
+      joined[0] = cnb > 0 ? min(TT, cq.add - ct * TT) * P.rep : 0;
+      joined[1] = cq.row0 + ct * TT;
+      joined[2] = cnb;
+      joined[3] = ch;
+    }
+  }
 
   // units: the tiles' blocks and overheads.  A thread counts its requests'
   // tiles; a warp together those of a request with many.
-  const int per = (P.n + PC_THREADS - 1) / PC_THREADS;
+  const int per = clustered ? 0 : (P.n + PC_THREADS - 1) / PC_THREADS;
   uint32_t mine = 0;
   bool bad = false, falls = false;
   for (int i = 0; i < per; ++i) {
@@ -203,7 +234,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     mine += u;
   }
   int* scan_tmp = reinterpret_cast<int*>(smem + C::o_kv);  // not loaded to yet
-  const int T = place_units<PC_THREADS / 32>(P, pre, per, mine, falls, scan_tmp);
+  const int T = clustered ? 0 : place_units<PC_THREADS / 32>(P, pre, per, mine, falls, scan_tmp);
   if (bad && blockIdx.x == 0) latch(P.status, MK_ERR_BOUNDS);
   fence_proxy_async_smem();  // the scan's words, before a load takes their place
   tc_fence_before();
@@ -214,7 +245,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
 
   const int G = min((int)gridDim.x, T), c = blockIdx.x;
   const Runs runs(T, max(G, 1));
-  const int u0 = c < G ? runs.start(c) : 0, u1 = c < G ? runs.start(c + 1) : 0;
+  const int u0 = c < G ? runs.start(c) : 0, u1 = clustered ? (cb0 < cb1 ? 1 : 0) : c < G ? runs.start(c + 1) : 0;
 
   // Values are loaded by a warp of their own where pages are of 16 tokens: a
   // block's keys and values are then 32 boxes of 2 KB, which one warp does not
@@ -279,15 +310,15 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       int stage = 0, slot = 0;
       uint32_t sphase = 1, mphase = 1, qphase = 1;
       const int step = split_v ? 2 : 1;
-      int r = u0 < u1 ? find_le(pre, P.n, u0) : 0, t = -1, head = 0;
+      int r = u0 < u1 && !clustered ? find_le(pre, P.n, u0) : cr, t = clustered ? ct : -1, head = ch;
       bool up = true;
       for (int u = u0; u < u1 && up;) {
-        while (pre[r + 1] <= u) {
+        while (!clustered && pre[r + 1] <= u) {
           ++r;
           t = -1;
         }
-        const Request q = kept.again(P, r);
-        const int per_head = (pre[r + 1] - pre[r]) / P.hkv, ntile = (q.add + TT - 1) / TT;
+        const Request q = clustered ? cq : kept.again(P, r);
+        const int per_head = clustered ? 1 : (pre[r + 1] - pre[r]) / P.hkv, ntile = (q.add + TT - 1) / TT;
         int x0 = 0, b0;  // first unit of the tile in this run
         if (t < 0) {  // find the tile of unit u
           const int local = u - pre[r];
@@ -314,11 +345,11 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         }
         // units [x0, x1) of the tile: blocks [blk, blk + nblk)
         const int nb = tile_blocks<TREE>(P, q, t, TT, &b0), x1 = min(nb + PC_OVER, x0 + u1 - u);
-        const int blk = max(0, x0 - PC_OVER), nblk = max(0, x1 - PC_OVER) - blk;
+        const int blk = clustered ? cb0 : max(0, x0 - PC_OVER), nblk = clustered ? cb1 - cb0 : max(0, x1 - PC_OVER) - blk;
         const int ntok = min(TT, q.add - t * TT), end = u - x0 + nb + PC_OVER;
         if (nblk == 0) break;  // the run ends with the tile's overhead: the next CTA has it all
         const bool whole = blk == 0 && nblk == nb;
-        if (blk == 0 && !whole && lane == 0) {
+        if (blk == 0 && !whole && lane == 0 && !clustered) {
           const int last = runs.of(end - 1);  // CTA of the tile's last unit
           PartDesc d;
           d.row0 = q.row0 + t * TT; d.rows = ntok * P.rep; d.head = head; d.parts = last - c + 1;
@@ -330,7 +361,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           Tile m;
           m.key0 = (b0 + blk) * 128; m.nblk = nblk; m.row0 = q.row0 + t * TT; m.ntok = ntok; m.head = head;
           m.pos0 = q.pos0 + t * TT; m.lo = q.lo; m.hi = q.hi;
-          m.part = whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
+          m.part = clustered && P.cluster > 1 ? -2 : clustered || whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
           m.req = r;
           m.ctx = is_tree<TREE>(P, q) ? q.pos0 : -0x7fffffff - 1;
           meta[slot] = m;
@@ -462,6 +493,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       if (*dead) let_land();
       __syncwarp();
     }
+    if (clustered && P.cluster > 1) {
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     // ------------------------------------------------------------ softmax
     setmaxnreg_inc<PC_REGS_SOFT>();
@@ -475,6 +510,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     uint32_t blkn = 0, sn = 0, on = 0;
     int slot = 0;
     uint32_t mphase = 0;
+    int held = -1;  // in a cluster: this thread's row of the tile, its maximum and sum
+    float held_m = 0.f, held_l = 0.f;
     for (;;) {
       wait_phase(&mfull[slot], mphase, dead, P.status);
       if (*dead) break;
@@ -660,6 +697,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       tc_fence_after();
       const bool live = tok_in < ntok;
       const int prow = tok0 * P.rep + row;
+      if (clustered && m.part == -2) {  // (the one tile)
+        if (live) held = prow;
+        held_m = mx * cs - top;
+        held_l = l;
+        continue;
+      }
       if (m.part < 0) {
         // Four lanes exchange 16-byte pieces so that a store writes 64
         // contiguous bytes of a row: lane 4 a + b then has piece b of the rows
@@ -708,6 +751,83 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (live) W.ml[(int64_t)m.part * W.rt + prow] = make_float2(mx * cs - top, l);
       }
       tc_fence_before();  // the next tile's first P V is issued behind this group's next P
+    }
+    if (clustered && P.cluster > 1) {
+      // A cluster's CTAs have the tile's rows, each over its share of the keys: CTA k
+      // joins rows [k per, (k + 1) per), which all of them write to its shared memory
+      // ([CTA][4 columns][row]), where the keys and values were and before them (rows
+      // of up to 15 more than the tile has), maxima and sums at its start.
+      constexpr int o_parts = C::o_kv - 16384;
+      static_assert((256 + 15) * HD * 4 <= C::o_meta - o_parts && (256 + 15) * 8 <= 8192 && 8192 + (256 + 15) * 4 <= o_parts, "room for the parts");
+      const int cl = P.cluster, rows = joined[0], nb = joined[2], per_cta = max(1, (rows + cl - 1) / cl), rk = (int)cluster_rank();
+      const uint32_t has = __ballot_sync(0xffffffffu, lane < cl && share_of(nb, lane, cl) < share_of(nb, lane + 1, cl));  // CTAs that had keys
+      cluster_sync();  // nothing of the cluster's products and loads is on its way
+      if (__any_sync(0xffffffffu, held >= 0)) {
+        const int owner = max(held, 0) / per_cta, at = max(held, 0) - owner * per_cta;
+        const uint32_t o_to = cluster_addr(smem + o_parts, owner) + (uint32_t)((rk * per_cta * HD + at * 4) * 4);
+        const uint32_t ml_to = cluster_addr(smem, owner) + (uint32_t)((rk * per_cta + at) * 8);
+        if (held >= 0) st_cluster64(ml_to, pack_f32x2(held_m, held_l));
+#pragma unroll 1
+        for (int x = 0; x < HD; x += 32) {
+          float o[32];
+          tmem_ld32(o_t + x, o);
+          if (held >= 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              st_cluster128(o_to + (uint32_t)((x + i) * per_cta * 4), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+          }
+        }
+        tc_fence_before();
+      }
+      cluster_sync();
+      // the CTAs' factors of a row (16 lanes a row, one a CTA), then the rows
+      const float2* ml = reinterpret_cast<const float2*>(smem);
+      float* factor = reinterpret_cast<float*>(smem + 8192);
+      const float4* part = reinterpret_cast<const float4*>(smem + o_parts);
+      if (!*dead) {
+        for (int rw0 = warp * 2; rw0 < per_cta; rw0 += 16) {
+          const int rw = rw0 + (lane >> 4), c = lane & 15;
+          const bool in = rw < per_cta && (has >> c & 1u);
+          const float2 y = in ? ml[c * per_cta + rw] : make_float2(-INFINITY, 0.f);
+          float mm = y.x;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+          const float f = ex2(y.x - (mm == -INFINITY ? 0.f : mm));
+          float ll = in ? y.y * f : 0.f;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
+          if (c < cl && rw < per_cta) factor[c * per_cta + rw] = f * inv_of(ll);
+          const int prow = rk * per_cta + rw;
+          if (c == 0 && P.lse && rw < per_cta && prow < rows) {
+            const int tk = P.token_of(prow);
+            P.lse[(int64_t)(joined[1] + tk) * (P.hkv * P.rep) + joined[3] * P.rep + prow - tk * P.rep] = lse_of(mm, ll);
+          }
+        }
+      }
+      named_bar(1, 256);
+      for (int i = tid; i < per_cta * (HD / 4) && !*dead; i += 256) {
+        const int d4 = i / per_cta, rw = i - d4 * per_cta, prow = rk * per_cta + rw;
+        if (prow >= rows) continue;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < cl; c0 += 4) {
+          float f[4];
+          float4 v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // (of a CTA without keys: factor 0 and whatever was there)
+            const int k = min(c0 + c, cl - 1);
+            f[c] = factor[k * per_cta + rw];
+            v[c] = part[(k * (HD / 4) + d4) * per_cta + rw];
+            if (c0 + c >= cl || f[c] == 0.f) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            acc.x += v[c].x * f[c]; acc.y += v[c].y * f[c]; acc.z += v[c].z * f[c]; acc.w += v[c].w * f[c];
+          }
+        }
+        const int tk = P.token_of(prow);
+        *reinterpret_cast<uint2*>(P.out + (int64_t)(joined[1] + tk) * P.o_stride + (int64_t)(joined[3] * P.rep + prow - tk * P.rep) * HD + d4 * 4) =
+            make_uint2(down2<BF>(acc.x, acc.y), down2<BF>(acc.z, acc.w));
+      }
     }
   }
   tc_fence_before();
@@ -780,6 +900,7 @@ template <int HD, bool BF>
 __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const __grid_constant__ PagedAttnParams P, const __grid_constant__ PagedParts B) {
   constexpr int DG = HD / 32, Q = DG;
   __shared__ int upto[225], tmp[JT_THREADS / 32];
+  __shared__ PartDesc desc[224];
   __shared__ float other[8][4][33];
   __shared__ float2 other_ml[32];
   __shared__ uint2 rows_out[2][32][HD / 4 + 1];
@@ -787,7 +908,7 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
   grid_launch_dependents();
   grid_wait_prior();
   PartDesc d{};
-  if (tid < B.ctas) d = B.desc[tid];
+  if (tid < B.ctas) desc[tid] = d = B.desc[tid];
   int total;  // items of all dimensions
   bool any;
   const uint32_t at = block_scan<JT_THREADS / 32>(d.parts ? (uint32_t)(d.rows + 31) / 32 : 0u, false, tmp, &total, &any);
@@ -811,7 +932,7 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
   if (total * DG > 2 * (int)gridDim.x) {
     for (int item = 2 * blockIdx.x + team; item < total; item += 2 * gridDim.x) {
       const int c = find_le(upto, B.ctas, item), row0 = (item - upto[c]) * 32;
-      const PartDesc t = B.desc[c];
+      const PartDesc t = desc[c];
       float m, l;
       float4 o[Q];
       join_parts<HD, Q, 2>(B, c, t.parts, row0 + lane, quad * Q, 0, 1, &m, &l, o);
@@ -828,7 +949,7 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
   }
   for (int item = blockIdx.x; item < total * DG; item += gridDim.x) {
     const int c = find_le(upto, B.ctas, item / DG), row0 = (item / DG - upto[c]) * 32, d0 = item % DG * 32;
-    const PartDesc t = B.desc[c];
+    const PartDesc t = desc[c];
     float m, l;
     float4 o[1];
     join_parts<HD, 1, 5>(B, c, t.parts, row0 + lane, d0 / 4 + quad, team, 2, &m, &l, o);
@@ -851,7 +972,37 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
   }
 }
 
-template <int HD, bool BF, bool TREE>
+// Clusters of `ctas` CTAs that the device holds at once (asked once for each size).
+template <int HD, bool BF>
+int clusters_at_once(int device, int ctas) {
+  static std::atomic<int> known[64][17];
+  std::atomic<int>* mine = device < 64 ? &known[device][ctas] : nullptr;
+  int n = mine ? mine->load(std::memory_order_relaxed) : 0;  // one more than the number
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(PC_THREADS);
+    cfg.dynamicSmemBytes = ChunkCfg<HD>::most;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const void* kernel = (const void*)paged_chunk_kernel<HD, BF, true, true>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<HD>::most) != cudaSuccess ||
+        (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    ++n;
+    if (mine) mine->store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
+template <int HD, bool BF, bool TREE, bool CLUSTERS>
 cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
   CUtensorMap tq, tk, tv;
   if (!make_page_tmap(&tk, kv.k, kv, HD, 128, 1, BF) || !make_page_tmap(&tv, kv.v, kv, HD, 128, 1, BF) ||
@@ -859,13 +1010,22 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
     return cudaErrorInvalidValue;
   // the register split needs the block to be launched with what it counts on
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF, TREE>,
+  const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF, TREE, CLUSTERS>,
                                       ChunkCfg<HD>::most, PC_REGS, p.device, &ready);
   if (e != cudaSuccess) return e;
+  if constexpr (CLUSTERS)
+    return paged_launch_clusters(paged_chunk_kernel<HD, BF, TREE, CLUSTERS>, p.cluster_tiles * p.cluster, p.cluster, PC_THREADS,
+                                 ChunkCfg<HD>::total(p.n), st, tq, tk, tv, p, w);
   // behind the few-row kernel it is set up while that one ends; alone it is launched
   // behind the whole of what precedes (8192-token prompt 363 against 368 us)
-  return paged_launch_if(TREE || p.few_rows > 0, paged_chunk_kernel<HD, BF, TREE>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
+  return paged_launch_if(TREE || p.few_rows > 0, paged_chunk_kernel<HD, BF, TREE, CLUSTERS>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
                          tq, tk, tv, p, w);
+}
+
+template <bool TREE, bool CLUSTERS>
+cudaError_t launch_type(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d, bool bf, cudaStream_t st) {
+  if (d == 128) return bf ? launch<128, true, TREE, CLUSTERS>(p, kv, w, st) : launch<128, false, TREE, CLUSTERS>(p, kv, w, st);
+  return bf ? launch<64, true, TREE, CLUSTERS>(p, kv, w, st) : launch<64, false, TREE, CLUSTERS>(p, kv, w, st);
 }
 
 }  // namespace
@@ -873,11 +1033,38 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
 cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
                                bool bf, cudaStream_t st) {
   if (p.masks) {
-    if (d == 128) return bf ? launch<128, true, true>(p, kv, w, st) : launch<128, false, true>(p, kv, w, st);
-    return bf ? launch<64, true, true>(p, kv, w, st) : launch<64, false, true>(p, kv, w, st);
+    if (p.cluster) return launch_type<true, true>(p, kv, w, d, bf, st);
+    return launch_type<true, false>(p, kv, w, d, bf, st);
   }
-  if (d == 128) return bf ? launch<128, true, false>(p, kv, w, st) : launch<128, false, false>(p, kv, w, st);
-  return bf ? launch<64, true, false>(p, kv, w, st) : launch<64, false, false>(p, kv, w, st);
+  return launch_type<false, false>(p, kv, w, d, bf, st);
+}
+
+// Few tiles over few keys: a cluster for each, of as many CTAs as the device holds at
+// once for all, joined in their shared memory (a lone request of 32 tokens over 4096
+// keys, 8 kv heads of 128, 14.3 against 16.6 us of runs over all SMs, parts in memory
+// and the join's launch; 16 of them over 512 keys, a CTA a tile, 15.7 against 23.1).
+// The keys that a tile may have are bounded by the table's width.  Past 8 blocks a
+// CTA the SMs that no cluster fills cost more than the join (over 16384 keys 26.3
+// against 25.4), with tiles of two halves, whose exchange is twice as long, past 3
+// (2 x 64 tokens over 4096 keys 27.2 against 25.8; 64 over 4096 19.4, 19.6); a CTA a
+// tile has nothing to exchange.
+void paged_chunk_clusters(PagedAttnParams* p, int d, bool bf) {
+  const int tt = 2 * (128 / p->rep);
+  const int64_t tiles = (int64_t)p->n * p->hkv * (((int64_t)p->max_new + tt - 1) / tt);
+  const int64_t blocks = (((int64_t)p->max_blocks << p->page_shift) + 127) / 128;
+  p->cluster = p->cluster_tiles = 0;
+  if (tiles > 256) return;
+  for (int c = 16; c >= 1; --c) {
+    const int most = d == 128 ? (bf ? clusters_at_once<128, true>(p->device, c) : clusters_at_once<128, false>(p->device, c))
+                              : (bf ? clusters_at_once<64, true>(p->device, c) : clusters_at_once<64, false>(p->device, c));
+    if (tiles > most) continue;
+    const int64_t most_blocks = c == 1 ? 16 : (int64_t)p->max_new * p->rep > 128 ? 3 * c : 8 * c;
+    if (blocks <= most_blocks) {
+      p->cluster = c;
+      p->cluster_tiles = (int)tiles;
+    }
+    return;
+  }
 }
 
 cudaError_t paged_join_tiles_launch(const PagedAttnParams& p, const PagedParts& b, int d, bool bf, cudaStream_t st) {
