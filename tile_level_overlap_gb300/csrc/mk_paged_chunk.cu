@@ -60,6 +60,8 @@ struct ChunkCfg {
 };
 static_assert(ChunkCfg<128>::most <= 232448 && ChunkCfg<64>::most <= 232448, "shared memory of a CTA");
 
+constexpr int PART_PAIR = 1 << 30;  // in a PartDesc's head: rows of two heads, the second's from 128 on
+
 struct Tile {
   int key0, nblk;          // first key of the run; 0 blocks: the end
   int row0, ntok, head;    // first token (row of q), tokens of the tile
@@ -68,7 +70,8 @@ struct Tile {
   int part;                // workspace part, -1: all of the tile's blocks
   int req;                 // its request
   int ctx;                 // of a tree: its cached tokens; else -2^31
-  int pad[5];
+  int pair;                // the halves are two heads' rows, from `head` on
+  int pad[4];
 };
 static_assert(sizeof(Tile) == 64, "meta slot");
 
@@ -76,6 +79,17 @@ static_assert(sizeof(Tile) == 64, "meta slot");
 template <bool TREE>
 __device__ __forceinline__ bool is_tree(const PagedAttnParams& P, const Request& q) {
   return TREE && q.add <= 32 * P.mask_words;
+}
+
+// Trees of at most 128 rows go in pairs of kv heads, where heads are 64 wide and of even
+// number: a tile's halves are the rows of two heads, whose blocks take turns in the
+// ring.  Alone a half's softmax and products take 1.1 us a block, in turn, of which
+// HBM needs 0.73 (32 requests of 13 tokens over 2048 keys 47.6 us alone, 37.7 in
+// pairs).  Of 128-wide heads HBM needs 1.47 and the half 1.4: pairs only make the parts
+// larger (32 of 32 over 1280 48.4 alone, 54.8 in pairs).
+template <bool PAIRS>
+__device__ __forceinline__ bool is_pair(const PagedAttnParams& P, const Request& q, int TS) {
+  return PAIRS && (P.hkv & 1) == 0 && q.add <= TS;
 }
 
 // First block and number of blocks of tile t of a request (TT tokens a tile).  Any
@@ -120,6 +134,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
                        const __grid_constant__ PagedParts W) {
   using C = ChunkCfg<HD>;
   constexpr int ST = C::STAGES;
+  constexpr bool PAIRS = TREE && !CLUSTERS && HD == 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::o_bar);
   uint64_t* empty = full + ST;
@@ -229,7 +244,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == from) u = v;
     }
-    u = (u + PC_OVER * ntile) * P.hkv;
+    u = (u + PC_OVER * ntile) * (is_pair<PAIRS>(P, q, TS) ? P.hkv / 2 : P.hkv);
     if (r < P.n) pre[r] = u;
     mine += u;
   }
@@ -297,9 +312,11 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         bool up = true;
         for (int i = 0; i < m.nblk && up; ++i) {
           const int next = i + 1 < m.nblk ? page_of(tab, b0 + i + 1, m.lo, m.hi) : -1;
-          up = load(&tv, stage, sphase, b0 + i, m.head, page);
-          stage += 2;
-          if (stage > ST) { stage = 1; sphase ^= 1; }
+          for (int h = 0; h <= (PAIRS ? m.pair : 0) && up; ++h) {
+            up = load(&tv, stage, sphase, b0 + i, m.head + h, page);
+            stage += 2;
+            if (stage > ST) { stage = 1; sphase ^= 1; }
+          }
           page = next;
         }
         if (!up) break;
@@ -318,7 +335,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           t = -1;
         }
         const Request q = clustered ? cq : kept.again(P, r);
-        const int per_head = clustered ? 1 : (pre[r + 1] - pre[r]) / P.hkv, ntile = (q.add + TT - 1) / TT;
+        const bool pair = is_pair<PAIRS>(P, q, TS);
+        const int per_head = clustered ? 1 : (pre[r + 1] - pre[r]) / (pair ? P.hkv / 2 : P.hkv), ntile = (q.add + TT - 1) / TT;
         int x0 = 0, b0;  // first unit of the tile in this run
         if (t < 0) {  // find the tile of unit u
           const int local = u - pre[r];
@@ -348,18 +366,20 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         const int blk = clustered ? cb0 : max(0, x0 - PC_OVER), nblk = clustered ? cb1 - cb0 : max(0, x1 - PC_OVER) - blk;
         const int ntok = min(TT, q.add - t * TT), end = u - x0 + nb + PC_OVER;
         if (nblk == 0) break;  // the run ends with the tile's overhead: the next CTA has it all
+        const int first_head = pair ? 2 * head : head;
         const bool whole = blk == 0 && nblk == nb;
         if (blk == 0 && !whole && lane == 0 && !clustered) {
           const int last = runs.of(end - 1);  // CTA of the tile's last unit
           PartDesc d;
-          d.row0 = q.row0 + t * TT; d.rows = ntok * P.rep; d.head = head; d.parts = last - c + 1;
+          d.row0 = q.row0 + t * TT; d.rows = ntok * P.rep; d.head = first_head | (pair ? PART_PAIR : 0); d.parts = last - c + 1;
           W.desc[c] = d;
         }
         wait_phase(&mempty[slot], mphase, dead, P.status);
         if (*dead) break;
         if (lane == 0) {
           Tile m;
-          m.key0 = (b0 + blk) * 128; m.nblk = nblk; m.row0 = q.row0 + t * TT; m.ntok = ntok; m.head = head;
+          m.key0 = (b0 + blk) * 128; m.nblk = nblk; m.row0 = q.row0 + t * TT; m.ntok = ntok; m.head = first_head;
+          m.pair = pair;
           m.pos0 = q.pos0 + t * TT; m.lo = q.lo; m.hi = q.hi;
           m.part = clustered && P.cluster > 1 ? -2 : clustered || whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
           m.req = r;
@@ -373,27 +393,29 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         for (int i = 0; i < nblk && up; ++i) {
           const int b = b0 + blk + i;
           const int next = i + 1 < nblk ? page_of(tab, b + 1, q.lo, q.hi) : -1;
-          up = load(&tk, stage, sphase, b, head, page);
-          stage += step;
-          if (up && i == 0) {
-            wait_phase(qempty, qphase, dead, P.status);
-            qphase ^= 1;
-            if (*dead) { up = false; break; }
-            const int halves = ntok > TS ? 2 : 1;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(qfull, halves * (HD / 64) * TS * P.rep * 128);
-              for (int h = 0; h < halves; ++h)
-                for (int x = 0; x < HD / 64; ++x)
-                  tma_rows(smem + h * C::TILE + x * 16384, &tq, 64 * x, head * P.rep,
-                           q.row0 + t * TT + h * TS, qfull);
+          for (int h = 0; h <= (pair ? 1 : 0) && up; ++h) {
+            up = load(&tk, stage, sphase, b, first_head + h, page);
+            stage += step;
+            if (up && i == 0 && h == 0) {
+              wait_phase(qempty, qphase, dead, P.status);
+              qphase ^= 1;
+              if (*dead) { up = false; break; }
+              const int halves = pair || ntok > TS ? 2 : 1;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(qfull, halves * (HD / 64) * TS * P.rep * 128);
+                for (int y = 0; y < halves; ++y)
+                  for (int x = 0; x < HD / 64; ++x)
+                    tma_rows(smem + y * C::TILE + x * 16384, &tq, 64 * x, (first_head + (pair ? y : 0)) * P.rep,
+                             q.row0 + t * TT + (pair ? 0 : y * TS), qfull);
+              }
+              __syncwarp();
             }
-            __syncwarp();
+            if (up && !split_v) {
+              up = load(&tv, stage, sphase, b, first_head + h, page);
+              ++stage;
+            }
+            if (stage >= ST) { stage = 0; sphase ^= 1; }
           }
-          if (up && !split_v) {
-            up = load(&tv, stage, sphase, b, head, page);
-            ++stage;
-          }
-          if (stage >= ST) { stage = 0; sphase ^= 1; }
           page = next;
         }
         u += x1 - x0;
@@ -438,13 +460,59 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         wait_phase(&mfull[slot], mphase, dead, P.status);
         if (*dead) break;
         const int nblk = meta[slot].nblk;
-        const bool mine = h == 0 || meta[slot].ntok > TS;
+        const bool mine = h == 0 || meta[slot].ntok > TS, pair = PAIRS && meta[slot].pair;
         __syncwarp();
         if (lane == 0) mbar_arrive(&mempty[slot]);
         if (nblk == 0) break;
         if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
         wait_phase(qfull, qn & 1, dead, P.status);
         ++qn;
+        if (PAIRS && pair) {
+          // A half's products are those of its own head's blocks, every other one.  A
+          // stage is released twice by the one that used it; a phase that a half does
+          // not see cannot be taken for another, since a stage that it uses is not
+          // filled again before it has.
+          const uint32_t end = blkn + 2 * nblk;
+          uint32_t b = blkn + h;
+          blkn = end;
+          auto s_of = [&](uint32_t st) {
+            s_product(st);
+            tc_commit(&empty[st]);
+            tc_commit(&empty[st]);
+          };
+          wait_phase(&full[kst(b)], kph(b), dead, P.status);
+          if (*dead) break;
+          tc_fence_after();
+          if (elect_one()) {
+            s_of(kst(b));
+            if (nblk == 1) tc_commit(qempty);
+          }
+          for (bool first = true; b < end; b += 2, first = false) {
+            const uint32_t vst = kst(b) + 1;
+            const bool more = b + 2 < end;
+            wait_phase(&full[vst], kph(b), dead, P.status);
+            if (more) wait_phase(&full[kst(b + 2)], kph(b + 2), dead, P.status);
+            wait_phase(&pfull[h], pn & 1, dead, P.status);
+            ++pn;
+            if (*dead) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_ta(t_o, t_s + 8u * kk, dv + (vst * (C::TILE / 16) + 128u * kk), id_o, !first || kk != 0);
+              if (more) {
+                s_of(kst(b + 2));
+                if (b + 4 >= end) tc_commit(qempty);
+              } else {
+                tc_commit(&ofull[h]);
+              }
+              tc_commit(&empty[vst]);
+              tc_commit(&empty[vst]);
+            }
+          }
+          if (*dead) break;
+          continue;
+        }
         if (!mine) {  // a tile of one half: see every phase, use nothing
           if (lane == 0) mbar_arrive(qempty);
           for (int j = 0; j < 2 * nblk; ++j) {
@@ -520,7 +588,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       if (lane == 0) mbar_arrive(&mempty[slot]);
       if (m.nblk == 0) break;
       if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
-      const int tok0 = half * TS;             // this half's first token of the tile
+      const bool pair = PAIRS && m.pair;
+      const int tok0 = pair ? 0 : half * TS;  // this half's first token of the tile
       if (tok0 >= m.ntok) {
         blkn += m.nblk;
         continue;
@@ -562,7 +631,9 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         }
       }
       float mx = -INFINITY, l = 0.f;
-      for (int j = 0; j < m.nblk; ++j, ++blkn) {
+      const uint32_t blk_step = pair ? 2 : 1, tile_end = blkn + (pair ? 2 * m.nblk : m.nblk);
+      if (pair) blkn += half;
+      for (int j = 0; j < m.nblk; ++j, blkn += blk_step) {
         const int key0 = m.key0 + 128 * j;
         uint32_t named[4] = {0, 0, 0, 0};  // columns of the block that the row's mask names
         if constexpr (TREE) {
@@ -692,11 +763,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[half]);
       }
+      blkn = tile_end;
       wait_phase(&ofull[half], on & 1, dead, P.status);
       ++on;
       tc_fence_after();
       const bool live = tok_in < ntok;
-      const int prow = tok0 * P.rep + row;
+      const int prow = (pair ? 128 * half : tok0 * P.rep) + row, head = m.head + (pair ? half : 0);
       if (clustered && m.part == -2) {  // (the one tile)
         if (live) held = prow;
         held_m = mx * cs - top;
@@ -715,7 +787,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           const int rw = (row & ~3) + i, tk = P.token_of(rw);
           put[i] = tk < ntok;
           dst[i] = P.out + (int64_t)(m.row0 + tok0 + tk) * P.o_stride +
-                   (int64_t)(m.head * P.rep + rw - tk * P.rep) * HD + (lane & 3) * 8;
+                   (int64_t)(head * P.rep + rw - tk * P.rep) * HD + (lane & 3) * 8;
         }
 #pragma unroll 1
         for (int x = 0; x < HD; x += 32) {
@@ -733,7 +805,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             if (put[i]) *reinterpret_cast<uint4*>(dst[i] + x) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
         }
         if (live && P.lse)
-          P.lse[(int64_t)(m.row0 + tok0 + tok_in) * (P.hkv * P.rep) + m.head * P.rep + hq_in] =
+          P.lse[(int64_t)(m.row0 + tok0 + tok_in) * (P.hkv * P.rep) + head * P.rep + hq_in] =
               lse_of(mx * cs - top, l);
       } else {
         // a part: [4 columns][row], a warp's lanes end to end
@@ -911,9 +983,17 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
   if (tid < B.ctas) desc[tid] = d = B.desc[tid];
   int total;  // items of all dimensions
   bool any;
-  const uint32_t at = block_scan<JT_THREADS / 32>(d.parts ? (uint32_t)(d.rows + 31) / 32 : 0u, false, tmp, &total, &any);
+  // items of a tile: its rows by 32, of a pair those of each head
+  const uint32_t at = block_scan<JT_THREADS / 32>(d.parts ? (uint32_t)((d.rows + 31) / 32 << (d.head >= PART_PAIR ? 1 : 0)) : 0u, false, tmp, &total, &any);
   if (tid <= B.ctas) upto[tid] = (int)at;
   __syncthreads();
+  // item x of a tile: the tile as of one head, the item's first row, its first row in the parts
+  auto item_of = [&](PartDesc& t, int x, int* row0) {
+    const int per = (t.rows + 31) / 32, half = t.head >= PART_PAIR && x >= per ? 1 : 0;
+    t.head = (t.head & ~PART_PAIR) + half;
+    *row0 = (x - half * per) * 32;
+    return *row0 + 128 * half;
+  };
   auto put_lse = [&](const PartDesc& t, int row, float m, float l) {
     if (!P.lse || row >= t.rows) return;
     const int tk = P.token_of(row);
@@ -931,11 +1011,13 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
   };
   if (total * DG > 2 * (int)gridDim.x) {
     for (int item = 2 * blockIdx.x + team; item < total; item += 2 * gridDim.x) {
-      const int c = find_le(upto, B.ctas, item), row0 = (item - upto[c]) * 32;
-      const PartDesc t = desc[c];
+      const int c = find_le(upto, B.ctas, item);
+      PartDesc t = desc[c];
+      int row0;
+      const int in_part = item_of(t, item - upto[c], &row0);
       float m, l;
       float4 o[Q];
-      join_parts<HD, Q, 2>(B, c, t.parts, row0 + lane, quad * Q, 0, 1, &m, &l, o);
+      join_parts<HD, Q, 2>(B, c, t.parts, in_part + lane, quad * Q, 0, 1, &m, &l, o);
       const float inv = inv_of(l);
       named_bar(1 + team, JT_TEAM);  // the previous rows have been written
 #pragma unroll
@@ -948,11 +1030,13 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
     return;
   }
   for (int item = blockIdx.x; item < total * DG; item += gridDim.x) {
-    const int c = find_le(upto, B.ctas, item / DG), row0 = (item / DG - upto[c]) * 32, d0 = item % DG * 32;
-    const PartDesc t = desc[c];
+    const int c = find_le(upto, B.ctas, item / DG), d0 = item % DG * 32;
+    PartDesc t = desc[c];
+    int row0;
+    const int in_part = item_of(t, item / DG - upto[c], &row0);
     float m, l;
     float4 o[1];
-    join_parts<HD, 1, 5>(B, c, t.parts, row0 + lane, d0 / 4 + quad, team, 2, &m, &l, o);
+    join_parts<HD, 1, 5>(B, c, t.parts, in_part + lane, d0 / 4 + quad, team, 2, &m, &l, o);
     if (team) {
       other[quad][0][lane] = o[0].x; other[quad][1][lane] = o[0].y; other[quad][2][lane] = o[0].z; other[quad][3][lane] = o[0].w;
       if (quad == 0) other_ml[lane] = make_float2(m, l);
