@@ -336,12 +336,75 @@ struct Layers {
   uint16_t* kv[2 * MK_PAGED_MAX_LAYERS];  // keys, values of each layer in turn
   int64_t page_stride, head_stride, token_stride;
   int32_t* status;
-  int hkv, n_pages, page_shift, lanes;  // lanes: 16-byte pieces of a head
+  int hkv, n_pages, page_shift, lanes, lane_shift;  // lanes: 16-byte pieces of a head, log2 of it
 };
 
 // ---------------------------------------------------------------- copies of pages
-// A CTA copies PC_ROWS rows (one head of one token) of one page, keys or values of
-// one layer: each thread has all its loads in flight at once.
+// Bound by HBM.  Where the tokens of a head lie end to end (or a token's heads and the
+// tokens) what is copied of a page is a few spans: a warp copies up to 64 KB of them
+// through shared memory with bulk copies, three warps an SM in turn.  (16 bytes a thread
+// and load, as below, spends 70% of the issue slots on addresses: 56 pages of 64
+// tokens in 32 layers 68 us, 55 with spans.)
+constexpr int PC_SPANS = 65536;  // bytes of a CTA
+
+__global__ void __launch_bounds__(32) paged_copy_spans_kernel(const __grid_constant__ Layers L, const int32_t* copies, int n, int groups, int per, int span,
+                                                              bool tokens_first) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ uint64_t bar;
+  __shared__ volatile int dead;
+  const int lane = threadIdx.x;
+  if (lane == 0) {
+    mbar_init(&bar, 1);
+    dead = 0;
+    fence_mbar_init();
+  }
+  grid_launch_dependents();
+  grid_wait_prior();
+  __syncwarp();
+  const int i = blockIdx.x / groups, s = (blockIdx.x - i * groups) * per + lane, page = 1 << L.page_shift;
+  const int from = copies[i], to = copies[n + i];
+  if (from == -1) return;
+  int tokens = copies[2 * n + i];
+  const bool bad = from < 0 || from >= L.n_pages || to < 0 || to >= L.n_pages;
+  if ((bad || tokens < 0 || tokens > page) && lane == 0) latch(L.status, MK_ERR_BOUNDS);
+  if (bad) return;
+  tokens = min(max(tokens, 0), page);
+  // this lane's span: a head's tokens, or `span` bytes of the tokens
+  const int64_t row = (int64_t)L.lanes * 16;
+  int64_t at, len;
+  if (tokens_first) {
+    at = (int64_t)s * span;
+    len = min((int64_t)span, tokens * row * L.hkv - at);
+  } else {
+    at = s * L.head_stride * 2;
+    len = s < L.hkv ? tokens * row : 0;
+  }
+  if (lane >= per || len < 0) len = 0;
+  const uint32_t mine = (uint32_t)len;
+  uint32_t all = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  if (all == 0) return;
+  uint8_t* base = reinterpret_cast<uint8_t*>(L.kv[blockIdx.y]);
+  uint8_t* buf = smem_raw + (int64_t)lane * span;
+  if (lane == 0) mbar_arrive_expect_tx(&bar, all);
+  __syncwarp();
+  if (mine) bulk_in(buf, base + from * L.page_stride * 2 + at, mine, &bar);
+  wait_phase(&bar, 0, &dead, L.status);
+  if (dead) {  // leave after the loads, none of which takes a millisecond, have landed
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {
+    }
+    return;
+  }
+  if (mine) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(base + to * L.page_stride * 2 + at), "r"(smem_u32(buf)), "r"(mine) : "memory");
+    asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
+  }
+}
+
+// Any layout: a row is one head of one token, and each thread has all its loads in
+// flight at once.
 constexpr int PC_COPY_THREADS = 256, PC_UNROLL = 4;
 
 __global__ void __launch_bounds__(PC_COPY_THREADS) paged_copy_kernel(const __grid_constant__ Layers L, const int32_t* copies, int n, int parts) {
@@ -359,6 +422,10 @@ __global__ void __launch_bounds__(PC_COPY_THREADS) paged_copy_kernel(const __gri
   uint16_t* base = L.kv[blockIdx.y];
   const uint16_t* src = base + from * L.page_stride;
   uint16_t* dst = base + to * L.page_stride;
+  if (tokens == 0) return;
+  // row / tokens by its reciprocal: the error, row 2^-32 at most, is below 1 / tokens (rows
+  // are below 2^24, tokens at most 2^8, and an exact quotient's error is none of below)
+  const uint32_t inv = 0xffffffffu / (uint32_t)tokens + 1;
   const int total = L.hkv * tokens * L.lanes, step = parts * PC_COPY_THREADS;
   for (int x0 = part * PC_COPY_THREADS + threadIdx.x; x0 < total; x0 += PC_UNROLL * step) {
     uint4 v[PC_UNROLL];
@@ -367,7 +434,7 @@ __global__ void __launch_bounds__(PC_COPY_THREADS) paged_copy_kernel(const __gri
     for (int k = 0; k < PC_UNROLL; ++k) {
       const int x = x0 + k * step;
       if (x < total) {
-        const int row = x / L.lanes, c = x - row * L.lanes, h = row / tokens, t = row - h * tokens;
+        const int row = x >> L.lane_shift, c = x & (L.lanes - 1), h = tokens == 1 ? row : (int)__umulhi((uint32_t)row, inv), t = row - h * tokens;
         at[k] = h * L.head_stride + t * L.token_stride + c * 8;
         v[k] = __ldcs(reinterpret_cast<const uint4*>(src + at[k]));
       }
@@ -471,6 +538,7 @@ int fill_layers(const mk_paged_cache* c, void* const* ks, void* const* vs, int n
   L->page_stride = c->page_stride; L->head_stride = c->head_stride; L->token_stride = c->token_stride;
   L->status = c->status;
   L->hkv = c->n_kv_heads; L->n_pages = c->n_pages; L->page_shift = paged_log2(c->page_size); L->lanes = c->head_dim / 8;
+  L->lane_shift = c->head_dim == 128 ? 4 : 3;
   return MK_OK;
 }
 
@@ -525,6 +593,34 @@ extern "C" int mk_paged_copy(const mk_paged_cache* c, void* const* ks, void* con
   if (!copies || !al4(copies) || n_copies < 0) return MK_ERR_INVALID_ARG;
   if (n_copies > MK_PAGED_MAX_REQUESTS) return MK_ERR_UNSUPPORTED;
   if (n_copies == 0) return MK_OK;
+  const int row = L.lanes * 16;
+  // spans: the heads' tokens, or the tokens' heads, end to end
+  const bool heads_first = c->token_stride == c->head_dim, tokens_first = !heads_first && c->head_stride == c->head_dim && c->token_stride == (int64_t)c->n_kv_heads * c->head_dim;
+  if (heads_first || tokens_first) {
+    const int64_t bytes = (int64_t)c->page_size * c->n_kv_heads * row;
+    const int span = heads_first ? c->page_size * row : (int)std::min<int64_t>(16384, bytes);
+    const int64_t spans = heads_first ? c->n_kv_heads : (bytes + span - 1) / span;
+    const int per = (int)std::min<int64_t>({32, PC_SPANS / span, spans});
+    const int64_t groups = (spans + per - 1) / per;
+    if (groups * n_copies <= 0x7fffffff) {
+      static std::atomic<uint64_t> ready{0};
+      int dev = 0;
+      cudaError_t e = cudaGetDevice(&dev);
+      if (e == cudaSuccess) e = paged_prepare((const void*)paged_copy_spans_kernel, PC_SPANS, 0, dev, &ready);
+      if (e != cudaSuccess) return paged_done(e);
+      cudaLaunchConfig_t cfg{};
+      cudaLaunchAttribute at{};
+      at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at.val.programmaticStreamSerializationAllowed = 1;
+      cfg.gridDim = dim3((int)(groups * n_copies), 2 * n_layers);
+      cfg.blockDim = dim3(32);
+      cfg.dynamicSmemBytes = per * span;
+      cfg.stream = (cudaStream_t)stream;
+      cfg.attrs = &at;
+      cfg.numAttrs = 1;
+      return paged_done(cudaLaunchKernelEx(&cfg, paged_copy_spans_kernel, L, copies, n_copies, (int)groups, per, span, tokens_first));
+    }
+  }
   const int64_t pieces = (int64_t)c->n_kv_heads * c->page_size * L.lanes;
   const int parts = (int)std::min<int64_t>(64, (pieces + PC_COPY_THREADS * PC_UNROLL - 1) / (PC_COPY_THREADS * PC_UNROLL));
   cudaLaunchConfig_t cfg{};
