@@ -25,6 +25,13 @@
 // lives in TMEM, is seldom rescaled.
 // No wait on O is needed for that: S of block j is issued behind P V of block
 // j - 1, so when S is complete O is at rest.
+//
+// The kernel's other forms take trees of drafted tokens, whose rows see the cached keys
+// and the new ones that their masks name: the masks change the blocks that hold new
+// tokens, as four words of bits a row.  Bound by HBM where a tile has one half (a block
+// of 128-wide heads takes a half 1.4 us, HBM 1.5: 2 x 16 tokens over 128K keys 171 us,
+// 6.3 TB/s), else by the softmax as above (1.8 us).  Forms, their rules and figures
+// stand at is_pair, paged_chunk_clusters and the join.
 #include "mk_paged_dev.cuh"
 #include "mk_paged_tc.cuh"
 #include "mk_tmap.h"
