@@ -166,6 +166,7 @@ struct VerifyCtl {  // what the first CTA asks of the others
 struct VerifySmem {
   int up[MK_TREE_MAX_NODES], tok[MK_TREE_MAX_NODES], path[MK_TREE_MAX_NODES];
   float p[MK_TREE_MAX_NODES], q[MK_TREE_MAX_NODES], u[MK_TREE_MAX_NODES];
+  uint32_t first[MK_TREE_MAX_NODES / 32];  // tokens that stand if none of their siblings has been refused
   int gone[MK_TREE_MAX_NODES];      // tokens found that were refused at this node, and their units
   u64 gone_units[MK_TREE_MAX_NODES];
   u64 warp_sum[TV_WARPS], total, scan[TV_WARPS];
@@ -296,10 +297,10 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const Verify
       }
       k = 0;
     }
-    for (int i = tid; i < k; i += TV_THREADS) {
+    for (int i = tid; i < ((k + 31) & ~31); i += TV_THREADS) {
       int up = -1, x = -1;
       float p = 0.f, q = 0.f, u = 0.f;
-      if (i > 0) {
+      if (i > 0 && i < k) {
         up = P.parents[c0 + i];
         x = P.tokens[c0 + i];
         u = P.u[c0 + i];
@@ -311,8 +312,11 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const Verify
           if (P.q) q = probability(P.q[(c0 + up) * P.q_stride + x]);
         }
       }
+      u = u >= 1.f ? 0x1.fffffep-1f : fmaxf(u, 0.f);
       S.up[i] = up; S.tok[i] = x; S.p[i] = p; S.q[i] = q;
-      S.u[i] = u >= 1.f ? 0x1.fffffep-1f : fmaxf(u, 0.f);
+      S.u[i] = u;
+      const uint32_t m = __ballot_sync(0xffffffffu, (double)u * (P.q ? (double)q : 1.0) < (double)p);
+      if (lane == 0) S.first[i / 32] = m;
     }
     __syncthreads();
     if (warp == 0 && k > 0) at = next_child(S.up, k, 0, 1, lane);
@@ -328,7 +332,9 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const Verify
       while (at < k) {
         const int i = at, x = S.tok[i];
         bool again = false, stands;
-        if (P.q) {
+        if (P.q ? sum_z == 0.0 : n_gone == 0) {
+          stands = S.first[i / 32] >> (i & 31) & 1u;
+        } else if (P.q) {
           const double left = fmax((double)S.p[i] - sum_z * (double)S.q[i], 0.0);
           stands = (double)S.u[i] * (double)S.q[i] * z < left;
         } else {
