@@ -674,7 +674,7 @@ int mk_paged_fork(const int32_t *table, int n, const int32_t *lens, const int32_
 
 /* Copy the first copies[2][i] tokens of page copies[0][i] to page copies[1][i], keys
  * and values of all kv heads, in n_layers caches of the same shape: `cache` with k
- * and v replaced by ks[l], vs[l] (host arrays, read during the call).  A pair with a
+ * and v replaced by ks[l], vs[l] (host arrays, read during the call; no two the same).  A pair with a
  * source of -1 is none.  Pages that are not the cache's and more tokens than a page
  * has are latched in cache->status (the pair is left out, the tokens clamped).  No
  * page may be the target of two pairs or the target of one and the source of

@@ -253,6 +253,8 @@ def test_python_refusals_of_pages():
     other = mk.PagedCache(*(torch.zeros(4, 2, 32, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)), n_q_heads=2)
     with pytest.raises(ValueError):
         mk.PagedLayers([layers.caches[0], other])
+    with pytest.raises(ValueError):
+        mk.PagedLayers([layers.caches[0], layers.caches[1], layers.caches[0]])
     for c in (ints([1, 2, 3]), ints(np.zeros((2, 4))), ints(np.zeros((3, 4))).long(), ints(np.zeros((4, 3))).t()):
         with pytest.raises(ValueError):
             layers.copy(c)

@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   volatile int* dead = reinterpret_cast<volatile int*>(ofull + 2);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(const_cast<int*>(dead) + 1);
   int* joined = reinterpret_cast<int*>(tslot + 1);  // [4] a cluster's tile: rows, first token, blocks, head
+  uint64_t* pdone = reinterpret_cast<uint64_t*>(joined + 4);  // both halves have seen the loads of a pair
+  static_assert((2 * ST + 2 + 2 * C::SLOTS + 6) * 8 + 8 + 16 + 8 <= C::o_pre - C::o_bar, "barriers");
   Tile* meta = reinterpret_cast<Tile*>(smem + C::o_meta);
   const Kept kept(smem + C::o_pre, P.n);
   int* pre = kept.pre;
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       mbar_init(&pfull[h], 4);
       mbar_init(&ofull[h], 1);
     }
+    if (PAIRS) mbar_init(pdone, 2);
     *dead = 0;
     fence_mbar_init();
   }
@@ -450,6 +453,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       const uint64_t dv = sdesc_sw128_mn(smem_u32(smem + C::o_kv), 16384u);
       const uint32_t t_s = T_S + 128u * h, t_o = T_O + 128u * h;
       uint32_t blkn = 0, pn = 0, qn = 0;  // blocks loaded, P's and tiles seen
+      uint32_t pairs = 0, pairs_seen = 0;
       int slot = 0;
       uint32_t mphase = 0;
       auto kst = [](uint32_t b) { return (2 * b) % ST; };
@@ -475,10 +479,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         wait_phase(qfull, qn & 1, dead, P.status);
         ++qn;
         if (PAIRS && pair) {
-          // A half's products are those of its own head's blocks, every other one.  A
-          // stage is released twice by the one that used it; a phase that a half does
-          // not see cannot be taken for another, since a stage that it uses is not
-          // filled again before it has.
+          // A half's products are those of its own head's blocks, every other one; a
+          // stage is released twice by the one that used it.  A pair's blocks are even
+          // in number, and so are the stages: while tiles are pairs a half always has
+          // the same stages and sees all their phases.
           const uint32_t end = blkn + 2 * nblk;
           uint32_t b = blkn + h;
           blkn = end;
@@ -518,7 +522,18 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             }
           }
           if (*dead) break;
+          if (lane == 0) mbar_arrive(pdone);
+          ++pairs;
           continue;
+        }
+        // Behind a pair a half may come to a stage that the other one had: not before
+        // that one has seen its loads land, or a wait for this phase could be met by
+        // the one before.  (The other is at most a tile behind: its queries' room was
+        // needed for this one's.)
+        if (PAIRS && pairs != pairs_seen) {
+          wait_phase(pdone, (pairs - 1) & 1, dead, P.status);
+          pairs_seen = pairs;
+          if (*dead) break;
         }
         if (!mine) {  // a tile of one half: see every phase, use nothing
           if (lane == 0) mbar_arrive(qempty);

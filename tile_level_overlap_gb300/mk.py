@@ -862,6 +862,7 @@ class PagedLayers(_OnDevice):
         for c in caches:
             _need(c.device == first.device and c.dtype == first.dtype and c.k.shape == first.k.shape
                   and c.k.stride() == first.k.stride(), "caches of one shape, type and device")
+        _need(len({_ptr(t) for c in caches for t in (c.k, c.v)}) == 2 * len(caches), "caches: none twice")
         self.caches, self.n = caches, len(caches)
         row = ctypes.c_void_p * self.n
         self._ks, self._vs = row(*[_ptr(c.k) for c in caches]), row(*[_ptr(c.v) for c in caches])
