@@ -139,6 +139,34 @@ inline cudaError_t paged_launch_clusters(void (*kernel)(P...), int grid, int clu
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
+// Clusters of `ctas` (<= 16) CTAs of a kernel that the device holds at once; asked once
+// for each size, `known` keeps one more than the number.
+inline int paged_clusters_at_once(const void* kernel, int threads, int smem, int device, int ctas, std::atomic<int> (&known)[64][17]) {
+  std::atomic<int>* mine = device < 64 ? &known[device][ctas] : nullptr;
+  int n = mine ? mine->load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if ((smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) ||
+        (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    ++n;
+    if (mine) mine->store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
 cudaError_t paged_few_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
                              bool bf, cudaStream_t st);
 cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,

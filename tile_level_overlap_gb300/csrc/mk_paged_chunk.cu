@@ -1078,34 +1078,10 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
   }
 }
 
-// Clusters of `ctas` CTAs that the device holds at once (asked once for each size).
 template <int HD, bool BF>
 int clusters_at_once(int device, int ctas) {
   static std::atomic<int> known[64][17];
-  std::atomic<int>* mine = device < 64 ? &known[device][ctas] : nullptr;
-  int n = mine ? mine->load(std::memory_order_relaxed) : 0;  // one more than the number
-  if (n == 0) {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ctas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(PC_THREADS);
-    cfg.dynamicSmemBytes = ChunkCfg<HD>::most;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const void* kernel = (const void*)paged_chunk_kernel<HD, BF, true, true>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<HD>::most) != cudaSuccess ||
-        (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
-        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      n = 0;
-    }
-    ++n;
-    if (mine) mine->store(n, std::memory_order_relaxed);
-  }
-  return n - 1;
+  return paged_clusters_at_once((const void*)paged_chunk_kernel<HD, BF, true, true>, PC_THREADS, ChunkCfg<HD>::most, device, ctas, known);
 }
 
 template <int HD, bool BF, bool TREE, bool CLUSTERS>

@@ -85,9 +85,9 @@ __global__ void __launch_bounds__(TT_THREADS) paged_tree_kernel(const TreeParams
 // which none is 64 bits wide.  p - S q has its parts subtracted, with the product's
 // rounding error from a second multiply-add.  (64-bit whole numbers, 40 instructions a
 // pair of values, took 32 trees 68 us instead of 39.)  Bound by latency for few requests
-// (one of five rows of 128256 7.9 us), by HBM (the rows that are drawn from) and these
-// instructions for many: 64 chains without draft probabilities 12.9 us, 32 trees of 17
-// to 32 tokens of 151936, in up to five passes, 38.5 us.  256 threads with four
+// (one of five rows of 128256 7.5 us), by HBM (the rows that are drawn from) and these
+// instructions for many: 64 chains without draft probabilities 12.7 us, 32 trees of 17
+// to 32 tokens of 151936, in up to five passes, 38.3 us.  256 threads with four
 // vectors of each row in flight, two CTAs an SM: 512 with two 51 us, with eight in
 // flight 39.2.
 constexpr int TV_THREADS = 256, TV_WARPS = TV_THREADS / 32;
@@ -497,39 +497,15 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const Verify
   cluster_sync();  // no CTA's shared memory is read any more
 }
 
-// CTAs of a request: as many as all requests' fit the GPU at once (two an SM).  16 are
-// more than a device has to take in a cluster; it is asked once.
-int verify_cluster_most(int device) {
-  static std::atomic<uint64_t> known{0}, wide{0};
-  const uint64_t bit = 1ull << (device & 63);
-  if (!(known.load(std::memory_order_acquire) & bit) || device >= 64) {
-    int n = 0;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 16;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(16);
-    cfg.blockDim = dim3(TV_THREADS);
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const bool ok = cudaFuncSetAttribute(tree_verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                    cudaOccupancyMaxActiveClusters(&n, tree_verify_kernel, &cfg) == cudaSuccess && n > 0;
-    if (!ok) cudaGetLastError();
-    if (device >= 64) return ok ? 16 : 8;
-    if (ok) wide.fetch_or(bit, std::memory_order_relaxed);
-    known.fetch_or(bit, std::memory_order_release);
-  }
-  return wide.load(std::memory_order_relaxed) & bit ? 16 : 8;
-}
-
+// CTAs of a request: as many as all requests' fit the GPU at once (two an SM), not
+// powers of two alone (40 trees of 17 to 24 tokens of 128256 34.7 against 40.3 us, 80
+// chains of 5 rows 22.6 against 27.4).
 cudaError_t verify_launch(const VerifyParams& p, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  static std::atomic<int> known[64][17];
+  int dev = 0, cluster = 16;
+  const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int cluster = verify_cluster_most(dev);
-  while (cluster > 1 && p.n * cluster > 2 * sms) cluster /= 2;
+  while (cluster > 1 && p.n > paged_clusters_at_once((const void*)tree_verify_kernel, TV_THREADS, 0, dev, cluster, known)) --cluster;
   return paged_launch_clusters(tree_verify_kernel, p.n * cluster, cluster, TV_THREADS, 0, st, p);
 }
 
