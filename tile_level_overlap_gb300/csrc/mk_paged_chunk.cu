@@ -28,10 +28,10 @@
 //
 // The kernel's other forms take trees of drafted tokens, whose rows see the cached keys
 // and the new ones that their masks name: the masks change the blocks that hold new
-// tokens, as four words of bits a row.  Bound by HBM where a tile has one half (a block
-// of 128-wide heads takes a half 1.4 us, HBM 1.5: 2 x 16 tokens over 128K keys 171 us,
-// 6.3 TB/s), else by the softmax as above (1.8 us).  Forms, their rules and figures
-// stand at is_pair, paged_chunk_clusters and the join.
+// tokens, as four words of bits a row.  Bound by HBM where tiles have one half
+// (2 x 16 tokens over 128K keys 169 us, 6.4 TB/s), else by the softmax as above (1.8 us
+// a block, HBM 1.5).  Forms, their rules and figures stand at the kernel, is_pair,
+// paged_chunk_clusters and the join.
 #include "mk_paged_dev.cuh"
 #include "mk_paged_tc.cuh"
 #include "mk_tmap.h"
@@ -61,7 +61,7 @@ struct ChunkCfg {
   static constexpr int o_kv = 2 * TILE;                    // after the queries' halves
   static constexpr int o_meta = o_kv + STAGES * TILE;
   static constexpr int o_bar = o_meta + SLOTS * 64;
-  static constexpr int o_pre = o_bar + 256;
+  static constexpr int o_pre = o_bar + 320;
   static constexpr int total(int n) { return o_pre + Kept::bytes(n); }
   static constexpr int most = o_pre + KEPT_MOST;
 };
@@ -90,10 +90,10 @@ __device__ __forceinline__ bool is_tree(const PagedAttnParams& P, const Request&
 
 // Trees of at most 128 rows go in pairs of kv heads, where heads are 64 wide and of even
 // number: a tile's halves are the rows of two heads, whose blocks take turns in the
-// ring.  Alone a half's softmax and products take 1.1 us a block, in turn, of which
-// HBM needs 0.73 (32 requests of 13 tokens over 2048 keys 47.6 us alone, 37.7 in
-// pairs).  Of 128-wide heads HBM needs 1.47 and the half 1.4: pairs only make the parts
-// larger (32 of 32 over 1280 48.4 alone, 54.8 in pairs).
+// ring.  Alone a half's softmax takes more than the 0.73 us that HBM needs of a block
+// (32 requests of 13 tokens over 2048 keys 43.2 us alone, with the halves' S in turn,
+// 37.4 in pairs).  Of 128-wide heads HBM needs 1.47: pairs only make the parts larger
+// (32 of 32 over 1280 48.4 alone, without turns, 54.8 in pairs).
 template <bool PAIRS>
 __device__ __forceinline__ bool is_pair(const PagedAttnParams& P, const Request& q, int TS) {
   return PAIRS && (P.hkv & 1) == 0 && q.add <= TS;
@@ -133,15 +133,24 @@ __device__ __forceinline__ void quad_swap(uint32_t (&a)[4], uint32_t (&b)[4], in
 }
 
 // TREE: rows of requests with masks see the cached keys and the new ones that their
-// masks name.  CLUSTERS: a cluster for each tile instead of runs of all tiles' blocks.
-template <int HD, bool BF, bool TREE, bool CLUSTERS>
+// masks name.  FORM: runs of all tiles' blocks, the same where no tile has two halves, or
+// a cluster for each tile.  In the last two a tile of one half has the S of both in turn:
+// the next block's product is there when a block's softmax ends, which else takes a
+// chain of 1.4 us a block of 128-wide heads (32 x 32 tokens over 8192 keys 186.4 -> 182.7
+// us, over 1280 48.9 -> 47.2, one of 32 over 4096 14.0 -> 13.2; 20 heads on 5 of 64, 32 x
+// 13 over 2048 35.6 -> 31.6).  A block's P may then be written before that of the one
+// before has been seen, so P has barriers in turn too; a rescaled O waits for the last
+// P V.  Where tiles of both kinds meet, the second half's S would have to change hands
+// (32 requests of 1 to 64 tokens 63.2 -> 64.8 us).
+enum { RUNS, RUNS_OF_HALVES, CLUSTERS };
+template <int HD, bool BF, bool TREE, int FORM>
 __global__ void __launch_bounds__(PC_THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedAttnParams P,
                        const __grid_constant__ PagedParts W) {
   using C = ChunkCfg<HD>;
   constexpr int ST = C::STAGES;
-  constexpr bool PAIRS = TREE && !CLUSTERS && HD == 64;
+  constexpr bool PAIRS = TREE && FORM == RUNS && HD == 64, TURNS = FORM != RUNS;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::o_bar);
   uint64_t* empty = full + ST;
@@ -156,7 +165,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(const_cast<int*>(dead) + 1);
   int* joined = reinterpret_cast<int*>(tslot + 1);  // [4] a cluster's tile: rows, first token, blocks, head
   uint64_t* pdone = reinterpret_cast<uint64_t*>(joined + 4);  // both halves have seen the loads of a pair
-  static_assert((2 * ST + 2 + 2 * C::SLOTS + 6) * 8 + 8 + 16 + 8 <= C::o_pre - C::o_bar, "barriers");
+  uint64_t* sturn = pdone + 1;  // blocks in turns: S of turn b complete
+  uint64_t* oturn = sturn + 2;  // P V of turn b complete
+  uint64_t* pturn = oturn + 2;  // P of turn b written
+  static_assert((2 * ST + 2 + 2 * C::SLOTS + 6) * 8 + 8 + 16 + 8 + 48 <= C::o_pre - C::o_bar, "barriers");
   Tile* meta = reinterpret_cast<Tile*>(smem + C::o_meta);
   const Kept kept(smem + C::o_pre, P.n);
   int* pre = kept.pre;
@@ -184,6 +196,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       mbar_init(&ofull[h], 1);
     }
     if (PAIRS) mbar_init(pdone, 2);
+    if (TURNS)
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sturn[b], 1);
+        mbar_init(&oturn[b], 1);
+        mbar_init(&pturn[b], 4);
+      }
     *dead = 0;
     fence_mbar_init();
   }
@@ -196,7 +214,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   // written before that one's own wait, but a grid is promised to see it only by
   // waiting itself: mixed step of 27 requests 46.8 us, with the wait at the end 44.5.)
   grid_wait_prior();
-  constexpr bool clustered = CLUSTERS;
+  constexpr bool clustered = FORM == CLUSTERS;
   if (tid == 0 && !clustered) W.desc[blockIdx.x].parts = 0;
 
   // In clusters: this one's tile, of which the CTA takes blocks [cb0, cb1).
@@ -459,12 +477,16 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       auto kst = [](uint32_t b) { return (2 * b) % ST; };
       auto kph = [](uint32_t b) { return ((2 * b) / ST) & 1; };
       // S from the K block in stage st
-      auto s_product = [&](uint32_t st) {
+      uint32_t turn = 0;
+      auto s_product_to = [&](uint32_t t, uint32_t st) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint32_t off = ((uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u) >> 4;
-          tc_mma(t_s, dq + off, dk + (st * (C::TILE / 16) + off), id_s, kk != 0);
+          tc_mma(t, dq + off, dk + (st * (C::TILE / 16) + off), id_s, kk != 0);
         }
+      };
+      auto s_product = [&](uint32_t st) {
+        s_product_to(t_s, st);
         tc_commit(&sfull[h]);
       };
       for (;;) {
@@ -472,6 +494,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (*dead) break;
         const int nblk = meta[slot].nblk;
         const bool mine = h == 0 || meta[slot].ntok > TS, pair = PAIRS && meta[slot].pair;
+        const bool in_turn = TURNS && meta[slot].ntok <= TS;
         __syncwarp();
         if (lane == 0) mbar_arrive(&mempty[slot]);
         if (nblk == 0) break;
@@ -546,6 +569,45 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           if (*dead) break;
           continue;
         }
+        if (TURNS && in_turn) {
+          auto s_turn = [&](int j) {
+            const uint32_t st = kst(blkn + j);
+            wait_phase(&full[st], kph(blkn + j), dead, P.status);
+            if (*dead) return;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t b = (turn + j) & 1;
+              s_product_to(T_S + 128u * (j & 1), st);
+              tc_commit(&sturn[b]);
+              tc_commit(&empty[st]);
+              if (j + 1 == nblk) tc_commit(qempty);
+            }
+            __syncwarp();
+          };
+          s_turn(0);
+          if (nblk > 1 && !*dead) s_turn(1);
+          for (int j = 0; j < nblk; ++j) {
+            const uint32_t vst = kst(blkn + j) + 1, b = (turn + j) & 1;
+            wait_phase(&full[vst], kph(blkn + j), dead, P.status);
+            wait_phase(&pturn[b], ((turn + j) >> 1) & 1, dead, P.status);
+            if (*dead) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_ta(t_o, T_S + 128u * (j & 1) + 8u * kk, dv + (vst * (C::TILE / 16) + 128u * kk), id_o, (j | kk) != 0);
+              tc_commit(&oturn[b]);
+              tc_commit(&empty[vst]);
+              if (j + 1 == nblk) tc_commit(&ofull[h]);
+            }
+            __syncwarp();
+            if (j + 2 < nblk) s_turn(j + 2);
+          }
+          if (*dead) break;
+          blkn += nblk;
+          turn += nblk;
+          continue;
+        }
         wait_phase(&full[kst(blkn)], kph(blkn), dead, P.status);
         tc_fence_after();
         if (elect_one()) {
@@ -592,12 +654,14 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     setmaxnreg_inc<PC_REGS_SOFT>();
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_t = T_S + 128u * half + lanes, o_t = T_O + 128u * half + lanes;
+    const uint32_t s_t0 = T_S + 128u * half + lanes;
+    uint32_t s_t = s_t0;
+    const uint32_t o_t = T_O + 128u * half + lanes;
     const int tok_in = P.token_of(row), hq_in = row - tok_in * P.rep;
     const float cs = fabsf(P.scale) * 1.4426950408889634f;
     const bool neg = P.scale < 0.f;
     constexpr float top = BF ? 0.f : PC_TOP_FP16;
-    uint32_t blkn = 0, sn = 0, on = 0;
+    uint32_t blkn = 0, sn = 0, on = 0, turn = 0;
     int slot = 0;
     uint32_t mphase = 0;
     int held = -1;  // in a cluster: this thread's row of the tile, its maximum and sum
@@ -655,6 +719,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       float mx = -INFINITY, l = 0.f;
       const uint32_t blk_step = pair ? 2 : 1, tile_end = blkn + (pair ? 2 * m.nblk : m.nblk);
       if (pair) blkn += half;
+      // in turns: a buffer and barriers of every other block
+      const uint32_t two = TURNS && m.ntok <= TS ? 1 : 0;
+      uint64_t *s_bar = two ? sturn : &sfull[half], *p_bar = two ? pturn : &pfull[half];
+      uint32_t count = two ? turn : sn;
       for (int j = 0; j < m.nblk; ++j, blkn += blk_step) {
         const int key0 = m.key0 + 128 * j;
         uint32_t named[4] = {0, 0, 0, 0};  // columns of the block that the row's mask names
@@ -674,8 +742,13 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             for (int i = 0; i < 4; ++i) named[i] = __funnelshift_r(w[i], w[i + 1], d & 31);
           }
         }
-        wait_phase(&sfull[half], sn & 1, dead, P.status);
-        ++sn;
+        if constexpr (TURNS) {
+          s_t = s_t0 + ((j & two) << 7);
+          wait_phase(&s_bar[count & two], (count >> two) & 1, dead, P.status);
+        } else {
+          wait_phase(&sfull[half], sn & 1, dead, P.status);
+          ++sn;
+        }
         tc_fence_after();
         float s[128];
         tmem_ld128(s_t, s);
@@ -721,6 +794,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           l *= a;
           mx = mn;
           if (j > 0) {
+            if (TURNS && two) {  // (S of this block was issued before P V of the last)
+              wait_phase(&oturn[(count - 1) & 1], ((count - 1) >> 1) & 1, dead, P.status);
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int x = 0; x < HD; x += 32) {
               float o[32];
@@ -783,8 +860,15 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[half]);
+        if constexpr (TURNS) {
+          if (lane == 0) mbar_arrive(&p_bar[count & two]);
+          ++count;
+        } else {
+          if (lane == 0) mbar_arrive(&pfull[half]);
+        }
       }
+      if (TURNS && two) turn = count;
+      else if (TURNS) sn = count;
       blkn = tile_end;
       wait_phase(&ofull[half], on & 1, dead, P.status);
       ++on;
@@ -1081,10 +1165,10 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
 template <int HD, bool BF>
 int clusters_at_once(int device, int ctas) {
   static std::atomic<int> known[64][17];
-  return paged_clusters_at_once((const void*)paged_chunk_kernel<HD, BF, true, true>, PC_THREADS, ChunkCfg<HD>::most, device, ctas, known);
+  return paged_clusters_at_once((const void*)paged_chunk_kernel<HD, BF, true, CLUSTERS>, PC_THREADS, ChunkCfg<HD>::most, device, ctas, known);
 }
 
-template <int HD, bool BF, bool TREE, bool CLUSTERS>
+template <int HD, bool BF, bool TREE, int FORM>
 cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, cudaStream_t st) {
   CUtensorMap tq, tk, tv;
   if (!make_page_tmap(&tk, kv.k, kv, HD, 128, 1, BF) || !make_page_tmap(&tv, kv.v, kv, HD, 128, 1, BF) ||
@@ -1092,22 +1176,22 @@ cudaError_t launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts
     return cudaErrorInvalidValue;
   // the register split needs the block to be launched with what it counts on
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF, TREE, CLUSTERS>,
+  const cudaError_t e = paged_prepare((const void*)paged_chunk_kernel<HD, BF, TREE, FORM>,
                                       ChunkCfg<HD>::most, PC_REGS, p.device, &ready);
   if (e != cudaSuccess) return e;
-  if constexpr (CLUSTERS)
-    return paged_launch_clusters(paged_chunk_kernel<HD, BF, TREE, CLUSTERS>, p.cluster_tiles * p.cluster, p.cluster, PC_THREADS,
+  if constexpr (FORM == CLUSTERS)
+    return paged_launch_clusters(paged_chunk_kernel<HD, BF, TREE, FORM>, p.cluster_tiles * p.cluster, p.cluster, PC_THREADS,
                                  ChunkCfg<HD>::total(p.n), st, tq, tk, tv, p, w);
   // behind the few-row kernel it is set up while that one ends; alone it is launched
   // behind the whole of what precedes (8192-token prompt 363 against 368 us)
-  return paged_launch_if(TREE || p.few_rows > 0, paged_chunk_kernel<HD, BF, TREE, CLUSTERS>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
+  return paged_launch_if(TREE || p.few_rows > 0, paged_chunk_kernel<HD, BF, TREE, FORM>, w.ctas, PC_THREADS, ChunkCfg<HD>::total(p.n), st,
                          tq, tk, tv, p, w);
 }
 
-template <bool TREE, bool CLUSTERS>
+template <bool TREE, int FORM>
 cudaError_t launch_type(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d, bool bf, cudaStream_t st) {
-  if (d == 128) return bf ? launch<128, true, TREE, CLUSTERS>(p, kv, w, st) : launch<128, false, TREE, CLUSTERS>(p, kv, w, st);
-  return bf ? launch<64, true, TREE, CLUSTERS>(p, kv, w, st) : launch<64, false, TREE, CLUSTERS>(p, kv, w, st);
+  if (d == 128) return bf ? launch<128, true, TREE, FORM>(p, kv, w, st) : launch<128, false, TREE, FORM>(p, kv, w, st);
+  return bf ? launch<64, true, TREE, FORM>(p, kv, w, st) : launch<64, false, TREE, FORM>(p, kv, w, st);
 }
 
 }  // namespace
@@ -1115,21 +1199,27 @@ cudaError_t launch_type(const PagedAttnParams& p, const PagedKv& kv, const Paged
 cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, const PagedParts& w, int d,
                                bool bf, cudaStream_t st) {
   if (p.masks) {
-    if (p.cluster) return launch_type<true, true>(p, kv, w, d, bf, st);
-    return launch_type<true, false>(p, kv, w, d, bf, st);
+    if (p.cluster) return launch_type<true, CLUSTERS>(p, kv, w, d, bf, st);
+    // (heads of 64 of even number go in pairs)
+    if (p.max_new <= 128 / p.rep && (d == 128 || (p.hkv & 1))) return launch_type<true, RUNS_OF_HALVES>(p, kv, w, d, bf, st);
+    return launch_type<true, RUNS>(p, kv, w, d, bf, st);
   }
-  return launch_type<false, false>(p, kv, w, d, bf, st);
+  return launch_type<false, RUNS>(p, kv, w, d, bf, st);
 }
 
 // Few tiles over few keys: a cluster for each, of as many CTAs as the device holds at
 // once for all, joined in their shared memory (a lone request of 32 tokens over 4096
-// keys, 8 kv heads of 128, 14.3 against 16.6 us of runs over all SMs, parts in memory
-// and the join's launch; 16 of them over 512 keys, a CTA a tile, 15.7 against 23.1).
+// keys, 8 kv heads of 128, 13.2 against 17.2 us of runs over all SMs, parts in memory
+// and the join's launch; 16 of them over 512 keys, a CTA a tile, 14.6 against 24.6).
 // The keys that a tile may have are bounded by the table's width.  Past 8 blocks a
-// CTA the SMs that no cluster fills cost more than the join (over 16384 keys 26.3
-// against 25.4), with tiles of two halves, whose exchange is twice as long, past 3
-// (2 x 64 tokens over 4096 keys 27.2 against 25.8; 64 over 4096 19.4, 19.6); a CTA a
-// tile has nothing to exchange.
+// CTA the SMs that no cluster fills, and requests that are shorter than the longest,
+// cost what the join does (16 CTAs of 12 blocks 29.9 against 30.6 us, 9 of 8 25.4, 25.0);
+// with up to 6 CTAs, whose exchange is shorter, and 128-wide heads past 12 (4 requests of
+// 32 tokens over 6000 keys 27.4, 31.2; over 50 to 6000 24.8, 26.2; 8 over 50 to 3000 25.9,
+// 26.2, to 4000 28.2, 26.9).  With tiles of two halves, whose exchange is twice as
+// long, past 3 (16 CTAs of 4 blocks 26.1, 23.7), of up to 6 CTAs past 4 (4 requests of 64
+// tokens over 2000 keys 22.9, 26.8; 5 over 1456 24.3, 26.4, over 2992 34.5, 33.7); a CTA a tile
+// has nothing to exchange (10 requests of 32 tokens over 2000 keys 26.4, 30.5).
 void paged_chunk_clusters(PagedAttnParams* p, int d, bool bf) {
   const int tt = 2 * (128 / p->rep);
   const int64_t tiles = (int64_t)p->n * p->hkv * (((int64_t)p->max_new + tt - 1) / tt);
@@ -1140,7 +1230,8 @@ void paged_chunk_clusters(PagedAttnParams* p, int d, bool bf) {
     const int most = d == 128 ? (bf ? clusters_at_once<128, true>(p->device, c) : clusters_at_once<128, false>(p->device, c))
                               : (bf ? clusters_at_once<64, true>(p->device, c) : clusters_at_once<64, false>(p->device, c));
     if (tiles > most) continue;
-    const int64_t most_blocks = c == 1 ? 16 : (int64_t)p->max_new * p->rep > 128 ? 3 * c : 8 * c;
+    const bool halves = (int64_t)p->max_new * p->rep > 128, small = c <= 6;
+    const int64_t most_blocks = c == 1 ? 16 : c * (halves ? small ? 4 : 3 : small && d == 128 ? 12 : 8);
     if (blocks <= most_blocks) {
       p->cluster = c;
       p->cluster_tiles = (int)tiles;
