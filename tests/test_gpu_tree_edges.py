@@ -335,3 +335,46 @@ def test_steps_end_to_end_without_waiting(workspace):
         run(outs[1], False)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("ctx,new,hq,hkv,d,page,typ,wide", [
+    # tiles of one half in runs: several of odd and even numbers of blocks, lone blocks among them; in clusters; tiles of two halves; pairs of heads
+    ([5000, 300, 60, 0, 9000], [32, 20, 3, 1, 32], 32, 8, 128, 16, "bf16", True), ([20000] * 2 + [100] * 7, [8] * 9, 40, 5, 128, 64, "fp16", True),
+    ([9000, 200, 3000], [13, 30, 2], 20, 5, 64, 16, "bf16", True), ([700] * 40, [25] * 40, 12, 3, 64, 32, "fp16", True),
+    ([4096], [32], 32, 8, 128, 16, "bf16", False), ([1500, 90], [30, 32], 8, 2, 64, 16, "fp16", False), ([3000], [64], 16, 4, 128, 16, "bf16", False),
+    ([5000, 300], [64, 40], 32, 8, 128, 16, "bf16", True), ([5000, 300], [30, 20], 32, 8, 64, 16, "bf16", True)])
+def test_maxima_that_grow_with_every_block(ctx, new, hq, hkv, d, page, typ, wide, workspace):
+    s = trees.make_tree(ctx, new, -(-max(new) // 32), hq, hkv, d, page, TYPES[typ], seed=len(ctx) + d, pad=1, masks="trees")
+    # a head's scores grow by more than 2^8 a block of 128 keys, or fall with every other one
+    s["q"][:, :, 0] = 8.0
+    s["q"][:, 1::3, 0] = -8.0
+    for r, kv in enumerate(s["kv"]):
+        for j in range(-(-int(kv) // page)):
+            p, m = int(s["table"][r, j]), min(page, int(kv) - j * page)
+            s["k"][p, :, :m, 0] = (16.0 * (j * page // 128)) % 1024
+    trees.check_tree(widen(s, 1 << 14 if page == 16 else 6000) if wide else s, workspace=workspace)
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verification_in_batches_of_every_size(drawn):
+    # clusters of 16 CTAs down to one: the requests of a batch are eight, in turn
+    r, vocab, k = random.Random(8), 20011, 9
+    forest = [trees.grow(r, k, width=3) for _ in range(8)]
+    g = torch.Generator(device=DEV).manual_seed(2)
+    p, q = (torch.softmax(3 * torch.randn(8 * k, vocab, generator=g, device=DEV), -1) for _ in range(2))
+    q = 0.5 * p + 0.5 * q
+    up = torch.tensor([k * i + max(x, 0) for i, t in enumerate(forest) for x in t], device=DEV)
+    tokens = torch.multinomial(q[up], 1, generator=g)[:, 0].to(torch.int32)
+    u, ul = torch.rand(8 * k, generator=g, device=DEV), torch.rand(8, generator=g, device=DEV)
+    first = None
+    for n in (8, 1, 2, 17, 19, 20, 21, 23, 25, 27, 30, 33, 40, 45, 51, 61, 70, 77, 101, 110, 152, 153, 305):
+        of = torch.arange(n, device=DEV) % 8
+        rows = (of[:, None] * k + torch.arange(k, device=DEV)).reshape(-1)
+        batch = mk.PagedBatch(ints(np.zeros((n, 1))), ints(np.arange(n + 1) * k), ints([k] * n), page_size=16, max_new=k)
+        outs = [ints([9] * (n * k)), ints([9] * (n * k)), ints([9] * n), ints([9] * n)]
+        mk.DraftTree(batch, ints([x for i in range(n) for x in forest[i % 8]])).verify(
+            tokens[rows], p[rows], u[rows], ul[of], *outs, draft_probs=q[rows] if drawn else None)
+        outs = [x.view(n, -1) for x in outs]
+        first = first or outs
+        for x, y in zip(outs, first):
+            assert torch.equal(x, y[of])
