@@ -300,14 +300,17 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     setmaxnreg_dec<PC_REGS_REST>();
     const int boxt = min(128, 1 << P.page_shift), nbox = 128 / boxt;
     // page of this lane's box of a block; -1 where no row of the request sees any of it
-    auto page_of = [&](const int32_t* tab, int b, int lo, int hi) {
+    auto seen = [&](int b, int lo, int hi) {
       const int key = b * 128 + lane * boxt;
-      if (lane >= nbox || key >= hi || key + boxt <= lo) return -1;
-      const int p = tab[key >> P.page_shift];
+      return lane < nbox && key < hi && key + boxt > lo;
+    };
+    auto entry_of = [&](const int32_t* tab, int b) { return tab[(b * 128 + lane * boxt) >> P.page_shift]; };
+    auto page_in = [&](int p) {
       if (p >= 0 && p < P.n_pages) return p;
       latch(P.status, MK_ERR_BOUNDS);
       return -1;
     };
+    auto page_of = [&](const int32_t* tab, int b, int lo, int hi) { return seen(b, lo, hi) ? page_in(entry_of(tab, b)) : -1; };
     // a block's keys or values into a stage
     auto load = [&](const CUtensorMap* tm, int stage, uint32_t phase, int b, int head, int page) {
       wait_phase(&empty[stage], phase, dead, P.status);
@@ -402,6 +405,31 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           d.row0 = q.row0 + t * TT; d.rows = ntok * P.rep; d.head = first_head | (pair ? PART_PAIR : 0); d.parts = last - c + 1;
           W.desc[c] = d;
         }
+        auto load_q = [&]() {
+          const int halves = pair || ntok > TS ? 2 : 1;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(qfull, halves * (HD / 64) * TS * P.rep * 128);
+            for (int y = 0; y < halves; ++y)
+              for (int x = 0; x < HD / 64; ++x)
+                tma_rows(smem + y * C::TILE + x * 16384, &tq, 64 * x, (first_head + (pair ? y : 0)) * P.rep,
+                         q.row0 + t * TT + (pair ? 0 : y * TS), qfull);
+          }
+          __syncwarp();
+        };
+        const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
+        int page = -1;
+        bool has_page = false;
+        if (TURNS) {
+          // The first tile's queries while its pages are read, before all SMs' first
+          // blocks are on their way (32 x 32 tokens over 1280 keys 47.2 -> 46.3 us; runs with
+          // tiles of two halves gain nothing, 1 to 64 tokens 63.2, 63.5).
+          has_page = seen(b0 + blk, q.lo, q.hi);
+          if (has_page) page = entry_of(tab, b0 + blk);
+          if (u == u0) {
+            qphase ^= 1;  // (nothing has to be waited for)
+            load_q();
+          }
+        }
         wait_phase(&mempty[slot], mphase, dead, P.status);
         if (*dead) break;
         if (lane == 0) {
@@ -416,27 +444,19 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           mbar_arrive(&mfull[slot]);
         }
         if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
-        const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
-        int page = page_of(tab, b0 + blk, q.lo, q.hi);
+        if (!TURNS) page = page_of(tab, b0 + blk, q.lo, q.hi);
+        else if (has_page) page = page_in(page);
         for (int i = 0; i < nblk && up; ++i) {
           const int b = b0 + blk + i;
           const int next = i + 1 < nblk ? page_of(tab, b + 1, q.lo, q.hi) : -1;
           for (int h = 0; h <= (pair ? 1 : 0) && up; ++h) {
             up = load(&tk, stage, sphase, b, first_head + h, page);
             stage += step;
-            if (up && i == 0 && h == 0) {
+            if (up && i == 0 && h == 0 && !(TURNS && u == u0)) {
               wait_phase(qempty, qphase, dead, P.status);
               qphase ^= 1;
               if (*dead) { up = false; break; }
-              const int halves = pair || ntok > TS ? 2 : 1;
-              if (lane == 0) {
-                mbar_arrive_expect_tx(qfull, halves * (HD / 64) * TS * P.rep * 128);
-                for (int y = 0; y < halves; ++y)
-                  for (int x = 0; x < HD / 64; ++x)
-                    tma_rows(smem + y * C::TILE + x * 16384, &tq, 64 * x, (first_head + (pair ? y : 0)) * P.rep,
-                             q.row0 + t * TT + (pair ? 0 : y * TS), qfull);
-              }
-              __syncwarp();
+              load_q();
             }
             if (up && !split_v) {
               up = load(&tv, stage, sphase, b, first_head + h, page);
@@ -1209,7 +1229,7 @@ cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, cons
 
 // Few tiles over few keys: a cluster for each, of as many CTAs as the device holds at
 // once for all, joined in their shared memory (a lone request of 32 tokens over 4096
-// keys, 8 kv heads of 128, 13.2 against 17.2 us of runs over all SMs, parts in memory
+// keys, 8 kv heads of 128, 12.9 against 17.2 us of runs over all SMs, parts in memory
 // and the join's launch; 16 of them over 512 keys, a CTA a tile, 14.6 against 24.6).
 // The keys that a tile may have are bounded by the table's width.  Past 8 blocks a
 // CTA the SMs that no cluster fills, and requests that are shorter than the longest,
