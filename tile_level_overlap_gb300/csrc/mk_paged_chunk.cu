@@ -46,8 +46,10 @@ constexpr int PC_REGS = 168, PC_REGS_SOFT = 216, PC_REGS_REST = 72;
 static_assert(2 * PC_REGS_SOFT + PC_REGS_REST == 3 * PC_REGS, "registers of the three warpgroups");
 // What a tile costs beside its blocks (filling the pipeline, writing the rows),
 // in blocks: without it the SMs with the short tiles of a prompt's start ended
-// a quarter later than the others.
-constexpr int PC_OVER = 2;
+// a quarter later than the others.  Of trees 1, their blocks take longer (1.7 us, a tile
+// 2: with 2 blocks a mixed step 40.6 us, with 1 39.4, with none 42.5; 32 requests over
+// 500 to 2000 keys 63.5, 62.9, 65.6).
+constexpr int PC_OVER = 2, PC_OVER_TREE = 1;
 // P is relative to a maximum that may lag by 2^PC_LAG.  In fp16 it is scaled by
 // 2^PC_TOP_FP16 besides (together 2^15): weights lose bits only 2^21 or more below
 // the row's largest, and are lost 2^32 or more below it, instead of 2^14 and 2^25.
@@ -151,6 +153,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   using C = ChunkCfg<HD>;
   constexpr int ST = C::STAGES;
   constexpr bool PAIRS = TREE && FORM == RUNS && HD == 64, TURNS = FORM != RUNS;
+  constexpr int OVER = TREE ? PC_OVER_TREE : PC_OVER;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::o_bar);
   uint64_t* empty = full + ST;
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == from) u = v;
     }
-    u = (u + PC_OVER * ntile) * (is_pair<PAIRS>(P, q, TS) ? P.hkv / 2 : P.hkv);
+    u = (u + OVER * ntile) * (is_pair<PAIRS>(P, q, TS) ? P.hkv / 2 : P.hkv);
     if (r < P.n) pre[r] = u;
     mine += u;
   }
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           int rem = local - head * per_head;
           for (int base = 0;; base += 32) {
             int f, k = 0;
-            if (base + lane < ntile) k = tile_blocks<TREE>(P, q, base + lane, TT, &f) + PC_OVER;
+            if (base + lane < ntile) k = tile_blocks<TREE>(P, q, base + lane, TT, &f) + OVER;
             int x = k;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -393,9 +396,9 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           }
         }
         // units [x0, x1) of the tile: blocks [blk, blk + nblk)
-        const int nb = tile_blocks<TREE>(P, q, t, TT, &b0), x1 = min(nb + PC_OVER, x0 + u1 - u);
-        const int blk = clustered ? cb0 : max(0, x0 - PC_OVER), nblk = clustered ? cb1 - cb0 : max(0, x1 - PC_OVER) - blk;
-        const int ntok = min(TT, q.add - t * TT), end = u - x0 + nb + PC_OVER;
+        const int nb = tile_blocks<TREE>(P, q, t, TT, &b0), x1 = min(nb + OVER, x0 + u1 - u);
+        const int blk = clustered ? cb0 : max(0, x0 - OVER), nblk = clustered ? cb1 - cb0 : max(0, x1 - OVER) - blk;
+        const int ntok = min(TT, q.add - t * TT), end = u - x0 + nb + OVER;
         if (nblk == 0) break;  // the run ends with the tile's overhead: the next CTA has it all
         const int first_head = pair ? 2 * head : head;
         const bool whole = blk == 0 && nblk == nb;
