@@ -29,7 +29,7 @@
 // The kernel's other forms take trees of drafted tokens, whose rows see the cached keys
 // and the new ones that their masks name: the masks change the blocks that hold new
 // tokens, as four words of bits a row.  Bound by HBM where tiles have one half
-// (2 x 16 tokens over 128K keys 169 us, 6.4 TB/s), else by the softmax as above (1.8 us
+// (2 x 16 tokens over 128K keys 166 us, 6.5 TB/s), else by the softmax as above (1.8 us
 // a block, HBM 1.5).  Forms, their rules and figures stand at the kernel, is_pair,
 // paged_chunk_clusters and the join.
 #include "mk_paged_dev.cuh"
@@ -314,6 +314,9 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       return -1;
     };
     auto page_of = [&](const int32_t* tab, int b, int lo, int hi) { return seen(b, lo, hi) ? page_in(entry_of(tab, b)) : -1; };
+    // Keys and values are read once: they leave L2 before the parts do, which the join
+    // reads (32 x 32 tokens over 1280 keys 46.4 -> 44.1 us, 8 x 32 over 8192 59.0 -> 56.4).
+    const uint64_t once = TREE ? policy_evict_first() : 0;
     // a block's keys or values into a stage
     auto load = [&](const CUtensorMap* tm, int stage, uint32_t phase, int b, int head, int page) {
       wait_phase(&empty[stage], phase, dead, P.status);
@@ -324,7 +327,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         uint8_t* dst = smem + C::o_kv + stage * C::TILE + lane * boxt * 128;
         const int tok = (b * 128 + lane * boxt) & ((1 << P.page_shift) - 1);
 #pragma unroll
-        for (int x = 0; x < HD / 64; ++x) tma_page(dst + x * 16384, tm, tok, x, head, page, &full[stage]);
+        for (int x = 0; x < HD / 64; ++x) {
+          if constexpr (TREE) tma_page(dst + x * 16384, tm, tok, x, head, page, &full[stage], once);
+          else tma_page(dst + x * 16384, tm, tok, x, head, page, &full[stage]);
+        }
       }
       return true;
     };
@@ -1045,10 +1051,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
 // tiles end to end.  Latency bound: what counts is that all loads of an item are in
 // flight at once and that the items go round few times.  With few of them (a lone
 // request: 8 tiles of 19 parts) an item is 32 dimensions of which the block's two
-// teams take every other part; with many (two parts each, mostly) a team takes all
-// dimensions of an item of its own.  (a lone request of 32 tokens over 4096 keys
-// 30.7 -> 17.3 us by this and the spared launch).
-constexpr int JT_THREADS = 512, JT_TEAM = JT_THREADS / 2;
+// teams take every other part (a lone request of 32 tokens over 4096 keys 30.7 -> 17.3
+// us by this and the spared launch); with many (two parts each, mostly) each warp takes
+// 8 dimensions of an item for itself and writes 16 bytes a row (32 requests over 500 to
+// 2000 keys 59.6 us; by teams, through shared memory 61.4; 16 dimensions a warp 60.7,
+// 4 63.3).
+constexpr int JT_THREADS = 512;
 
 // A team's warp `quad` joins parts first, first + step, .. of 32 rows (one a lane), Q
 // groups of four dimensions, AHEAD parts in flight.
@@ -1099,12 +1107,12 @@ __device__ __forceinline__ void join_parts(const PagedParts& B, int c, int parts
 
 template <int HD, bool BF>
 __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const __grid_constant__ PagedAttnParams P, const __grid_constant__ PagedParts B) {
-  constexpr int DG = HD / 32, Q = DG;
+  constexpr int DG = HD / 32;
   __shared__ int upto[225], tmp[JT_THREADS / 32];
   __shared__ PartDesc desc[224];
   __shared__ float other[8][4][33];
   __shared__ float2 other_ml[32];
-  __shared__ uint2 rows_out[2][32][HD / 4 + 1];
+  __shared__ uint2 rows_out[32][9];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = warp >> 3, quad = warp & 7;
   grid_launch_dependents();
   grid_wait_prior();
@@ -1128,33 +1136,25 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
     const int tk = P.token_of(row);
     P.lse[(int64_t)(t.row0 + tk) * (P.hkv * P.rep) + t.head * P.rep + row - tk * P.rep] = lse_of(m, l);
   };
-  // a team's rows to memory, `pieces` of 8 bytes each
-  auto put_rows = [&](const PartDesc& t, int row0, int d0, int pieces) {
-    for (int i = tid & (JT_TEAM - 1); i < 32 * pieces; i += JT_TEAM) {
-      const int rw = row0 + i / pieces, q = i % pieces;
-      if (rw >= t.rows) break;
-      const int tk = P.token_of(rw);
-      *reinterpret_cast<uint2*>(P.out + (int64_t)(t.row0 + tk) * P.o_stride + (int64_t)(t.head * P.rep + rw - tk * P.rep) * HD + d0 + q * 4) =
-          rows_out[team][i / pieces][q];
-    }
-  };
   if (total * DG > 2 * (int)gridDim.x) {
-    for (int item = 2 * blockIdx.x + team; item < total; item += 2 * gridDim.x) {
-      const int c = find_le(upto, B.ctas, item);
+    constexpr int WARPS = HD / 8, Q = 2;
+    for (int x = JT_THREADS / 32 * blockIdx.x + warp; x < WARPS * total; x += JT_THREADS / 32 * gridDim.x) {
+      const int item = x / WARPS, d0 = x % WARPS * 8, c = find_le(upto, B.ctas, item);
       PartDesc t = desc[c];
       int row0;
-      const int in_part = item_of(t, item - upto[c], &row0);
+      const int in_part = item_of(t, item - upto[c], &row0), row = row0 + lane;
       float m, l;
       float4 o[Q];
-      join_parts<HD, Q, 2>(B, c, t.parts, in_part + lane, quad * Q, 0, 1, &m, &l, o);
+      join_parts<HD, Q, 2>(B, c, t.parts, in_part + lane, d0 / 4, 0, 1, &m, &l, o);
+      if (d0 == 0) put_lse(t, row, m, l);
+      if (row >= t.rows) continue;
       const float inv = inv_of(l);
-      named_bar(1 + team, JT_TEAM);  // the previous rows have been written
+      const int tk = P.token_of(row);
+      uint4* dst = reinterpret_cast<uint4*>(P.out + (int64_t)(t.row0 + tk) * P.o_stride + (int64_t)(t.head * P.rep + row - tk * P.rep) * HD + d0);
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-        rows_out[team][lane][quad * Q + q] = make_uint2(down2<BF>(o[q].x * inv, o[q].y * inv), down2<BF>(o[q].z * inv, o[q].w * inv));
-      if (quad == 0) put_lse(t, row0 + lane, m, l);
-      named_bar(1 + team, JT_TEAM);
-      put_rows(t, row0, 0, HD / 4);
+      for (int q = 0; q < Q; q += 2)
+        dst[q / 2] = make_uint4(down2<BF>(o[q].x * inv, o[q].y * inv), down2<BF>(o[q].z * inv, o[q].w * inv),
+                                down2<BF>(o[q + 1].x * inv, o[q + 1].y * inv), down2<BF>(o[q + 1].z * inv, o[q + 1].w * inv));
     }
     return;
   }
@@ -1176,12 +1176,16 @@ __global__ void __launch_bounds__(JT_THREADS, 2) paged_join_tiles_kernel(const _
       const float mn = fmaxf(m, y.x), ref = mn == -INFINITY ? 0.f : mn, a = ex2(m - ref), f = ex2(y.x - ref);
       l = l * a + y.y * f;
       const float inv = inv_of(l);
-      rows_out[0][lane][quad] = make_uint2(down2<BF>((o[0].x * a + other[quad][0][lane] * f) * inv, (o[0].y * a + other[quad][1][lane] * f) * inv),
-                                           down2<BF>((o[0].z * a + other[quad][2][lane] * f) * inv, (o[0].w * a + other[quad][3][lane] * f) * inv));
+      rows_out[lane][quad] = make_uint2(down2<BF>((o[0].x * a + other[quad][0][lane] * f) * inv, (o[0].y * a + other[quad][1][lane] * f) * inv),
+                                        down2<BF>((o[0].z * a + other[quad][2][lane] * f) * inv, (o[0].w * a + other[quad][3][lane] * f) * inv));
       if (quad == 0 && d0 == 0) put_lse(t, row0 + lane, mn, l);
     }
     __syncthreads();
-    if (!team) put_rows(t, row0, d0, 8);
+    if (!team) {  // 64 bytes a row
+      const int rw = row0 + tid / 8, q = tid % 8, tk = P.token_of(rw);
+      if (rw < t.rows)
+        *reinterpret_cast<uint2*>(P.out + (int64_t)(t.row0 + tk) * P.o_stride + (int64_t)(t.head * P.rep + rw - tk * P.rep) * HD + d0 + q * 4) = rows_out[tid / 8][q];
+    }
   }
 }
 
@@ -1232,17 +1236,18 @@ cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, cons
 
 // Few tiles over few keys: a cluster for each, of as many CTAs as the device holds at
 // once for all, joined in their shared memory (a lone request of 32 tokens over 4096
-// keys, 8 kv heads of 128, 12.9 against 17.2 us of runs over all SMs, parts in memory
-// and the join's launch; 16 of them over 512 keys, a CTA a tile, 14.6 against 24.6).
+// keys, 8 kv heads of 128, 13.1 against 16.7 us of runs over all SMs, parts in memory
+// and the join's launch; 16 of them over 512 keys, a CTA a tile, 13.3 against 23.1).
 // The keys that a tile may have are bounded by the table's width.  Past 8 blocks a
 // CTA the SMs that no cluster fills, and requests that are shorter than the longest,
-// cost what the join does (16 CTAs of 12 blocks 29.9 against 30.6 us, 9 of 8 25.4, 25.0);
-// with up to 6 CTAs, whose exchange is shorter, and 128-wide heads past 12 (4 requests of
-// 32 tokens over 6000 keys 27.4, 31.2; over 50 to 6000 24.8, 26.2; 8 over 50 to 3000 25.9,
-// 26.2, to 4000 28.2, 26.9).  With tiles of two halves, whose exchange is twice as
-// long, past 3 (16 CTAs of 4 blocks 26.1, 23.7), of up to 6 CTAs past 4 (4 requests of 64
-// tokens over 2000 keys 22.9, 26.8; 5 over 1456 24.3, 26.4, over 2992 34.5, 33.7); a CTA a tile
-// has nothing to exchange (10 requests of 32 tokens over 2000 keys 26.4, 30.5).
+// cost what the join does (2 requests of 32 tokens over 9168 keys, 8 CTAs of 9 blocks, 25.2
+// against 23.9 us; 8 over 50 to 2000 keys, 2 CTAs of 8, 20.6 both, to 3000 25.0, 21.9);
+// with 3 to 6 CTAs, whose exchange is short, past 12 (4 requests over 6000 keys 25.8,
+// 29.7; over 50 to 6000 24.0, 25.1).  Tiles of two halves exchange twice as much: up to
+// 6 CTAs of 4 blocks (4 requests of 64 tokens over 2000 keys 22.8, 24.0; 5 over 1456 24.6,
+// 26.4; 3 over 2992 25.2, 24.8; of 16 CTAs, a lone one over 2000 16.6, 15.9, over 4016
+// 19.0, 19.8).  A CTA a tile has nothing to exchange (10 requests of 32 tokens over 2000
+// keys 24.9, 28.4).
 void paged_chunk_clusters(PagedAttnParams* p, int d, bool bf) {
   const int tt = 2 * (128 / p->rep);
   const int64_t tiles = (int64_t)p->n * p->hkv * (((int64_t)p->max_new + tt - 1) / tt);
@@ -1253,8 +1258,8 @@ void paged_chunk_clusters(PagedAttnParams* p, int d, bool bf) {
     const int most = d == 128 ? (bf ? clusters_at_once<128, true>(p->device, c) : clusters_at_once<128, false>(p->device, c))
                               : (bf ? clusters_at_once<64, true>(p->device, c) : clusters_at_once<64, false>(p->device, c));
     if (tiles > most) continue;
-    const bool halves = (int64_t)p->max_new * p->rep > 128, small = c <= 6;
-    const int64_t most_blocks = c == 1 ? 16 : c * (halves ? small ? 4 : 3 : small && d == 128 ? 12 : 8);
+    const int each = (int64_t)p->max_new * p->rep > 128 ? (c <= 6 ? 4 : 0) : c >= 3 && c <= 6 ? 12 : 8;
+    const int64_t most_blocks = c == 1 ? 16 : c * each;
     if (blocks <= most_blocks) {
       p->cluster = c;
       p->cluster_tiles = (int)tiles;

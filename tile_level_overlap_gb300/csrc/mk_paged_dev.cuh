@@ -160,6 +160,16 @@ __device__ __forceinline__ void tma_page(void* dst, const void* tmap, int token,
       : "memory");
 }
 
+// The same, with an L2 policy.
+__device__ __forceinline__ void tma_page(void* dst, const void* tmap, int token, int part, int head,
+                                         int page, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(0), "r"(token), "r"(part), "r"(head), "r"(page), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- the requests
 // What a request asks of attention, from the device arrays; `bad` where the
 // status is to be latched.  Keys [lo, hi) are what any of its rows may see;
