@@ -547,7 +547,7 @@ int mk_paged_attention(const mk_paged_cache *cache, const mk_paged_batch *batch,
  * mk_paged_tables (the tree's tokens take the slots ctx, ctx + 1, .. in the order
  * of the rows), mk_paged_tree (masks, positions), per layer mk_paged_append and
  * mk_paged_tree_attention, then mk_tree_verify (which tokens stand, and the one
- * that follows), mk_paged_keep (their keys and values move together, all layers in
+ * that follows; mk_tree_verify_mixed beside chunks of prompts), mk_paged_keep (their keys and values move together, all layers in
  * one launch) and mk_paged_fork in its trimming form (pages behind them go back to
  * the free list). */
 
@@ -630,6 +630,22 @@ int mk_tree_verify(const mk_paged_batch *batch, const int32_t *parents, const in
                    int64_t draft_stride, int vocab, const float *uniforms, const float *last_uniforms,
                    int32_t *path, int32_t *emitted, int32_t *kept, int32_t *lens, int32_t *status,
                    void *stream);
+
+/* mk_tree_verify for a step that may have chunks of prompts beside its trees, told
+ * apart as by mk_paged_tree and mk_paged_tree_attention: requests of more than 32
+ * mask_words new tokens, of any number (mk_tree_verify takes every request for a
+ * tree).  All of a chunk stands, so that mk_paged_keep moves none of it and
+ * mk_paged_fork cuts nothing: path 0, 1, .. to its end, kept its new tokens, lens =
+ * kv_lens; emitted has the token drawn from the target row of its last token there
+ * (row kept - 1, where every request's last token is) and -1 before.  Where that row
+ * has no mass (nobody asks what follows a prompt's middle) that is -1 too, and
+ * nothing is latched.  A chunk's parents, tokens, uniforms and other rows are not
+ * read; its row of last_uniforms is.  1 <= mask_words <= MK_TREE_MAX_NODES / 32. */
+int mk_tree_verify_mixed(const mk_paged_batch *batch, int mask_words, const int32_t *parents,
+                         const int32_t *tokens, const float *target_probs, int64_t target_stride,
+                         const float *draft_probs, int64_t draft_stride, int vocab,
+                         const float *uniforms, const float *last_uniforms, int32_t *path,
+                         int32_t *emitted, int32_t *kept, int32_t *lens, int32_t *status, void *stream);
 
 /* ------------------------------------------------------------------------
  * Sharing and giving back pages.  shared[p] is how many holders page p has beside

@@ -99,6 +99,7 @@ struct VerifyParams {
   int32_t *path, *emitted, *kept, *lens, *status;
   int64_t p_stride, q_stride;
   int n, rows, vocab;
+  int words;  // requests of more than 32 words new tokens are chunks of prompts; 0: none is
 };
 
 __device__ __forceinline__ float probability(float x) { return __saturatef(x); }  // NaN: 0
@@ -280,12 +281,14 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const Verify
   int k = 0, c0 = 0, kv = 0, cur = 0, depth = 0, at = 0, n_gone = 0;
   double sum_z = 0.0, z = 1.0;
   bool none = false;  // nothing to draw from: this request gets no token
+  bool chunk = false;  // of a prompt: all of it stands, its last row says what follows
   if (rank == 0) {
     c0 = P.cu[r];
     const int c1 = P.cu[r + 1];
     kv = P.kv[r];
     k = c1 - c0;
-    const bool below = begins_below(P.cu, r, c0), bad = below || c0 < 0 || c1 < c0 || c1 > P.rows || k > MK_TREE_MAX_NODES;
+    chunk = P.words > 0 && k > 32 * P.words;
+    const bool below = begins_below(P.cu, r, c0), bad = below || c0 < 0 || c1 < c0 || c1 > P.rows || (k > MK_TREE_MAX_NODES && !chunk);
     none = bad || k == 0 || kv < k;
     if (none) {
       if (!bad)
@@ -296,8 +299,9 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const Verify
         P.lens[r] = kv;
       }
       k = 0;
+      chunk = false;
     }
-    for (int i = tid; i < ((k + 31) & ~31); i += TV_THREADS) {
+    for (int i = tid; i < (chunk ? 0 : (k + 31) & ~31); i += TV_THREADS) {
       int up = -1, x = -1;
       float p = 0.f, q = 0.f, u = 0.f;
       if (i > 0 && i < k) {
@@ -319,7 +323,12 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const Verify
       if (lane == 0) S.first[i / 32] = m;
     }
     __syncthreads();
-    if (warp == 0 && k > 0) at = next_child(S.up, k, 0, 1, lane);
+    if (chunk) {
+      cur = depth = k - 1;
+      at = k;
+    } else if (warp == 0 && k > 0) {
+      at = next_child(S.up, k, 0, 1, lane);
+    }
   }
 
   const int vecs = (P.vocab + 3) / 4, per_cta = (vecs + ctas - 1) / ctas, per_warp = (per_cta + TV_WARPS - 1) / TV_WARPS;
@@ -414,8 +423,8 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const Verify
       if (pass == 0 && c.last && rank == 0) {  // meanwhile, what the walk has found
         for (int j = tid; j < k; j += TV_THREADS) {
           const int d = c.emitted - c0;
-          P.path[c0 + j] = j == 0 ? 0 : j <= d ? S.path[j] : -1;
-          if (j != d) P.emitted[c0 + j] = j < d ? S.tok[S.path[j + 1]] : -1;
+          P.path[c0 + j] = j == 0 ? 0 : chunk ? j : j <= d ? S.path[j] : -1;
+          if (j != d) P.emitted[c0 + j] = j < d && !chunk ? S.tok[S.path[j + 1]] : -1;
         }
         if (tid == 0) {
           P.kept[r] = c.emitted - c0 + 1;
@@ -442,8 +451,8 @@ __global__ void __launch_bounds__(TV_THREADS, 2) tree_verify_kernel(const Verify
     int32_t* last = P.emitted + c.emitted;
     if (total == 0) {
       if (rank == 0 && tid == 0) {
-        latch(P.status, MK_ERR_BOUNDS);
-        *last = 0;
+        if (!chunk) latch(P.status, MK_ERR_BOUNDS);
+        *last = chunk ? -1 : 0;
       }
     } else if (owner == rank) {
       const int w = find_sum(lane < TV_WARPS ? S.warp_sum[lane] : 0, TV_WARPS, lane, &want);
@@ -534,11 +543,10 @@ extern "C" int mk_paged_tree(const mk_paged_batch* b, const int32_t* parents, ui
   return paged_done(paged_launch(paged_tree_kernel, p.n + behind, TT_THREADS, 0, (cudaStream_t)stream, p));
 }
 
-extern "C" int mk_tree_verify(const mk_paged_batch* b, const int32_t* parents, const int32_t* tokens,
-                              const float* target_probs, int64_t target_stride, const float* draft_probs,
-                              int64_t draft_stride, int vocab, const float* uniforms, const float* last_uniforms,
-                              int32_t* path, int32_t* emitted, int32_t* kept, int32_t* lens, int32_t* status,
-                              void* stream) {
+static int verify(const mk_paged_batch* b, int mask_words, const int32_t* parents, const int32_t* tokens,
+                  const float* target_probs, int64_t target_stride, const float* draft_probs, int64_t draft_stride,
+                  int vocab, const float* uniforms, const float* last_uniforms, int32_t* path, int32_t* emitted,
+                  int32_t* kept, int32_t* lens, int32_t* status, void* stream) {
   const int rc = paged_check_batch(b);
   if (rc != MK_OK) return rc;
   if (!parents || !tokens || !target_probs || !uniforms || !last_uniforms || !path || !emitted || !kept || !lens || vocab < 1 ||
@@ -560,6 +568,26 @@ extern "C" int mk_tree_verify(const mk_paged_batch* b, const int32_t* parents, c
   p.p = target_probs; p.q = draft_probs; p.u = uniforms; p.u_last = last_uniforms;
   p.path = path; p.emitted = emitted; p.kept = kept; p.lens = lens; p.status = status;
   p.p_stride = target_stride; p.q_stride = draft_stride;
-  p.n = b->n; p.rows = b->max_tokens; p.vocab = vocab;
+  p.n = b->n; p.rows = b->max_tokens; p.vocab = vocab; p.words = mask_words;
   return paged_done(verify_launch(p, (cudaStream_t)stream));
+}
+
+extern "C" int mk_tree_verify(const mk_paged_batch* b, const int32_t* parents, const int32_t* tokens,
+                              const float* target_probs, int64_t target_stride, const float* draft_probs,
+                              int64_t draft_stride, int vocab, const float* uniforms, const float* last_uniforms,
+                              int32_t* path, int32_t* emitted, int32_t* kept, int32_t* lens, int32_t* status,
+                              void* stream) {
+  return verify(b, 0, parents, tokens, target_probs, target_stride, draft_probs, draft_stride, vocab, uniforms,
+                last_uniforms, path, emitted, kept, lens, status, stream);
+}
+
+extern "C" int mk_tree_verify_mixed(const mk_paged_batch* b, int mask_words, const int32_t* parents, const int32_t* tokens,
+                                    const float* target_probs, int64_t target_stride, const float* draft_probs,
+                                    int64_t draft_stride, int vocab, const float* uniforms, const float* last_uniforms,
+                                    int32_t* path, int32_t* emitted, int32_t* kept, int32_t* lens, int32_t* status,
+                                    void* stream) {
+  if (mask_words < 1) return MK_ERR_INVALID_ARG;
+  if (mask_words > MK_TREE_MAX_NODES / 32) return MK_ERR_UNSUPPORTED;
+  return verify(b, mask_words, parents, tokens, target_probs, target_stride, draft_probs, draft_stride, vocab, uniforms,
+                last_uniforms, path, emitted, kept, lens, status, stream);
 }

@@ -41,7 +41,7 @@ EXPORTED = [
     "mk_plan_set_lm_mode", "mk_decode_steps", "mk_prefill_logits", "mk_prefill_batch",
     "mk_decode_step_slots", "mk_plan_create_for_sms", "mk_prefill_chunks",
     "mk_paged_tables", "mk_rope_init", "mk_paged_append", "mk_paged_attention",
-    "mk_paged_tree", "mk_paged_tree_attention", "mk_tree_verify", "mk_paged_fork", "mk_paged_copy",
+    "mk_paged_tree", "mk_paged_tree_attention", "mk_tree_verify", "mk_tree_verify_mixed", "mk_paged_fork", "mk_paged_copy",
     "mk_paged_keep",
 ]
 
@@ -145,6 +145,7 @@ def lib() -> ctypes.CDLL:
     L.mk_paged_tree.argtypes = [vp, vp, vp, i32, vp, vp, vp]
     L.mk_paged_tree_attention.argtypes = [vp, vp, vp, i32, vp, i64, vp, i64, vp, f32, i32, vp]
     L.mk_tree_verify.argtypes = [vp, vp, vp, vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.mk_tree_verify_mixed.argtypes = [vp, i32, *L.mk_tree_verify.argtypes[1:]]
     L.mk_paged_fork.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, vp, vp]
     L.mk_paged_copy.argtypes = [vp, vp, vp, i32, vp, i32, vp]
     L.mk_paged_keep.argtypes = [vp, vp, vp, i32, vp, vp, vp]
@@ -783,7 +784,9 @@ class DraftTree(_OnDevice):
     of word j / 32: the row sees the request's new token j), positions int32 [rows]
     (the batch's own if not given).  build() makes masks and positions from the
     parents; masks alone suffice for PagedCache.attention(tree=...), parents alone for
-    verify().  Holds references to them and to the batch."""
+    verify() of a step of trees.  With masks, requests of more than 32 words new tokens
+    are chunks of prompts; without, every request is a tree.  Holds references to them
+    and to the batch."""
 
     def __init__(self, batch: PagedBatch, parents=None, masks=None, positions=None):
         _need(parents is not None or masks is not None, "a tree of parents, masks or both is wanted")
@@ -801,7 +804,8 @@ class DraftTree(_OnDevice):
         self.c = mk_paged_batch.from_buffer_copy(batch.c)
         self.c.max_tokens = rows
         self._p = ctypes.addressof(self.c)
-        self._build, self._verify = lib().mk_paged_tree, lib().mk_tree_verify
+        self._build = lib().mk_paged_tree
+        self._verify = lib().mk_tree_verify if masks is None else lib().mk_tree_verify_mixed
 
     def build(self, status=None, stream=None) -> None:
         """mk_paged_tree: masks and positions from the parents, behind the batch's own
@@ -818,10 +822,11 @@ class DraftTree(_OnDevice):
 
     def verify(self, tokens, target_probs, uniforms, last_uniforms, path, emitted, kept, lens, draft_probs=None,
                status=None, stream=None) -> None:
-        """mk_tree_verify: tokens int32 [rows], target_probs and draft_probs float32
-        [rows, vocab] (rows contiguous; draft_probs None: tokens that were found, not
-        drawn), uniforms float32 [rows], last_uniforms [n]; writes path, emitted int32
-        [rows], kept, lens [n]."""
+        """mk_tree_verify, of a tree with masks mk_tree_verify_mixed (chunks of prompts
+        stand whole): tokens int32 [rows], target_probs and draft_probs float32 [rows,
+        vocab] (rows contiguous; draft_probs None: tokens that were found, not drawn),
+        uniforms float32 [rows], last_uniforms [n]; writes path, emitted int32 [rows],
+        kept, lens [n].  A request's last token is emitted[cu_new + kept - 1]."""
         i32, f32, rows, n, dev = self._i32, self._f32, self.rows, self.batch.n, self._dev
         _need(self.parents is not None, "verify needs parents")
         vocab = target_probs.shape[-1]
@@ -841,7 +846,8 @@ class DraftTree(_OnDevice):
                 lens.copy_(self.batch.kv_lens)
             return
         one = rows == 1  # the stride of a lone row joins nothing
-        self._call(self._verify, "mk_tree_verify", self._p, self._parents, tokens.data_ptr(), target_probs.data_ptr(),
+        first = (self._p,) if self.masks is None else (self._p, self._words)
+        self._call(self._verify, "mk_tree_verify", *first, self._parents, tokens.data_ptr(), target_probs.data_ptr(),
                    vocab if one else target_probs.stride(0), None if draft_probs is None else draft_probs.data_ptr(),
                    0 if draft_probs is None else vocab if one else draft_probs.stride(0), vocab, uniforms.data_ptr(),
                    last_uniforms.data_ptr(), path.data_ptr(), emitted.data_ptr(), kept.data_ptr(), lens.data_ptr(),
