@@ -165,3 +165,19 @@ def test_without_masks_every_request_is_a_tree():
     new = [40, 1]
     parents, tokens, p, _, u, ul = make(new, 2, 30, False, 8)
     trees.run_verify([parents[:40], parents[40:]], tokens, p, None, u, ul)
+
+
+def test_steps_without_rows():
+    """Buffers of no rows, every request rests."""
+    b = mk.PagedBatch(ints(np.full((2, 3), -1)), ints([0] * 3), ints([0] * 2), ints([]), ints([]), page_size=16, max_new=4)
+    status = ints([0])
+    b.build(ints([5, 20]), ints([0, 0]), ints([0] * 4), ints([4]), ints([0]), status=status)
+    tree = mk.DraftTree(b, ints([]), ints(np.zeros((0, 1))))
+    tree.build(status=status)
+    kept, lens = ints([9, 9]), ints([9, 9])
+    tree.verify(ints([]), torch.zeros(0, 7, device=DEV), torch.zeros(0, device=DEV), torch.zeros(2, device=DEV), ints([]), ints([]), kept, lens, status=status)
+    assert kept.tolist() == [0, 0] and lens.tolist() == [5, 20] and status.item() == 0
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV)
+    cache = mk.PagedCache(*(torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)), n_q_heads=4)
+    cache.attention(q, b, q.clone(), tree=tree)
+    mk.PagedLayers([cache]).keep(b, ints([]))

@@ -816,6 +816,8 @@ class DraftTree(_OnDevice):
               "build needs parents, masks and positions")
         if not self._are(self._i32, (pos, self.rows), (status, 1)):
             _tensors(self.device, positions=(pos, self._i32, (self.rows,)), status=(status, self._i32, (1,)))
+        if self.rows == 0:  # empty tensors have no address
+            return
         self._call(self._build, "mk_paged_tree", self._p, self._parents, self._masks, self._words, pos.data_ptr(),
                    None if status is None else status.data_ptr(),
                    self._raw_stream(self._dev) if stream is None else int(stream.cuda_stream))
