@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   if (tid == 0 && !clustered) W.desc[blockIdx.x].parts = 0;
 
   // In clusters: this one's tile, of which the CTA takes blocks [cb0, cb1).
-  Request cq{};
+  Request cq;
   int cr = 0, ch = 0, ct = 0, cnb = 0, cb0 = 0, cb1 = 0, rank = 0;
   if constexpr (clustered) {
     const int tiles = (P.max_new + TT - 1) / TT, id = blockIdx.x / P.cluster;
@@ -313,7 +313,14 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       latch(P.status, MK_ERR_BOUNDS);
       return -1;
     };
-    auto page_of = [&](const int32_t* tab, int b, int lo, int hi) { return seen(b, lo, hi) ? page_in(entry_of(tab, b)) : -1; };
+    auto page_of = [&](const int32_t* tab, int b, int lo, int hi) {
+      const int key = b * 128 + lane * boxt;
+      if (lane >= nbox || key >= hi || key + boxt <= lo) return -1;
+      const int p = tab[key >> P.page_shift];
+      if (p >= 0 && p < P.n_pages) return p;
+      latch(P.status, MK_ERR_BOUNDS);
+      return -1;
+    };
     // Keys and values are read once: they leave L2 before the parts do, which the join
     // reads (32 x 32 tokens over 1280 keys 46.4 -> 44.1 us, 8 x 32 over 8192 59.0 -> 56.4).
     const uint64_t once = TREE ? policy_evict_first() : 0;
@@ -367,14 +374,16 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       int stage = 0, slot = 0;
       uint32_t sphase = 1, mphase = 1, qphase = 1;
       const int step = split_v ? 2 : 1;
-      int r = u0 < u1 && !clustered ? find_le(pre, P.n, u0) : cr, t = clustered ? ct : -1, head = ch;
+      int r = clustered ? cr : u0 < u1 ? find_le(pre, P.n, u0) : 0, t = clustered ? ct : -1, head = clustered ? ch : 0;
       bool up = true;
       for (int u = u0; u < u1 && up;) {
         while (!clustered && pre[r + 1] <= u) {
           ++r;
           t = -1;
         }
-        const Request q = clustered ? cq : kept.again(P, r);
+        Request q;
+        if constexpr (clustered) q = cq;
+        else q = kept.again(P, r);
         const bool pair = is_pair<PAIRS>(P, q, TS);
         const int per_head = clustered ? 1 : (pre[r + 1] - pre[r]) / (pair ? P.hkv / 2 : P.hkv), ntile = (q.add + TT - 1) / TT;
         int x0 = 0, b0;  // first unit of the tile in this run
@@ -414,21 +423,18 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           d.row0 = q.row0 + t * TT; d.rows = ntok * P.rep; d.head = first_head | (pair ? PART_PAIR : 0); d.parts = last - c + 1;
           W.desc[c] = d;
         }
-        auto load_q = [&]() {
-          const int halves = pair || ntok > TS ? 2 : 1;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(qfull, halves * (HD / 64) * TS * P.rep * 128);
-            for (int y = 0; y < halves; ++y)
-              for (int x = 0; x < HD / 64; ++x)
-                tma_rows(smem + y * C::TILE + x * 16384, &tq, 64 * x, (first_head + (pair ? y : 0)) * P.rep,
-                         q.row0 + t * TT + (pair ? 0 : y * TS), qfull);
-          }
-          __syncwarp();
-        };
-        const int32_t* tab = P.table + (int64_t)r * P.max_blocks;
-        int page = -1;
-        bool has_page = false;
-        if (TURNS) {
+        // (The queries' loads are written out at both places, and what only trees need is
+        // left out at compile time: the compiler's order of the causal form's code depends
+        // on it.  8192-token prompt 361 us so and before there were trees, 364 with a
+        // lambda, with a function 2 more than that.)
+        const int halves = pair || ntok > TS ? 2 : 1;
+        const int q_head = first_head * P.rep, q_tok = q.row0 + t * TT, next_head = pair ? P.rep : 0, next_tok = pair ? 0 : TS;
+        const int32_t* tab;
+        int page;
+        bool has_page;
+        if constexpr (TURNS) {
+          tab = P.table + (int64_t)r * P.max_blocks;
+          page = -1;
           // The first tile's queries while its pages are read, before all SMs' first
           // blocks are on their way (32 x 32 tokens over 1280 keys 47.2 -> 46.3 us; runs with
           // tiles of two halves gain nothing, 1 to 64 tokens 63.2, 63.5).
@@ -436,7 +442,13 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           if (has_page) page = entry_of(tab, b0 + blk);
           if (u == u0) {
             qphase ^= 1;  // (nothing has to be waited for)
-            load_q();
+            if (lane == 0) {
+              mbar_arrive_expect_tx(qfull, halves * (HD / 64) * TS * P.rep * 128);
+              for (int y = 0; y < halves; ++y)
+                for (int x = 0; x < HD / 64; ++x)
+                  tma_rows(smem + y * C::TILE + x * 16384, &tq, 64 * x, q_head + y * next_head, q_tok + y * next_tok, qfull);
+            }
+            __syncwarp();
           }
         }
         wait_phase(&mempty[slot], mphase, dead, P.status);
@@ -444,35 +456,47 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (lane == 0) {
           Tile m;
           m.key0 = (b0 + blk) * 128; m.nblk = nblk; m.row0 = q.row0 + t * TT; m.ntok = ntok; m.head = first_head;
-          m.pair = pair;
+          if constexpr (TREE) m.pair = pair;
           m.pos0 = q.pos0 + t * TT; m.lo = q.lo; m.hi = q.hi;
-          m.part = clustered && P.cluster > 1 ? -2 : clustered || whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
+          if constexpr (clustered) m.part = P.cluster > 1 ? -2 : -1;
+          else m.part = whole ? -1 : 2 * c + (blk == 0 ? 1 : 0);
           m.req = r;
-          m.ctx = is_tree<TREE>(P, q) ? q.pos0 : -0x7fffffff - 1;
+          if constexpr (TREE) m.ctx = is_tree<TREE>(P, q) ? q.pos0 : -0x7fffffff - 1;
           meta[slot] = m;
           mbar_arrive(&mfull[slot]);
         }
         if (++slot == C::SLOTS) { slot = 0; mphase ^= 1; }
-        if (!TURNS) page = page_of(tab, b0 + blk, q.lo, q.hi);
-        else if (has_page) page = page_in(page);
+        if constexpr (TURNS) {
+          if (has_page) page = page_in(page);
+        } else {
+          tab = P.table + (int64_t)r * P.max_blocks;
+          page = page_of(tab, b0 + blk, q.lo, q.hi);
+        }
         for (int i = 0; i < nblk && up; ++i) {
           const int b = b0 + blk + i;
           const int next = i + 1 < nblk ? page_of(tab, b + 1, q.lo, q.hi) : -1;
-          for (int h = 0; h <= (pair ? 1 : 0) && up; ++h) {
+          int h = 0;
+          do {
             up = load(&tk, stage, sphase, b, first_head + h, page);
             stage += step;
             if (up && i == 0 && h == 0 && !(TURNS && u == u0)) {
               wait_phase(qempty, qphase, dead, P.status);
               qphase ^= 1;
               if (*dead) { up = false; break; }
-              load_q();
+              if (lane == 0) {
+                mbar_arrive_expect_tx(qfull, halves * (HD / 64) * TS * P.rep * 128);
+                for (int y = 0; y < halves; ++y)
+                  for (int x = 0; x < HD / 64; ++x)
+                    tma_rows(smem + y * C::TILE + x * 16384, &tq, 64 * x, q_head + y * next_head, q_tok + y * next_tok, qfull);
+              }
+              __syncwarp();
             }
             if (up && !split_v) {
               up = load(&tv, stage, sphase, b, first_head + h, page);
               ++stage;
             }
             if (stage >= ST) { stage = 0; sphase ^= 1; }
-          }
+          } while (PAIRS && pair && up && ++h < 2);
           page = next;
         }
         u += x1 - x0;
@@ -674,7 +698,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       if (*dead) let_land();
       __syncwarp();
     }
-    if (clustered && P.cluster > 1) {
+    if constexpr (clustered) if (P.cluster > 1) {
       cluster_sync();
       cluster_sync();
     }
@@ -684,7 +708,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_t0 = T_S + 128u * half + lanes;
-    uint32_t s_t = s_t0;
     const uint32_t o_t = T_O + 128u * half + lanes;
     const int tok_in = P.token_of(row), hq_in = row - tok_in * P.rep;
     const float cs = fabsf(P.scale) * 1.4426950408889634f;
@@ -746,7 +769,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         }
       }
       float mx = -INFINITY, l = 0.f;
-      const uint32_t blk_step = pair ? 2 : 1, tile_end = blkn + (pair ? 2 * m.nblk : m.nblk);
+      const uint32_t blk_step = pair ? 2 : 1;
       if (pair) blkn += half;
       // in turns: a buffer and barriers of every other block
       const uint32_t two = TURNS && m.ntok <= TS ? 1 : 0;
@@ -771,6 +794,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             for (int i = 0; i < 4; ++i) named[i] = __funnelshift_r(w[i], w[i + 1], d & 31);
           }
         }
+        uint32_t s_t = s_t0;
         if constexpr (TURNS) {
           s_t = s_t0 + ((j & two) << 7);
           wait_phase(&s_bar[count & two], (count >> two) & 1, dead, P.status);
@@ -898,17 +922,19 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       }
       if (TURNS && two) turn = count;
       else if (TURNS) sn = count;
-      blkn = tile_end;
+      if (pair) blkn -= half;  // the tile's end
       wait_phase(&ofull[half], on & 1, dead, P.status);
       ++on;
       tc_fence_after();
       const bool live = tok_in < ntok;
       const int prow = (pair ? 128 * half : tok0 * P.rep) + row, head = m.head + (pair ? half : 0);
-      if (clustered && m.part == -2) {  // (the one tile)
-        if (live) held = prow;
-        held_m = mx * cs - top;
-        held_l = l;
-        continue;
+      if constexpr (clustered) {
+        if (m.part == -2) {  // (the one tile)
+          if (live) held = prow;
+          held_m = mx * cs - top;
+          held_l = l;
+          continue;
+        }
       }
       if (m.part < 0) {
         // Four lanes exchange 16-byte pieces so that a store writes 64
@@ -959,7 +985,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       }
       tc_fence_before();  // the next tile's first P V is issued behind this group's next P
     }
-    if (clustered && P.cluster > 1) {
+    if constexpr (clustered) if (P.cluster > 1) {
       // A cluster's CTAs have the tile's rows, each over its share of the keys: CTA k
       // joins rows [k per, (k + 1) per), which all of them write to its shared memory
       // ([CTA][4 columns][row]), where the keys and values were and before them (rows
