@@ -623,8 +623,9 @@ int mk_paged_tree_attention(const mk_paged_cache *cache, const mk_paged_batch *b
  * a parent that is not before its child has no such child; both are latched.  A
  * target row without mass where the last token is drawn: the token 0, latched.
  * Sums are of whole numbers (each value rounded to 2^-43), so that equal calls, and
- * equal requests in any batch, give equal tokens.  vocab 1 .. 2^24.  What is written may overlap
- * nothing else of the call; *status may be the cache's. */
+ * equal requests in any batch, give equal tokens.  vocab 1 .. 2^24, strides below 2^38,
+ * max_tokens * stride <= 2^60.  What is written may overlap nothing else of the call;
+ * *status may be the cache's. */
 int mk_tree_verify(const mk_paged_batch *batch, const int32_t *parents, const int32_t *tokens,
                    const float *target_probs, int64_t target_stride, const float *draft_probs,
                    int64_t draft_stride, int vocab, const float *uniforms, const float *last_uniforms,

@@ -1,5 +1,7 @@
 // Trees of drafted tokens: masks and positions of their rows, and which of them
 // stand against the target's probabilities (include/mk.h).
+#include <algorithm>
+
 #include "mk_paged_dev.cuh"
 
 namespace mk {
@@ -553,6 +555,9 @@ static int verify(const mk_paged_batch* b, int mask_words, const int32_t* parent
       target_stride < vocab || (draft_probs && draft_stride < vocab))
     return MK_ERR_INVALID_ARG;
   if (vocab > 1 << 24 || target_stride >= (1ll << 38) || (draft_probs && draft_stride >= (1ll << 38))) return MK_ERR_UNSUPPORTED;
+  // the rows' extent in bytes is counted in 64 bits
+  const int64_t most = (1ll << 60) / std::max(b->max_tokens, 1);
+  if (target_stride > most || (draft_probs && draft_stride > most)) return MK_ERR_UNSUPPORTED;
   const void* ptrs[] = {parents, tokens, target_probs, draft_probs, uniforms, last_uniforms, path, emitted, kept, lens, status};
   for (const void* p : ptrs)
     if (!al4(p)) return MK_ERR_INVALID_ARG;
