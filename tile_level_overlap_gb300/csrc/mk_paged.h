@@ -159,7 +159,7 @@ inline int paged_clusters_at_once(const void* kernel, int threads, int smem, int
         (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      n = 0;
+      return 0;  // no answer: the next call asks again
     }
     ++n;
     if (mine) mine->store(n, std::memory_order_relaxed);
