@@ -619,7 +619,9 @@ int mk_paged_tree_attention(const mk_paged_cache *cache, const mk_paged_batch *b
  * MK_TREE_MAX_NODES (or whose rows are out of order or past max_tokens) likewise,
  * its path and emitted left alone and MK_ERR_BOUNDS latched in *status.  Where
  * kv_lens is less than the new tokens (refused by mk_paged_tables) kept is 0 and
- * lens kv_lens, path and emitted -1.  A token outside the vocabulary never stands,
+ * lens kv_lens, path and emitted -1: such a request's cached tokens and pages are still
+ * those of its ctx_lens, which mk_paged_fork has to be given as its lens and keep (0
+ * would leave its pages with nobody).  A token outside the vocabulary never stands,
  * a parent that is not before its child has no such child; both are latched.  A
  * target row without mass where the last token is drawn: the token 0, latched.
  * Sums are of whole numbers (each value rounded to 2^-43), so that equal calls, and

@@ -181,3 +181,39 @@ def test_steps_without_rows():
     cache = mk.PagedCache(*(torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)), n_q_heads=4)
     cache.attention(q, b, q.clone(), tree=tree)
     mk.PagedLayers([cache]).keep(b, ints([]))
+
+
+def test_requests_that_find_no_free_page_keep_their_context():
+    """The tables refuse a request when the pages run out (kv_lens 0): with its own
+    lengths in their place trim leaves it as it was, and no page leaks."""
+    hq, hkv, d, page, vocab, typ = 4, 2, 64, 16, 20, torch.bfloat16
+    ctx, new, words = [30, 15, 47, 16], [8, 20, 33, 0], 1  # one page more, two, a chunk that needs two, none
+    n, total, pages = 4, sum(new), 10
+    held = [-(-c // page) for c in ctx]  # 2, 1, 3, 1: three are free
+    table, at = np.full((n, 6), -1), pages
+    for r in range(n):
+        for b in range(held[r]):
+            at -= 1
+            table[r, b] = at
+    table, free, count, left, shared = ints(table), ints(list(range(at)) + [-1] * (pages - at)), ints([at]), ints([0]), ints([0] * pages)
+    before, status = table.clone(), ints([0])
+    b = mk.PagedBatch(table, ints([0] * 5), ints([0] * 4), ints([0] * total), ints([0] * total), page_size=page, max_new=max(new))
+    tree = mk.DraftTree(b, ints(sum(([i - 1 for i in range(k)] for k in new), [])), ints(np.zeros((total, words))))
+    cache = mk.PagedCache(*(torch.zeros(pages, hkv, page, d, dtype=typ, device=DEV) for _ in range(2)), n_q_heads=hq)
+    ctx_t, p = ints(ctx), torch.full((total, vocab), 1 / vocab, device=DEV)
+    path, emitted, kept, after, lens = ints([9] * total), ints([9] * total), ints([9] * n), ints([9] * n), ints([9] * n)
+    b.build(ctx_t, ints(new), free, count, left, status=status)
+    assert status.item() == mk.MK_ERR_BOUNDS and b.kv_lens.tolist() == [38, 35, 0, 16]
+    tree.build()
+    x = torch.ones(total, hq, d, dtype=typ, device=DEV)
+    cache.append(x, x[:, :hkv].contiguous(), x[:, :hkv].contiguous(), b.slots)
+    cache.attention(x, b, torch.empty_like(x), tree=tree)
+    tree.verify(ints([1] * total), p, torch.zeros(total, device=DEV), torch.zeros(n, device=DEV), path, emitted, kept, after)
+    mk.PagedLayers([cache]).keep(b, path)
+    assert kept.tolist() == [8, 20, 0, 0] and cache.status() == 0
+    mine = [torch.where(kept > 0, t, ctx_t) for t in (b.kv_lens, after)]
+    b.trim(*mine, lens, shared, free, left, count)
+    assert lens.tolist() == [38, 35, 47, 16]
+    assert torch.equal(table[2], before[2])
+    ids = [table[r, :-(-c // page)].tolist() for r, c in enumerate(lens.tolist())]
+    assert sorted(sum(ids, []) + free[:count.item()].tolist()) == list(range(pages)) and not shared.any()

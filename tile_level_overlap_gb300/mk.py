@@ -828,7 +828,8 @@ class DraftTree(_OnDevice):
         stand whole): tokens int32 [rows], target_probs and draft_probs float32 [rows,
         vocab] (rows contiguous; draft_probs None: tokens that were found, not drawn),
         uniforms float32 [rows], last_uniforms [n]; writes path, emitted int32 [rows],
-        kept, lens [n].  A request's last token is emitted[cu_new + kept - 1]."""
+        kept, lens [n].  A request's last token is emitted[cu_new + kept - 1].  One that
+        found no free page (kept 0) still holds its ctx_lens, not lens."""
         i32, f32, rows, n, dev = self._i32, self._f32, self.rows, self.batch.n, self._dev
         _need(self.parents is not None, "verify needs parents")
         vocab = target_probs.shape[-1]
