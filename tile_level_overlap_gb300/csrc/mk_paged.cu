@@ -513,8 +513,9 @@ cudaError_t attention_launch(PagedAttnParams& p, const PagedKv& kv, int d, bool 
   const bool all_few = most <= 16;
   const int want = all_few ? (int)most : p.rep;
   p.few_rows = want <= 8 ? 8 : want <= 16 ? 16 : 0;
-  // Among trees a request of a single token is an exception that the tile kernel
-  // takes too: a launch for it would be paid by every call.
+  // Among trees a request of a single token goes to the tile kernel too: a launch for
+  // it would be paid by every call.  (64 requests over 500 to 2000 keys, 59.0 us as a decode
+  // step: all of one token where trees of 32 may be 66, with 4 such trees 67, with 32 70.)
   if (p.masks && !all_few) {
     p.few_rows = 0;
     paged_chunk_clusters(&p, d, bf);

@@ -321,8 +321,13 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       latch(P.status, MK_ERR_BOUNDS);
       return -1;
     };
-    // Keys and values are read once: they leave L2 before the parts do, which the join
-    // reads (32 x 32 tokens over 1280 keys 46.4 -> 44.1 us, 8 x 32 over 8192 59.0 -> 56.4).
+    // Keys and values that only one tile reads leave L2 before the parts do, which the
+    // join reads (32 x 32 tokens over 1280 keys 46.4 -> 44.1 us, over 8192 180 -> 174.7,
+    // 16 x 32 over 4000 58.5 -> 53.8).  It is no loss beside a chunk of a prompt, whose tiles
+    // read them again (16 x 16 with a chunk of 600 over 2000 keys 64.6 -> 62.3, over 8000 177
+    // -> 173), it is one for trees of several tiles (4 x 160, 8 heads a kv head, 146.4 -> 148)
+    // and where requests share pages in tiles of two halves (32 x 64 over the same 8192
+    // tokens 222.9 -> 229.6; 32 x 32 144.6 -> 141).
     const uint64_t once = TREE ? policy_evict_first() : 0;
     // a block's keys or values into a stage
     auto load = [&](const CUtensorMap* tm, int stage, uint32_t phase, int b, int head, int page) {
@@ -1262,9 +1267,11 @@ cudaError_t paged_chunk_launch(const PagedAttnParams& p, const PagedKv& kv, cons
 
 // Few tiles over few keys: a cluster for each, of as many CTAs as the device holds at
 // once for all, joined in their shared memory (a lone request of 32 tokens over 4096
-// keys, 8 kv heads of 128, 13.1 against 16.7 us of runs over all SMs, parts in memory
-// and the join's launch; 16 of them over 512 keys, a CTA a tile, 13.3 against 23.1).
-// The keys that a tile may have are bounded by the table's width.  Past 8 blocks a
+// keys, 8 kv heads of 128, 12.9 against 16.9 us of runs over all SMs, parts in memory
+// and the join's launch; 16 of them over 512 keys, a CTA a tile, 13.0 against 23.2; 4 over
+// 2000 15.4, 20.3).  The host does not know the lengths: what a tile may have is bounded
+// by the table's width, so that with tables of 32768 tokens these calls take the second
+// figures.  Past 8 blocks a
 // CTA the SMs that no cluster fills, and requests that are shorter than the longest,
 // cost what the join does (2 requests of 32 tokens over 9168 keys, 8 CTAs of 9 blocks, 25.2
 // against 23.9 us; 8 over 50 to 2000 keys, 2 CTAs of 8, 20.6 both, to 3000 25.0, 21.9);

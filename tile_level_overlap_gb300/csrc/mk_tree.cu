@@ -10,8 +10,11 @@ namespace {
 // ---------------------------------------------------------------- masks, positions
 // A CTA per request (and some for the rows behind the last one): its parents go to
 // shared memory, a thread takes a row and a word of its mask and walks up.  Parents
-// precede their children, so a walk ends below its word.  Latency bound (32 trees of
-// 16 tokens 2.0 us, 256 of up to 128 with four words a row 4.4 us).
+// precede their children, so a walk ends below its word.  Latency bound for shallow
+// trees (32 of 16 tokens 2.0 us, 256 of up to 128 with four words a row 4.4 us, one of
+// 512 at random 38).  A path is walked once for each word of its row, a step a read of
+// shared memory: chains take words x nodes^2 steps, 128 with four words 10.3 us, with
+// 16 31.6, 256 with eight 60, 512 with 16 437, 1024 with 32 3.4 ms.
 constexpr int TT_THREADS = 128;
 
 struct TreeParams {
@@ -73,8 +76,8 @@ __global__ void __launch_bounds__(TT_THREADS) paged_tree_kernel(const TreeParams
 // ---------------------------------------------------------------- verification
 // A cluster of CTAs per request.  Its first CTA reads the probabilities of all
 // drafted tokens (two of each, at once), walks the tree and says which row's rest
-// is to be summed; all of them sum their share of the vocabulary.  A chain needs one
-// such pass, to draw its last token; a tree one more for every refused child that has
+// is to be summed; all of them sum their share of the vocabulary.  A chain (and a chunk
+// of a prompt, where nothing is walked) needs one such pass, to draw its last token; a tree one more for every refused child that has
 // siblings behind it.  For q >= 0 the rest after several refusals is
 // max(p - S q, 0) with S the sum of the Z so far (max(max(a, 0) - b, 0) =
 // max(a - b, 0)), so that a pass reads the two rows and keeps nothing.
@@ -87,8 +90,8 @@ __global__ void __launch_bounds__(TT_THREADS) paged_tree_kernel(const TreeParams
 // which none is 64 bits wide.  p - S q has its parts subtracted, with the product's
 // rounding error from a second multiply-add.  (64-bit whole numbers, 40 instructions a
 // pair of values, took 32 trees 68 us instead of 39.)  Bound by latency for few requests
-// (one of five rows of 128256 7.5 us), by HBM (the rows that are drawn from) and these
-// instructions for many: 64 chains without draft probabilities 12.7 us, 32 trees of 17
+// (one of five rows of 128256 7.6 us), by HBM (the rows that are drawn from) and these
+// instructions for many: 64 chains without draft probabilities 12.6 us, 32 trees of 17
 // to 32 tokens of 151936, in up to five passes, 38.3 us.  256 threads with four
 // vectors of each row in flight, two CTAs an SM: 512 with two 51 us, with eight in
 // flight 39.2.
